@@ -384,6 +384,128 @@ int quest_decode_static(const quest_cache_t* cache, const void* q, int32_t top_k
                         quest_stream_t stream);
 
 /*
+ * ---- Narrow caches: K and V in 8 bits ------------------------------------------------
+ *
+ * A paged cache whose complete pages are e4m3 (4 exponent bits, 3 fraction bits, largest
+ * value 448) with one fp32 scale per (page, kv head), and whose open page (the partial
+ * last page of a sequence) is fp16.  The value of a stored key or value is code * scale.
+ *   k_pool, v_pool   : e4m3 [num_phys][num_kv_heads][page_size][128], 16-byte aligned
+ *   k_scale, v_scale : fp32 [num_phys][num_kv_heads]
+ *   k_open, v_open   : fp16 [batch][num_kv_heads][page_size][128]: rows 0 .. seq_len %
+ *                      page_size - 1 are the sequence's open page; the rows behind them are
+ *                      left as they are and never read as tokens
+ *   meta, block_table, seq_lens: as in quest_cache_t.  The boxes are those of the fp16 keys
+ *                      that were written, so page bounds and selection are the fp16 cache's.
+ * quest_narrow_prefill and quest_narrow_append set a page's scale, when the page becomes
+ * complete, to the smallest power of two s with max |x| <= 448 s over the page's finite
+ * values of that head (1 if they are all zero) and store x / s rounded to the nearest e4m3
+ * number, ties to even; infinities become +-448 s, NaN stays NaN.  A token that completes a
+ * page is not written to the open page.  Attention takes any finite scales, so pages may
+ * also come from elsewhere.  The open page's block-table entry must be mapped, as that of
+ * every page a call's new tokens reach.
+ */
+typedef struct quest_narrow_cache {
+    int32_t batch;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t num_phys;
+    void* k_pool;
+    void* v_pool;
+    float* k_scale;
+    float* v_scale;
+    void* k_open;
+    void* v_open;
+    void* meta;
+    const int32_t* block_table;
+    int32_t* seq_lens;
+} quest_narrow_cache_t;
+
+/* Bytes of workspace for every quest_narrow_* call on this cache with this top_k and opts;
+ * 0 if the arguments are invalid.  Conventions as for quest_workspace_size. */
+size_t quest_narrow_workspace_size(const quest_narrow_cache_t* cache, int32_t top_k,
+                                   const quest_opts_t* opts);
+
+/* quest_prefill into a narrow cache: k, v: fp16 [batch][n_tokens][num_kv_heads][128] at
+ * positions seq_lens[b] .. seq_lens[b] + n_tokens - 1.  The same cache, bit for bit, as
+ * n_tokens quest_narrow_append calls.  A sequence with no room, or with a touched page
+ * outside [0, num_phys), is reported; its open page and its length are left unchanged. */
+int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const void* v,
+                         int32_t n_tokens, void* ws, size_t ws_bytes, quest_stream_t stream);
+
+/* quest_append into a narrow cache: k_new, v_new: fp16 [batch][num_kv_heads][128]. */
+int quest_narrow_append(const quest_narrow_cache_t* cache, const void* k_new, const void* v_new,
+                        void* ws, size_t ws_bytes, quest_stream_t stream);
+
+/* quest_sparse_decode over a narrow cache: attention over the pages idx[b][g][0 .. count-1]
+ * (every one in [0, N_b), none twice).  fp32 sums over the exact products of q and the
+ * codes; the softmax weights enter the second product as two fp16 numbers each (22 bits).
+ * opts: pages_per_split. */
+int quest_narrow_sparse_decode(const quest_narrow_cache_t* cache, const void* q,
+                               const int32_t* idx, const int32_t* count, int32_t top_k, void* out,
+                               float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,
+                               quest_stream_t stream);
+
+/* quest_dense_decode over a narrow cache: every token. */
+int quest_narrow_dense_decode(const quest_narrow_cache_t* cache, const void* q, void* out,
+                              float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,
+                              quest_stream_t stream);
+
+/* quest_decode and quest_decode_step on a narrow cache, as a chain of kernels: (append,)
+ * page bounds, top-K, attention over the kept pages.  opts: pages_per_split,
+ * score_tile_pages, sink_pages, local_pages; gqa_union, cluster_size and the one-launch
+ * paths answer QUEST_ERR_UNSUPPORTED.  Arguments and results otherwise as there. */
+int quest_narrow_decode(const quest_narrow_cache_t* cache, const void* q, int32_t top_k,
+                        void* out, float* lse, int32_t* idx_out, int32_t* count_out, void* ws,
+                        size_t ws_bytes, const quest_opts_t* opts, quest_stream_t stream);
+int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, const void* k_new,
+                             const void* v_new, int32_t top_k, void* out, float* lse,
+                             int32_t* idx_out, int32_t* count_out, void* ws, size_t ws_bytes,
+                             const quest_opts_t* opts, quest_stream_t stream);
+
+/*
+ * ---- Sliding window with sink tokens -------------------------------------------------
+ *
+ * Attention in which the query token at position i sees token j if j <= i and (j <
+ * sink_tokens or i - j < window): itself, the window - 1 tokens before it, and the first
+ * sink_tokens tokens of the sequence.  sink_tokens >= 0, window >= 1; a window of
+ * max_pages * page_size or more is plain causal attention.  Pages without a visible token
+ * are never read, and neither are their block-table entries (pages that fell behind the
+ * window may be unmapped).  What hidden tokens hold (infinities, NaN) does not reach a
+ * result.  A row that sees no token gives out = 0, lse = -inf.
+ */
+
+/* Bytes of workspace of quest_window_decode (n_tokens = 1) and of quest_window_prefill with
+ * up to n_tokens query tokens per sequence; 0 if the arguments are invalid. */
+size_t quest_window_workspace_size(const quest_cache_t* cache, int32_t n_tokens,
+                                   const quest_opts_t* opts);
+
+/* The last token of every sequence: q fp16 [batch][num_q_heads][128] at position
+ * seq_lens[b] - 1 (append its key and value first); out, lse as in quest_dense_decode.
+ * opts: pages_per_split. */
+int quest_window_decode(const quest_cache_t* cache, const void* q, int32_t sink_tokens,
+                        int32_t window, void* out, float* lse, void* ws, size_t ws_bytes,
+                        const quest_opts_t* opts, quest_stream_t stream);
+
+/* The same on a narrow cache; ws as for the other quest_narrow_* calls. */
+int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
+                               int32_t sink_tokens, int32_t window, void* out, float* lse,
+                               void* ws, size_t ws_bytes, const quest_opts_t* opts,
+                               quest_stream_t stream);
+
+/* Prompt attention: the last n_tokens tokens of every sequence, which quest_prefill wrote
+ * before.  q: fp16 [batch][n_tokens][num_q_heads][128], token i of sequence b at position
+ * seq_lens[b] - n_tokens + i; out: fp16 of the same shape; lse: fp32
+ * [batch][n_tokens][num_q_heads] or NULL.  In a sequence with fewer than n_tokens tokens
+ * the rows at negative positions see nothing.  n_tokens = 0 does nothing.
+ * opts: pages_per_split. */
+int quest_window_prefill(const quest_cache_t* cache, const void* q, int32_t n_tokens,
+                         int32_t sink_tokens, int32_t window, void* out, float* lse, void* ws,
+                         size_t ws_bytes, const quest_opts_t* opts, quest_stream_t stream);
+
+/*
  * Synchronise `stream`, return the device status recorded in the workspace (QUEST_OK
  * or a QUEST_ERR_* code) and clear it.  detail (nullable, 3 ints) receives the first
  * fault's sequence, logical page and a kernel-specific code.

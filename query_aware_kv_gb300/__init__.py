@@ -13,4 +13,7 @@ from ._lib import (  # noqa: F401
     decode_launches, decode_layers, decode_path, decode_step,
     dense_decode, estimate, estimate_heads, load, opts, prefill, read_status, sparse_decode, topk, workspace,
     workspace_init, workspace_size,
+    NarrowCache, NarrowPlan, QuestNarrowCacheDesc, WindowPlan, narrow_append, narrow_decode,
+    narrow_decode_step, narrow_dense_decode, narrow_prefill, narrow_sparse_decode,
+    narrow_window_decode, narrow_workspace, window_decode, window_prefill, window_workspace,
 )

@@ -42,6 +42,10 @@ EXPORTS = (
     "quest_decode", "quest_decode_layers", "quest_decode_path", "quest_decode_launches",
     "quest_decode_step", "quest_dense_decode", "quest_decode_static", "quest_read_status",
     "quest_last_error", "quest_status_string", "quest_version",
+    "quest_narrow_workspace_size", "quest_narrow_prefill", "quest_narrow_append",
+    "quest_narrow_sparse_decode", "quest_narrow_dense_decode", "quest_narrow_decode",
+    "quest_narrow_decode_step", "quest_narrow_window_decode",
+    "quest_window_workspace_size", "quest_window_decode", "quest_window_prefill",
 )
 
 
@@ -60,6 +64,12 @@ class QuestCacheDesc(ctypes.Structure):
         ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("meta", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
     ]
+
+
+class QuestNarrowCacheDesc(ctypes.Structure):
+    _fields_ = QuestCacheDesc._fields_[:9] + [
+        (n, ctypes.c_void_p) for n in ("k_scale", "v_scale", "k_open", "v_open", "meta",
+                                       "block_table", "seq_lens")]
 
 
 class QuestLayer(ctypes.Structure):
@@ -97,6 +107,7 @@ def load() -> ctypes.CDLL:
         V, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         C = ctypes.POINTER(QuestCacheDesc)
         O = ctypes.POINTER(QuestOpts)
+        N = ctypes.POINTER(QuestNarrowCacheDesc)
         sig = {
             "quest_workspace_size": (SZ, [C, I32, O]),
             "quest_workspace_init": (ctypes.c_int, [V, SZ, V]),
@@ -118,6 +129,18 @@ def load() -> ctypes.CDLL:
             "quest_last_error": (ctypes.c_char_p, []),
             "quest_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "quest_version": (ctypes.c_int, []),
+            "quest_narrow_workspace_size": (SZ, [N, I32, O]),
+            "quest_narrow_prefill": (ctypes.c_int, [N, V, V, I32, V, SZ, V]),
+            "quest_narrow_append": (ctypes.c_int, [N, V, V, V, SZ, V]),
+            "quest_narrow_sparse_decode": (ctypes.c_int, [N, V, V, V, I32, V, V, V, SZ, O, V]),
+            "quest_narrow_dense_decode": (ctypes.c_int, [N, V, V, V, V, SZ, O, V]),
+            "quest_narrow_decode": (ctypes.c_int, [N, V, I32, V, V, V, V, V, SZ, O, V]),
+            "quest_narrow_decode_step": (ctypes.c_int, [N, V, V, V, I32, V, V, V, V, V, SZ, O,
+                                                        V]),
+            "quest_narrow_window_decode": (ctypes.c_int, [N, V, I32, I32, V, V, V, SZ, O, V]),
+            "quest_window_workspace_size": (SZ, [C, I32, O]),
+            "quest_window_decode": (ctypes.c_int, [C, V, I32, I32, V, V, V, SZ, O, V]),
+            "quest_window_prefill": (ctypes.c_int, [C, V, I32, I32, I32, V, V, V, SZ, O, V]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -222,6 +245,80 @@ class PagedCache:
         B, max_pages = block_table.shape
         meta = torch.zeros((B, hkv, max_pages, 2, d), dtype=torch.float16, device=k_pool.device)
         return cls(k_pool, v_pool, meta, block_table, seq_lens, num_q_heads)
+
+    @property
+    def batch(self) -> int:
+        return self.desc.batch
+
+    @property
+    def num_kv_heads(self) -> int:
+        return self.desc.num_kv_heads
+
+    @property
+    def max_pages(self) -> int:
+        return self.desc.max_pages
+
+    @property
+    def page_size(self) -> int:
+        return self.desc.page_size
+
+
+@dataclass
+class NarrowCache:
+    """One layer's paged KV cache in 8 bits: complete pages are e4m3 with one fp32 scale per
+    (page, kv head), the open (partial last) page of a sequence is fp16.
+
+    k_pool, v_pool: [num_phys][Hkv][P][128] float8_e4m3fn; k_scale, v_scale: [num_phys][Hkv]
+    fp32; k_open, v_open: [B][Hkv][P][128] fp16; meta, block_table, seq_lens as in
+    ``PagedCache``.
+    """
+    k_pool: torch.Tensor
+    v_pool: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_open: torch.Tensor
+    v_open: torch.Tensor
+    meta: torch.Tensor
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+    num_q_heads: int
+
+    def __post_init__(self):
+        num_phys, hkv, P, d = self.k_pool.shape
+        B, max_pages = self.block_table.shape
+        _need(self.k_pool, "k_pool", torch.float8_e4m3fn)
+        _need(self.v_pool, "v_pool", torch.float8_e4m3fn, self.k_pool.shape)
+        _need(self.k_scale, "k_scale", torch.float32, (num_phys, hkv))
+        _need(self.v_scale, "v_scale", torch.float32, (num_phys, hkv))
+        _need(self.k_open, "k_open", torch.float16, (B, hkv, P, d))
+        _need(self.v_open, "v_open", torch.float16, (B, hkv, P, d))
+        _need(self.meta, "meta", torch.float16, (B, hkv, max_pages, 2, d))
+        _need(self.block_table, "block_table", torch.int32)
+        _need(self.seq_lens, "seq_lens", torch.int32, (B,))
+        self.desc = QuestNarrowCacheDesc(
+            B, int(self.num_q_heads), hkv, d, P, max_pages, num_phys, self.k_pool.data_ptr(),
+            self.v_pool.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+            self.k_open.data_ptr(), self.v_open.data_ptr(), self.meta.data_ptr(),
+            self.block_table.data_ptr(), self.seq_lens.data_ptr())
+
+    @classmethod
+    def allocate(cls, num_phys: int, num_kv_heads: int, page_size: int, block_table, seq_lens,
+                 num_q_heads: int):
+        """An empty cache of num_phys pages for this block table and these lengths."""
+        dev = block_table.device
+        B, max_pages = block_table.shape
+
+        def zeros(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        pool = (num_phys, num_kv_heads, page_size, HEAD_DIM)
+        rows = (B, num_kv_heads, page_size, HEAD_DIM)
+        return cls(zeros(pool, torch.uint8).view(torch.float8_e4m3fn),
+                   zeros(pool, torch.uint8).view(torch.float8_e4m3fn),
+                   zeros(pool[:2], torch.float32), zeros(pool[:2], torch.float32),
+                   zeros(rows, torch.float16), zeros(rows, torch.float16),
+                   zeros((B, num_kv_heads, max_pages, 2, HEAD_DIM), torch.float16), block_table,
+                   seq_lens, num_q_heads)
 
     @property
     def batch(self) -> int:
@@ -407,6 +504,8 @@ class DecodePlan:
     construction).  The outputs (``out``, ``lse``, ``idx_out``, ``count_out``) are
     overwritten by every call and returned by it."""
 
+    _decode_fn, _step_fn = "quest_decode", "quest_decode_step"
+
     def __init__(self, cache: PagedCache, top_k: int, ws: torch.Tensor,
                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
                  idx_out: Optional[torch.Tensor] = None,
@@ -425,6 +524,8 @@ class DecodePlan:
         self.idx_out, self.count_out = idx_out, count_out
         self._keep = (cache, ws, o)  # alive as long as the plan
         self._lib = load()
+        self._decode = getattr(self._lib, self._decode_fn)
+        self._step = getattr(self._lib, self._step_fn)
         self._desc = ctypes.byref(cache.desc)
         # the arguments after q (and k_new, v_new), in C order
         self._tail = (int(top_k), self.out.data_ptr(), _ptr(self.lse), _ptr(idx_out),
@@ -439,7 +540,7 @@ class DecodePlan:
         if not self._ok(q, self._qshape):
             _need(q, "q", torch.float16, self._qshape)
             raise ValueError("q is on another device than the cache")
-        rc = self._lib.quest_decode(self._desc, q.data_ptr(), *self._tail)
+        rc = self._decode(self._desc, q.data_ptr(), *self._tail)
         if rc:
             _check(rc)
         return self.out, self.lse
@@ -453,11 +554,186 @@ class DecodePlan:
             _need(v_new, "v_new", torch.float16, self._kvshape)
             raise ValueError("q / k_new / v_new are on another device than the cache")
         t = self._tail
-        rc = self._lib.quest_decode_step(self._desc, q.data_ptr(), k_new.data_ptr(),
-                                         v_new.data_ptr(), *t)
+        rc = self._step(self._desc, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), *t)
         if rc:
             _check(rc)
         return self.out, self.lse
+
+
+def narrow_workspace(cache: NarrowCache, top_k: int = 1,
+                     o: Optional[QuestOpts] = None) -> torch.Tensor:
+    """A zeroed workspace for every narrow_* call on this cache with this top_k / opts."""
+    lib = load()
+    n = lib.quest_narrow_workspace_size(ctypes.byref(cache.desc), int(top_k), _opts_ref(o))
+    if n == 0:
+        raise QuestError(QUEST_ERR_INVALID_ARG, lib.quest_last_error().decode())
+    return torch.zeros(int(n), dtype=torch.uint8, device=cache.k_pool.device)
+
+
+def narrow_prefill(cache: NarrowCache, k: torch.Tensor, v: torch.Tensor, ws: torch.Tensor,
+                   stream=None) -> None:
+    """``prefill`` into a narrow cache: complete pages become e4m3, the rest joins the open
+    page."""
+    if k.dim() != 4:
+        raise ValueError("k must be [batch][n_tokens][num_kv_heads][128]")
+    shape = (cache.batch, k.shape[1], cache.num_kv_heads, HEAD_DIM)
+    _need(k, "k", torch.float16, shape)
+    _need(v, "v", torch.float16, shape)
+    _check(load().quest_narrow_prefill(ctypes.byref(cache.desc), k.data_ptr(), v.data_ptr(),
+                                       int(k.shape[1]), ws.data_ptr(), ws.numel(),
+                                       _stream(stream)))
+
+
+def narrow_append(cache: NarrowCache, k_new: torch.Tensor, v_new: torch.Tensor,
+                  ws: torch.Tensor, stream=None) -> None:
+    """``append`` into a narrow cache."""
+    shape = (cache.batch, cache.num_kv_heads, HEAD_DIM)
+    _need(k_new, "k_new", torch.float16, shape)
+    _need(v_new, "v_new", torch.float16, shape)
+    _check(load().quest_narrow_append(ctypes.byref(cache.desc), k_new.data_ptr(),
+                                      v_new.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      _stream(stream)))
+
+
+def narrow_sparse_decode(cache: NarrowCache, q: torch.Tensor, idx: torch.Tensor,
+                         count: torch.Tensor, top_k: int, ws: torch.Tensor,
+                         o: Optional[QuestOpts] = None, out=None, lse=None,
+                         want_lse: bool = True, stream=None):
+    """``sparse_decode`` over a narrow cache."""
+    _need(q, "q", torch.float16, (cache.batch, cache.desc.num_q_heads, HEAD_DIM))
+    _need(idx, "idx", torch.int32, (cache.batch, cache.num_kv_heads, top_k))
+    _need(count, "count", torch.int32, (cache.batch, cache.num_kv_heads))
+    out, lse = _out(cache, q, out, lse, want_lse)
+    _check(load().quest_narrow_sparse_decode(
+        ctypes.byref(cache.desc), q.data_ptr(), idx.data_ptr(), count.data_ptr(), int(top_k),
+        out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
+    return out, lse
+
+
+def narrow_decode(cache: NarrowCache, q: torch.Tensor, top_k: int, ws: torch.Tensor,
+                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
+                  idx_out: Optional[torch.Tensor] = None,
+                  count_out: Optional[torch.Tensor] = None, stream=None):
+    """``decode`` (page bounds, top-K, attention over the kept pages) on a narrow cache."""
+    return NarrowPlan(cache, top_k, ws, o, out, lse, want_lse, idx_out, count_out,
+                      stream).decode(q)
+
+
+def narrow_decode_step(cache: NarrowCache, q: torch.Tensor, k_new: torch.Tensor,
+                       v_new: torch.Tensor, top_k: int, ws: torch.Tensor,
+                       o: Optional[QuestOpts] = None, out=None, lse=None,
+                       want_lse: bool = True, idx_out: Optional[torch.Tensor] = None,
+                       count_out: Optional[torch.Tensor] = None, stream=None):
+    """``decode_step`` (append, then decode) on a narrow cache."""
+    return NarrowPlan(cache, top_k, ws, o, out, lse, want_lse, idx_out, count_out,
+                      stream).step(q, k_new, v_new)
+
+
+def narrow_dense_decode(cache: NarrowCache, q: torch.Tensor, ws: torch.Tensor,
+                        o: Optional[QuestOpts] = None, out=None, lse=None,
+                        want_lse: bool = True, stream=None):
+    """``dense_decode`` over a narrow cache."""
+    return NarrowPlan(cache, 1, ws, o, out, lse, want_lse, stream=stream).dense(q)
+
+
+def narrow_window_decode(cache: NarrowCache, q: torch.Tensor, sink_tokens: int, window: int,
+                         ws: torch.Tensor, o: Optional[QuestOpts] = None, out=None, lse=None,
+                         want_lse: bool = True, stream=None):
+    """``window_decode`` over a narrow cache."""
+    return WindowPlan(cache, sink_tokens, window, ws, o, out, lse, want_lse, stream).decode(q)
+
+
+class NarrowPlan(DecodePlan):
+    """``DecodePlan`` for a narrow cache: ``decode`` and ``step`` as there, ``dense`` for
+    attention over every token."""
+
+    _decode_fn, _step_fn = "quest_narrow_decode", "quest_narrow_decode_step"
+
+    def dense(self, q: torch.Tensor):
+        """quest_narrow_dense_decode of this step's queries; returns (out, lse)."""
+        if not self._ok(q, self._qshape):
+            _need(q, "q", torch.float16, self._qshape)
+            raise ValueError("q is on another device than the cache")
+        t = self._tail
+        rc = self._lib.quest_narrow_dense_decode(self._desc, q.data_ptr(), t[1], t[2], *t[5:])
+        if rc:
+            _check(rc)
+        return self.out, self.lse
+
+
+def window_workspace(cache: PagedCache, n_tokens: int = 1,
+                     o: Optional[QuestOpts] = None) -> torch.Tensor:
+    """A zeroed workspace for window_decode and for window_prefill of up to n_tokens query
+    tokens per sequence."""
+    lib = load()
+    n = lib.quest_window_workspace_size(ctypes.byref(cache.desc), int(n_tokens), _opts_ref(o))
+    if n == 0:
+        raise QuestError(QUEST_ERR_INVALID_ARG, lib.quest_last_error().decode())
+    return torch.zeros(int(n), dtype=torch.uint8, device=cache.k_pool.device)
+
+
+class WindowPlan:
+    """window_decode (of a ``PagedCache``) or narrow_window_decode (of a ``NarrowCache``)
+    bound to its cache, sinks, window, workspace, stream and outputs, for a decode loop: each
+    call only checks q.  The outputs are overwritten by every call and returned by it."""
+
+    def __init__(self, cache, sink_tokens: int, window: int, ws: torch.Tensor,
+                 o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
+                 stream=None):
+        self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
+        self._dev = cache.k_pool.get_device()
+        probe = torch.empty(0, dtype=torch.float16, device=cache.k_pool.device)
+        self.out, self.lse = _out(cache, probe, out, lse, want_lse)
+        _need(ws, "ws", torch.uint8)
+        self._keep = (cache, ws, o)  # alive as long as the plan
+        self._lib = load()
+        self._fn = (self._lib.quest_narrow_window_decode if isinstance(cache, NarrowCache)
+                    else self._lib.quest_window_decode)
+        self._desc = ctypes.byref(cache.desc)
+        self._tail = (int(sink_tokens), int(window), self.out.data_ptr(), _ptr(self.lse),
+                      ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream))
+
+    def decode(self, q: torch.Tensor):
+        """The windowed attention of this step's queries; returns (out, lse)."""
+        if not (type(q) is torch.Tensor and q.dtype is torch.float16 and
+                q.shape == self._qshape and q.get_device() == self._dev and q.is_contiguous()):
+            _need(q, "q", torch.float16, self._qshape)
+            raise ValueError("q is on another device than the cache")
+        rc = self._fn(self._desc, q.data_ptr(), *self._tail)
+        if rc:
+            _check(rc)
+        return self.out, self.lse
+
+
+def window_decode(cache: PagedCache, q: torch.Tensor, sink_tokens: int, window: int,
+                  ws: torch.Tensor, o: Optional[QuestOpts] = None, out=None, lse=None,
+                  want_lse: bool = True, stream=None):
+    """Attention of the last token of every sequence over the first sink_tokens tokens and
+    the last `window` ones (itself included)."""
+    return WindowPlan(cache, sink_tokens, window, ws, o, out, lse, want_lse, stream).decode(q)
+
+
+def window_prefill(cache: PagedCache, q: torch.Tensor, sink_tokens: int, window: int,
+                   ws: torch.Tensor, o: Optional[QuestOpts] = None, out=None, lse=None,
+                   want_lse: bool = True, stream=None):
+    """Prompt attention: q [B][n][Hq][128] are the queries of the last n tokens of every
+    sequence (written by ``prefill`` before), each over the first sink_tokens tokens and the
+    last `window` ones up to itself.  Returns out [B][n][Hq][128] and lse [B][n][Hq]."""
+    if q.dim() != 4:
+        raise ValueError("q must be [batch][n_tokens][num_q_heads][128]")
+    shape = (cache.batch, q.shape[1], cache.desc.num_q_heads, HEAD_DIM)
+    _need(q, "q", torch.float16, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float16, device=q.device)
+    _need(out, "out", torch.float16, shape)
+    if lse is None and want_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, shape[:3])
+    _check(load().quest_window_prefill(
+        ctypes.byref(cache.desc), q.data_ptr(), int(shape[1]), int(sink_tokens), int(window),
+        out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
+    return out, lse
 
 
 def decode_layers(cache: PagedCache, layers: Sequence[PagedCache], q: Sequence[torch.Tensor],

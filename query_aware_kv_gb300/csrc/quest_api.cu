@@ -208,6 +208,10 @@ int decode_workspace_requirement(const quest_cache_t* cache, int top_k, size_t* 
 
 int set_last_error(int code, const char* message) { return fail(code, "%s", message); }
 
+int check_cache_desc(const quest_cache_t* cache) { return check_cache(cache); }
+int check_top_k(int top_k) { return check_topk(top_k); }
+int check_workspace(void* ws, size_t ws_bytes, size_t need) { return check_ws(ws, ws_bytes, need); }
+
 }  // namespace quest
 
 extern "C" {

@@ -26,6 +26,7 @@ constexpr long long kDefaultWaitNs = 1000000000LL;
 enum FaultSite : int {
   kSiteMeta = 1, kSiteAppend = 2, kSiteScore = 3, kSiteTopk = 4, kSiteDecode = 5,
   kSiteWaitSelection = 6, kSiteWaitStage = 7, kSiteWaitSlot = 8, kSiteSelection = 9,
+  kSiteSpan = 10, kSitePrompt = 11,
 };
 
 // First 256 bytes of the workspace.
@@ -188,6 +189,47 @@ int stream_slots(int G, int P, int max_pages, int top_k, int batch, int hq);
 size_t stream_smem_bytes(int G, int P, int max_pages, int top_k, int batch, int hq);
 cudaError_t launch_stream(const Params& p, const LayerPtrs& lay, int G, int max_ctas,
                           cudaStream_t s);
+// A narrow (8-bit) cache's own tensors (quest_narrow_cache_t); shape, boxes, block table
+// and lengths travel in Params.
+struct NarrowPtrs {
+  unsigned char* k_pool;  // e4m3 [num_phys][Hkv][P][128]
+  unsigned char* v_pool;
+  float* k_scale;         // [num_phys][Hkv]
+  float* v_scale;
+  __half* k_open;         // [B][Hkv][P][128]: the rows of each sequence's open page
+  __half* v_open;
+};
+
+// Which pages a span-decode row attends over.
+enum SpanMode : int { kSpanDense = 0, kSpanList = 1, kSpanWindow = 2 };
+
+// One launch of the span decode (quest_span_kernel.cu): a row is one query token and kv
+// head, its kept pages cut into n_splits runs.
+struct SpanParams {
+  Params p;               // q, out, lse: [B][n_tokens][Hq][128] / [B][n_tokens][Hq];
+                          // n_splits, part_ml, part_acc, decode_arrive: per row
+  NarrowPtrs nar;         // narrow caches only
+  int mode;               // SpanMode
+  int sink, window;       // kSpanWindow, in tokens
+  int n_tokens;           // query tokens per sequence (the last ones); 1 but for prompts
+};
+
+// Splits of a span-decode launch over `rows` rows of at most `pages` pages (1 for more than
+// kSplitRows rows: the counters of a workspace are where every call expects them).
+constexpr int kSplitRows = 1024;
+int span_splits(bool narrow, long long rows, int pages, int user_pps, int page_size);
+// The most partials (rows * splits) that a launch of up to `rows` rows can write.
+long long span_max_parts(bool narrow, long long rows, int pages, int user_pps, int page_size);
+cudaError_t launch_span(const SpanParams& sp, bool narrow, cudaStream_t s);
+cudaError_t launch_narrow_prefill(const Params& p, const NarrowPtrs& nar, const __half* k,
+                                  const __half* v, int n, cudaStream_t s);
+cudaError_t launch_narrow_append(const Params& p, const NarrowPtrs& nar, const __half* k_new,
+                                 const __half* v_new, cudaStream_t s);
+// Host checks shared with quest_api.cu (status code, error text set).
+int check_cache_desc(const quest_cache_t* cache);
+int check_top_k(int top_k);
+int check_workspace(void* ws, size_t ws_bytes, size_t need);
+
 constexpr int kStreamPiecePages = 8;  // kept pages per decode piece of the stream kernel
 constexpr size_t kMaxSmem = 227 * 1024;  // dynamic shared memory of one CTA
 

@@ -1,0 +1,603 @@
+// quest_span_kernel.cu - split-K attention of single query tokens over a run of pages of a
+// paged cache, on matrix instructions fed straight from global memory.
+//
+// One row is (query token, kv head): its G = 1..8 query heads attend over a list of pages
+// (every page, a selection, or the pages of a few sink tokens and of a sliding window):
+//   out_h = sum_t softmax_t(q_h . k_t / sqrt(128)) v_t,   lse_h = log sum_t exp(...)
+// The cache is fp16, or e4m3 with an fp32 scale per (page, kv head) and an fp16 open page.
+//
+// What bounds it: DRAM.  A token costs 512 B (fp16) or 256 B (e4m3) and 512 G flops.  On
+// the FP32 lanes eight heads over an e4m3 cache would need 54 TFMA/s at the copy rate, more
+// than the card has; mma.m16n8k16 takes the G heads as its eight columns and needs under a
+// fifth of that pipe.  tcgen05 would need the e4m3 tokens widened into shared memory first
+// (q is fp16, and both operands of one product have the same type) and buys nothing while
+// the pipe idles.
+//
+// Layout: a warp takes 16 tokens at a time, K and V go from global memory to the registers
+// of the lanes that multiply them, with no shared memory, barrier or wait in the loop: the
+// order of the contraction index is free, so lane (r, c) (r = lane / 4, c = lane % 4) owns
+// whole 16-byte pieces of K rows r and r + 8, and for V the 16-byte pieces at its r of the
+// tokens {2c, 2c+1, 2c+8, 2c+9}, whose columns a byte permute turns into V^T fragments.
+//   S^T [16 tokens x 8 heads] = K Q^T          (8 mma)
+//   O^T [128 dims  x 8 heads] += V^T P         (8 mma for the upper halves of P's fp32
+//                                               values and 8 for the lower ones)
+// P is split into two fp16 numbers (22 bits), so that its rounding stays below that of the
+// fp32 sums; the second product costs nothing next to the loads.  The running maximum moves
+// only when a score exceeds it by more than kLazy (in log2 units): weights are
+// 2^(s - m + kBias), so that the largest stay below 2^(kBias + kLazy) = 2^14 and the small
+// ones keep fp16's full precision down to 2^-22 of the reference.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "quest_device.cuh"
+
+namespace quest {
+
+namespace {
+
+constexpr int kSpanWarps = 8;
+constexpr int kSpanThreads = 32 * kSpanWarps;
+constexpr int kMaxSpanSplits = 64;
+constexpr int kSms = 152;  // of a GB300
+constexpr float kBias = 8.f;
+constexpr float kLazy = 6.f;
+
+__device__ __forceinline__ uint4 ldg_nc(const void* ptr) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(ptr));
+  return r;
+}
+// The same for buffers that an earlier call on the stream wrote and that share lines with
+// rows this kernel's grid may see again (the open page): a plain load.
+__device__ __forceinline__ uint4 ldg_plain(const void* ptr) {
+  return *reinterpret_cast<const uint4*>(ptr);
+}
+
+// D += A B, A 16x16 (row), B 16x8 (col), fp16 with fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of b16 over the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Two e4m3 numbers (16 bits) widened to fp16, exactly.
+__device__ __forceinline__ uint32_t widen(uint32_t two) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 t;\n\tmov.b32 {t, _}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(y)
+      : "r"(two));
+  return y;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t pack(__half a, __half b) {
+  const __half2 h = __halves2half2(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Which dims a lane holds.  k-step s of K Q^T multiplies dims dk .. dk + 3 of lane column c;
+// tile m of V^T P owns dims dv and dv + 1 of lane row r.  The e4m3 pieces are 16 dims wide,
+// the fp16 pieces 8; each keeps 64 or 128 B contiguous over the lanes of a load.
+template <bool N8> __device__ __forceinline__ int dk(int s, int c) {
+  return N8 ? 64 * (s >> 2) + 16 * c + 4 * (s & 3) : 32 * (s >> 1) + 8 * c + 4 * (s & 1);
+}
+template <bool N8> __device__ __forceinline__ int dv(int m, int r) {
+  return N8 ? 16 * r + 2 * m : 64 * (m >> 2) + 8 * r + 2 * (m & 3);
+}
+
+// The part of a row's softmax that one warp holds: reference maximum and (this lane's share
+// of the) sum for heads 2c and 2c + 1, and O^T.
+struct State {
+  float m[2], l[2];
+  float acc[8][4];
+};
+
+// Scores of a block (16 tokens) to weights: updates m, l and rescales acc when the
+// reference moves; returns P^T as fp16 pairs, upper and lower parts.
+__device__ __forceinline__ void weigh(State& st, float (&s)[4], uint32_t& h0, uint32_t& h1,
+                                      uint32_t& l0, uint32_t& l1) {
+  const bool over = fmaxf(s[0], s[2]) > st.m[0] + kLazy || fmaxf(s[1], s[3]) > st.m[1] + kLazy;
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = fmaxf(s[e], s[2 + e]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m = fmaxf(st.m[e], top);
+      const float f = m == -CUDART_INF_F ? 1.f : exp2f(st.m[e] - m);
+      st.m[e] = m;
+      st.l[e] *= f;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        st.acc[t][e] *= f;
+        st.acc[t][2 + e] *= f;
+      }
+    }
+  }
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float ref = st.m[i & 1] == -CUDART_INF_F ? 0.f : st.m[i & 1];
+    w[i] = exp2f(s[i] - ref + kBias);
+    st.l[i & 1] += w[i];
+  }
+  __half hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = __float2half_rn(w[i]);
+    lo[i] = __float2half_rn(w[i] - __half2float(hi[i]));
+  }
+  h0 = transpose8x8(pack(hi[0], hi[1]));
+  h1 = transpose8x8(pack(hi[2], hi[3]));
+  l0 = transpose8x8(pack(lo[0], lo[1]));
+  l1 = transpose8x8(pack(lo[2], lo[3]));
+}
+
+// acc[m] += scale * V^T P for one tile m, from this lane's V fragments.
+template <bool kScaled>
+__device__ __forceinline__ void add_tile(State& st, int m, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t h0, uint32_t h1, uint32_t l0,
+                                         uint32_t l1, float scale) {
+  if constexpr (kScaled) {
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    mma16816(t, a0, a1, a2, a3, l0, l1);
+    mma16816(t, a0, a1, a2, a3, h0, h1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st.acc[m][i] = fmaf(t[i], scale, st.acc[m][i]);
+  } else {
+    mma16816(st.acc[m], a0, a1, a2, a3, l0, l1);
+    mma16816(st.acc[m], a0, a1, a2, a3, h0, h1);
+  }
+}
+
+// Scores masked to the visible tokens: token t is visible if t < end and (t < sink_end or
+// t >= lo).
+struct Visible {
+  int end, lo, sink_end;
+  __device__ __forceinline__ bool token(int t) const {
+    return t < end && (t < sink_end || t >= lo);
+  }
+  __device__ __forceinline__ bool all16(int t) const {
+    return t + 16 <= end && (t + 16 <= sink_end || t >= lo);
+  }
+};
+
+// One 16-token block whose K / V rows are fp16 at kp / vp (row stride 128): the open page
+// of a narrow cache, in the narrow kernel's dims.
+__device__ __forceinline__ void open_block(State& st, const uint32_t (&qf)[8][2],
+                                           const __half* kp, const __half* vp, int t0,
+                                           const Visible& vis, float qscale, int r, int c) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint4 a[2], z[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      a[u] = ldg_plain(kp + r * kHeadDim + 64 * half + 16 * c + 8 * u);
+      z[u] = ldg_plain(kp + (r + 8) * kHeadDim + 64 * half + 16 * c + 8 * u);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int i = 2 * (w & 1);
+      mma16816(s, word(a[w >> 1], i), word(z[w >> 1], i), word(a[w >> 1], i + 1),
+               word(z[w >> 1], i + 1), qf[4 * half + w][0], qf[4 * half + w][1]);
+    }
+  }
+  const int ta = t0 + r, tz = t0 + r + 8;
+  s[0] = vis.token(ta) ? s[0] * qscale : -CUDART_INF_F;
+  s[1] = vis.token(ta) ? s[1] * qscale : -CUDART_INF_F;
+  s[2] = vis.token(tz) ? s[2] * qscale : -CUDART_INF_F;
+  s[3] = vis.token(tz) ? s[3] * qscale : -CUDART_INF_F;
+  uint32_t h0, h1, l0, l1;
+  weigh(st, s, h0, h1, l0, l1);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 2 * c + (j & 1) + 8 * (j >> 1);
+      v[j] = vis.token(t0 + t) ? ldg_plain(vp + t * kHeadDim + 16 * r + 8 * u)
+                               : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      add_tile<false>(st, 4 * u + i, __byte_perm(word(v[0], i), word(v[1], i), 0x5410),
+                      __byte_perm(word(v[0], i), word(v[1], i), 0x7632),
+                      __byte_perm(word(v[2], i), word(v[3], i), 0x5410),
+                      __byte_perm(word(v[2], i), word(v[3], i), 0x7632), h0, h1, l0, l1, 1.f);
+  }
+}
+
+// K and V of one block, as loaded.
+template <bool N8>
+struct Block {
+  static constexpr int kN = N8 ? 4 : 8;
+  uint4 k[kN], v[kN];
+};
+
+template <bool N8>
+__device__ __forceinline__ void load_k(Block<N8>& x, const unsigned char* kp, int r, int c) {
+  if constexpr (N8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x.k[i] = ldg_nc(kp + (r + 8 * (i >> 1)) * kHeadDim + 64 * (i & 1) + 16 * c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x.k[i] = ldg_nc(kp + (r + 8 * (i >> 2)) * 2 * kHeadDim + 64 * (i & 3) + 16 * c);
+  }
+}
+template <bool N8>
+__device__ __forceinline__ void load_v(Block<N8>& x, const unsigned char* vp, int r, int c) {
+  if constexpr (N8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x.v[j] = ldg_nc(vp + (2 * c + (j & 1) + 8 * (j >> 1)) * kHeadDim + 16 * r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x.v[j] = ldg_nc(vp + (2 * c + ((j >> 1) & 1) + 8 * (j >> 2)) * 2 * kHeadDim + 128 * (j & 1) +
+                      16 * r);
+  }
+}
+
+template <bool N8>
+__device__ __forceinline__ void scores(const Block<N8>& x, const uint32_t (&qf)[8][2],
+                                       float (&s)[4]) {
+  float u[4] = {0.f, 0.f, 0.f, 0.f};
+  s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    uint32_t a0, a1, a2, a3;
+    if constexpr (N8) {
+      const uint32_t p = word(x.k[t >> 2], t & 3), z = word(x.k[2 + (t >> 2)], t & 3);
+      a0 = widen(p);
+      a2 = widen(p >> 16);
+      a1 = widen(z);
+      a3 = widen(z >> 16);
+    } else {
+      const int i = 2 * (t & 1);
+      a0 = word(x.k[t >> 1], i);
+      a2 = word(x.k[t >> 1], i + 1);
+      a1 = word(x.k[4 + (t >> 1)], i);
+      a3 = word(x.k[4 + (t >> 1)], i + 1);
+    }
+    mma16816((t & 1) ? u : s, a0, a1, a2, a3, qf[t][0], qf[t][1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] += u[i];
+}
+
+// Values of tokens that the row does not see may be anything (a slot never written, a
+// token behind the window): their weight is 0, and 0 * NaN would not be.
+template <bool N8>
+__device__ __forceinline__ void zero_hidden(Block<N8>& x, const Visible& vis, int t0, int c) {
+#pragma unroll
+  for (int j = 0; j < Block<N8>::kN; ++j) {
+    const int e = N8 ? j : j >> 1;
+    if (!vis.token(t0 + 2 * c + (e & 1) + 8 * (e >> 1))) x.v[j] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+template <bool N8>
+__device__ __forceinline__ void accumulate(State& st, const Block<N8>& x, uint32_t h0, uint32_t h1,
+                                           uint32_t l0, uint32_t l1, float vscale) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (N8) {
+      // bytes (d, d + 1) of two tokens: {t0 d, t1 d, t0 d+1, t1 d+1}
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t sel = e ? 0x7362 : 0x5140;
+        const uint32_t p = __byte_perm(word(x.v[0], i), word(x.v[1], i), sel);
+        const uint32_t z = __byte_perm(word(x.v[2], i), word(x.v[3], i), sel);
+        add_tile<true>(st, 2 * i + e, widen(p), widen(p >> 16), widen(z), widen(z >> 16), h0, h1,
+                       l0, l1, vscale);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t a = word(x.v[u], i), b = word(x.v[2 + u], i);
+        const uint32_t y = word(x.v[4 + u], i), z = word(x.v[6 + u], i);
+        add_tile<false>(st, 4 * u + i, __byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                        __byte_perm(y, z, 0x5410), __byte_perm(y, z, 0x7632), h0, h1, l0, l1, 1.f);
+      }
+    }
+  }
+}
+
+// grid rows * n_splits (split fastest), kSpanThreads threads.  Split `s` of a row takes its
+// s-th share of the row's pages; warp w of the CTA every kSpanWarps-th page of it.
+template <bool N8>
+__global__ void __launch_bounds__(kSpanThreads, N8 ? 2 : 1) span_kernel(SpanParams sp) {
+  __shared__ float s_m[kSpanWarps][8], s_l[kSpanWarps][8];
+  __shared__ float s_red[kSpanWarps][8 * kHeadDim];
+  __shared__ int s_flag;
+  const Params& p = sp.p;
+  pdl_wait();
+  pdl_trigger();
+  const int split = (int)(blockIdx.x % (unsigned)p.n_splits);
+  const unsigned row = blockIdx.x / (unsigned)p.n_splits;  // (b * n_tokens + i) * Hkv + g
+  const int g = (int)(row % (unsigned)p.Hkv);
+  const int b = (int)(row / ((unsigned)p.Hkv * (unsigned)sp.n_tokens));
+  const int i_tok = (int)((row / (unsigned)p.Hkv) % (unsigned)sp.n_tokens);
+  const int G = p.Hq / p.Hkv, P = p.P;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+
+  // ---- the row's pages
+  const int L = load_len(p, b, kSiteSpan);
+  const int N = (L + P - 1) / P;
+  Visible vis;
+  vis.end = max(0, L - sp.n_tokens + i_tok + 1);
+  vis.lo = 0;
+  vis.sink_end = 0;
+  int n_sink = 0, first = 0, count = N;
+  const int* list = nullptr;
+  if (sp.mode == kSpanWindow) {
+    vis.lo = max(0, vis.end - sp.window);
+    vis.sink_end = min(sp.sink, vis.lo);
+    first = vis.lo / P;
+    n_sink = min((vis.sink_end + P - 1) / P, first);
+    count = vis.end > 0 ? n_sink + (vis.end + P - 1) / P - first : 0;
+  } else if (sp.mode == kSpanList) {
+    list = p.sel_idx + (size_t)row * p.top_k;  // n_tokens is 1: the row is (b, g)
+    count = p.sel_count[row];
+    const int cap = min(p.top_k, N);
+    if (count < 0 || count > cap) {
+      if (threadIdx.x == 0 && split == 0)
+        report(p, QUEST_ERR_BAD_SELECTION, b, count, kSiteSelection);
+      count = max(0, min(count, cap));
+    }
+  }
+  const int i0 = (int)((long long)count * split / p.n_splits);
+  const int i1 = (int)((long long)count * (split + 1) / p.n_splits);
+
+  // ---- the query: head r of the group in lane (r, c)'s K Q^T columns
+  const size_t head0 = (size_t)(b * sp.n_tokens + i_tok) * p.Hq + (size_t)g * G;
+  uint32_t qf[8][2];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    uint2 w = make_uint2(0u, 0u);
+    if (r < G)
+      w = *reinterpret_cast<const uint2*>(p.q + (head0 + r) * kHeadDim + dk<N8>(t, c));
+    qf[t][0] = w.x;
+    qf[t][1] = w.y;
+  }
+
+  State st;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    st.m[e] = -CUDART_INF_F;
+    st.l[e] = 0.f;
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) st.acc[m][e] = 0.f;
+
+  const unsigned char* k_pool = N8 ? sp.nar.k_pool : reinterpret_cast<const unsigned char*>(p.k_pool);
+  const unsigned char* v_pool = N8 ? sp.nar.v_pool : reinterpret_cast<const unsigned char*>(p.v_pool);
+  const int row_bytes = N8 ? kHeadDim : 2 * kHeadDim;
+  const int open_page = (N8 && L % P) ? L / P : -1;
+  const int per_page = P / 16;
+  bool has_open = false;
+
+  // ---- the warp's pages, 32 at a time: lane j looks the j-th one up
+  for (int base = i0 + warp; base < i1; base += 32 * kSpanWarps) {
+    const int mine = base + kSpanWarps * lane;
+    int lp = -1, phys = 0, ok = 0;
+    float ks = p.qscale, vs = 1.f;
+    if (mine < i1) {
+      lp = sp.mode == kSpanDense ? mine
+           : sp.mode == kSpanList ? list[mine]
+           : mine < n_sink ? mine : first + mine - n_sink;
+      if (lp < 0 || lp >= N) {
+        report(p, QUEST_ERR_BAD_SELECTION, b, lp, kSiteSelection);
+      } else if (lp == open_page) {
+        ok = 2;
+      } else {
+        phys = p.block_table[(size_t)b * p.max_pages + lp];
+        if (phys < 0 || phys >= p.num_phys) {
+          report(p, QUEST_ERR_BAD_PAGE, b, lp, kSiteSpan);
+          phys = 0;
+        } else {
+          ok = 1;
+          if constexpr (N8) {
+            ks *= sp.nar.k_scale[(size_t)phys * p.Hkv + g];
+            vs = sp.nar.v_scale[(size_t)phys * p.Hkv + g];
+          }
+        }
+      }
+    }
+    has_open |= __any_sync(0xffffffffu, ok == 2);
+    // blocks of the pages to stream; a page that is not (unmapped, open) is left out
+    unsigned live = __ballot_sync(0xffffffffu, ok == 1);
+    if (!live) continue;
+    Block<N8> x;
+    int j = __ffs(live) - 1, sub = 0;
+    size_t off = ((size_t)__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * P * row_bytes;
+    load_k<N8>(x, k_pool + off, r, c);
+    load_v<N8>(x, v_pool + off, r, c);
+    while (true) {
+      const int t0 = __shfl_sync(0xffffffffu, lp, j) * P + 16 * sub;
+      const float kscale = __shfl_sync(0xffffffffu, ks, j);
+      const float vscale = N8 ? __shfl_sync(0xffffffffu, vs, j) : 1.f;
+      // the next block
+      if (++sub == per_page) {
+        sub = 0;
+        live &= live - 1u;
+      }
+      const bool more = live != 0u;
+      j = more ? __ffs(live) - 1 : 0;
+      const size_t next =
+          (((size_t)__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * P + 16 * sub) * row_bytes;
+      float s[4];
+      scores<N8>(x, qf, s);
+      if (more) load_k<N8>(x, k_pool + next, r, c);
+      const bool whole = vis.all16(t0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] *= kscale;
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!vis.token(t0 + r + 8 * (i >> 1))) s[i] = -CUDART_INF_F;
+        zero_hidden<N8>(x, vis, t0, c);
+      }
+      uint32_t h0, h1, l0, l1;
+      weigh(st, s, h0, h1, l0, l1);
+      accumulate<N8>(st, x, h0, h1, l0, l1, vscale);
+      if (!more) break;
+      load_v<N8>(x, v_pool + next, r, c);
+    }
+  }
+  if (N8 && has_open) {
+    const size_t o = ((size_t)b * p.Hkv + g) * P * kHeadDim;
+    for (int sub = 0; sub < per_page; ++sub)
+      if (open_page * P + 16 * sub < vis.end)
+        open_block(st, qf, sp.nar.k_open + o + sub * 16 * kHeadDim,
+                   sp.nar.v_open + o + sub * 16 * kHeadDim, open_page * P + 16 * sub, vis,
+                   p.qscale, r, c);
+  }
+
+  // ---- the warps' states into one
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], o);
+  if (r == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s_m[warp][2 * c + e] = st.m[e];
+      s_l[warp][2 * c + e] = st.l[e];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int h = 2 * c + e;
+    if (h < G) {
+      float M = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      const float f = st.m[e] == -CUDART_INF_F ? 0.f : exp2f(st.m[e] - M);
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        *reinterpret_cast<float2*>(&s_red[warp][h * kHeadDim + dv<N8>(m, r)]) =
+            make_float2(st.acc[m][e] * f, st.acc[m][2 + e] * f);
+      }
+    }
+  }
+  __syncthreads();
+  const size_t slot0 = ((size_t)row * G) * p.n_splits;  // partials: [row][head][split]
+  for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
+    const int h = o / kHeadDim, d = o % kHeadDim;
+    float M = -CUDART_INF_F, Z = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < kSpanWarps; ++w) {
+      A += s_red[w][o];
+      if (s_m[w][h] != -CUDART_INF_F) Z = fmaf(s_l[w][h], exp2f(s_m[w][h] - M), Z);
+    }
+    if (p.n_splits == 1) {
+      p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
+      if (d == 0 && p.lse)
+        p.lse[head0 + h] = M == -CUDART_INF_F
+                               ? -CUDART_INF_F
+                               : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+    } else {
+      const size_t slot = slot0 + (size_t)h * p.n_splits + split;
+      p.part_acc[slot * kHeadDim + d] = A;
+      if (d == 0) {
+        p.part_ml[2 * slot] = M;
+        p.part_ml[2 * slot + 1] = Z;
+      }
+    }
+  }
+  if (p.n_splits == 1) return;
+
+  // ---- the last split of the row merges the partials
+  if (!arrive_last<kSpanThreads, false>(&p.decode_arrive[row], (unsigned)p.n_splits, &s_flag))
+    return;
+  float* msc = &s_red[0][0];  // [G][n_splits] scales, then per head Z and M
+  if (warp < G) {
+    const float* ml = p.part_ml + 2 * (slot0 + (size_t)warp * p.n_splits);
+    float M = -CUDART_INF_F, Z = 0.f;
+    for (int s = lane; s < p.n_splits; s += 32) M = fmaxf(M, __ldcg(ml + 2 * s));
+    M = warp_max(M);
+    for (int s = lane; s < p.n_splits; s += 32) {
+      const float ms = __ldcg(ml + 2 * s);
+      const float f = ms == -CUDART_INF_F ? 0.f : exp2f(ms - M);
+      msc[warp * p.n_splits + s] = f;
+      Z = fmaf(__ldcg(ml + 2 * s + 1), f, Z);
+    }
+    Z = warp_sum(Z);
+    if (lane == 0) {
+      s_m[0][warp] = M;
+      s_l[0][warp] = Z;
+    }
+  }
+  __syncthreads();
+  for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
+    const int h = o / kHeadDim, d = o % kHeadDim;
+    const float* pa = p.part_acc + (slot0 + (size_t)h * p.n_splits) * kHeadDim + d;
+    float A = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < p.n_splits; ++s) {
+      A = fmaf(__ldcg(pa + (size_t)s * kHeadDim), msc[h * p.n_splits + s], A);
+    }
+    const float M = s_m[0][h], Z = s_l[0][h];
+    p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
+    if (d == 0 && p.lse)
+      p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
+                                            : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+  }
+  if (threadIdx.x == 0) p.decode_arrive[row] = 0u;
+}
+
+}  // namespace
+
+// With few rows a row's pages are shared by enough CTAs to fill the GPU once, each with at
+// least four pages a warp.
+static long long span_slots(bool narrow) { return (long long)kSms * (narrow ? 2 : 1); }
+
+int span_splits(bool narrow, long long rows, int pages, int user_pps, int page_size) {
+  if (rows <= 0 || rows > kSplitRows) return 1;
+  long long s;
+  if (user_pps > 0) {
+    s = (pages + user_pps - 1) / user_pps;
+  } else {
+    const long long most = std::max(1, pages * (page_size / 16) / (4 * kSpanWarps));
+    s = std::min(most, span_slots(narrow) / rows);
+  }
+  return (int)std::max<long long>(1, std::min<long long>(s, kMaxSpanSplits));
+}
+
+long long span_max_parts(bool narrow, long long rows, int pages, int user_pps, int page_size) {
+  rows = std::min<long long>(rows, kSplitRows);
+  if (user_pps > 0) return rows * span_splits(narrow, rows, pages, user_pps, page_size);
+  // fewer rows get more splits, up to the slots of the GPU together
+  return std::min(span_slots(narrow), rows * kMaxSpanSplits);
+}
+
+cudaError_t launch_span(const SpanParams& sp, bool narrow, cudaStream_t s) {
+  SpanParams pp = sp;
+  void* args[] = {&pp};
+  const long long rows = (long long)sp.p.B * sp.n_tokens * sp.p.Hkv;
+  const void* fn = narrow ? (const void*)span_kernel<true> : (const void*)span_kernel<false>;
+  return launch_pdl(fn, dim3((unsigned)(rows * sp.p.n_splits)), dim3(kSpanThreads), 0, s, args);
+}
+
+}  // namespace quest
