@@ -1,0 +1,630 @@
+// quest_prompt_kernel.cu - windowed attention of prompt tokens over a paged fp16 cache, on
+// the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands by TMA).
+//
+// The last n tokens of a sequence are queries; token at position i sees j <= i with j < sink
+// or i - j < window.  One CTA owns 256 query rows of one (sequence, kv head): two tiles of
+// 128 rows, a row being (token, query head) with the G heads of the group side by side, so
+// that a group shares every K / V tile.  The CTA's visible pages form a list (the sinks'
+// pages, then the window's), cut into tiles of 128 tokens; each page is fetched by TMA with
+// its own coordinates, so a tile is any 8 (or 4) pages and a handful of sinks costs one page
+// instead of a tile.
+//
+// Per K / V tile and query tile, with the running maximum and sum of a softmax:
+//   S = Q K^T            tcgen05.mma, both operands in shared memory, S in TMEM
+//   P = 2^(S c - m + 8)  the tile's 128 softmax threads, one row each (no shuffles), written
+//                        back over S as fp16
+//   O += P V             tcgen05.mma, P from TMEM, V in shared memory (MN-major), O in TMEM
+// Warps 0-3 and 4-7 are the softmax of the two tiles, warp 8 fetches, warp 9 issues the
+// products: while one tile is in its softmax, the tensor core works for the other.  The order of
+// issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's columns.
+// The maximum m moves only when a row exceeds it by more than 2^6 (then O is rescaled in
+// TMEM by the softmax threads themselves), so weights reach 2^14 at most and keep fp16's full
+// precision down to 2^-22 of the largest.  P enters the second product as one fp16 number:
+// a rounding of 2^-11 per weight, random in sign, against the final rounding to fp16 of the
+// same size; its sum l is taken in fp32 before that rounding.
+//
+// What bounds it: the tensor core and the exponentials together.  A tile pair is 4 products
+// of 128 x 128 x 128 (1024 cycles at the dense rate) and 2 * 128 * 128 exponentials.
+#include <cuda.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "quest_device.cuh"
+
+namespace quest {
+
+namespace {
+
+// Three warpgroups: the softmax of either tile, and the fetch and issue warps (8 and 9; 10 and
+// 11 only hold their share of the registers).  Registers: 384 x 168 at launch, then 216 for
+// the softmax threads (a row of 128 scores each) and 72 for the others, the same total.
+constexpr int kPromptThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of the launch");
+constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
+constexpr int kTileTokens = 128;     // tokens of a K / V tile
+constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
+constexpr int kKvStages = 5;         // K and V tiles in flight, alternating
+constexpr int kHalfBytes = kTileBytes / 2;  // 64 dims of every row: one 128-byte swizzle span
+constexpr float kBias = 8.f;
+constexpr float kLazy = 6.f;
+
+struct PromptSmem {
+  static constexpr int q = 0;                             // [2][32 KiB]
+  static constexpr int kv = 2 * kTileBytes;               // [kKvStages][32 KiB]
+  static constexpr int bars = kv + kKvStages * kTileBytes;
+  static constexpr int total = bars + 256;
+};
+static_assert(PromptSmem::total + 1024 <= (int)kMaxSmem, "shared memory of a CTA");
+
+struct PromptParams {
+  Params p;
+  int n_tokens, sink, window;
+  int q_blocks;  // CTAs along the tokens of a (sequence, kv head)
+};
+
+// ---- tcgen05 / TMA
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                   smem_u32(slot))
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base));
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+// D (+)= A B with A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// The same with A in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+#define QUEST_R8(a, i) a[i], a[i + 1], a[i + 2], a[i + 3], a[i + 4], a[i + 5], a[i + 6], a[i + 7]
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle.  Rows of 128 B, 8 rows an atom of
+// 1 KiB.  K-major (Q, K): atoms 1 KiB apart along the rows.  MN-major (V, whose 64-dim spans
+// are kHalfBytes apart): atoms 1 KiB apart along the tokens.
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(kHalfBytes >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp16 x fp16 -> fp32, 128 x 128 x 16; bit 16: B is MN-major.
+constexpr uint32_t kIdescQK = 1u << 4 | (kTileTokens >> 3) << 17 | (kTileRows >> 4) << 24;
+constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kTileRows >> 4) << 24;
+
+// ---- bounded waits: a wait that runs out sets the CTA's give-up flag, and everyone leaves
+// (Everything this kernel calls is inlined: around a call the compiler keeps to the registers
+// that the smallest warpgroup has, and a row of scores would spill.)
+__device__ __forceinline__ void record(const Params& p, int code, int b, int page) {
+  if (atomicCAS(p.status, 0, code) == 0) {
+    p.status[1] = b;
+    p.status[2] = page;
+    p.status[3] = kSitePrompt;
+  }
+}
+__device__ __forceinline__ bool prompt_wait_slow(const Params& p, uint64_t* bar, uint32_t parity,
+                                              volatile int* give_up) {
+  const long long t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*give_up) return false;
+    if (global_ns() - t0 > p.wait_limit_ns) {
+      *give_up = 1;
+      record(p, QUEST_ERR_TIMEOUT, -1, -1);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool prompt_wait(const Params& p, uint64_t* bar, uint32_t parity,
+                                            volatile int* give_up) {
+  return mbar_try_wait(bar, parity) || prompt_wait_slow(p, bar, parity, give_up);
+}
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[kKvStages], kv_empty[kKvStages];
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  int give_up;
+};
+static_assert(sizeof(Bars) <= 256, "barrier area");
+
+// The CTA's list of pages: the sinks', then those from the first token any row's window
+// holds to the last row's own.
+struct PageList {
+  int n_sink, first, count, lo;  // lo: the first position in some row's window
+  __device__ __forceinline__ int page(int i) const { return i < n_sink ? i : first + i - n_sink; }
+};
+
+// A weight row's threads: 128 scores to weights.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int P>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  extern __shared__ unsigned char smem_raw[];
+  constexpr int PPT = kTileTokens / P;  // pages of a K / V tile
+  const Params& p = pp.p;
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + PromptSmem::bars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, TT = kTileRows / G;  // tokens of a query tile
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars.q_full, 1);
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(&bars.kv_full[i], 1);
+      mbar_init(&bars.kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.o_full[t], 1);
+    }
+    mbar_init(&bars.drain, 1);
+    bars.give_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&bars.tmem);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+  volatile int* give_up = &bars.give_up;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the CTA's work
+  const int split = (int)(blockIdx.x % (unsigned)p.n_splits);
+  const unsigned item = blockIdx.x / (unsigned)p.n_splits;  // (b * Hkv + g) * q_blocks + block
+  const int blk = pp.q_blocks - 1 - (int)(item % (unsigned)pp.q_blocks);
+  const int bg = (int)(item / (unsigned)pp.q_blocks);
+  const int b = bg / p.Hkv, g = bg % p.Hkv;
+  const int n = pp.n_tokens, tok0 = blk * 2 * TT;
+  const int tok1 = min(n, tok0 + 2 * TT);
+  int L = p.seq_lens[b];
+  if (L < 0 || (long long)L > (long long)p.max_pages * P) {
+    if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
+    L = 0;
+  }
+  const int pos0 = L - n;  // position of query token 0 (may be negative)
+  const int end = pos0 + tok1;
+  PageList list{0, 0, 0, 0};
+  if (end > 0) {
+    list.lo = max(0, max(0, pos0 + tok0) - pp.window + 1);
+    list.first = list.lo / P;
+    list.n_sink = min((min(pp.sink, list.lo) + P - 1) / P, list.first);
+    list.count = list.n_sink + (end + P - 1) / P - list.first;
+  }
+  const int tiles = (list.count + PPT - 1) / PPT;
+  const int j0 = (int)((long long)tiles * split / p.n_splits);
+  const int j1 = (int)((long long)tiles * (split + 1) / p.n_splits);
+  const int n_q = tok1 - tok0 > TT ? 2 : 1;  // query tiles with rows
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+    // ---- fetch: lane (slot, half) brings 64 dims of page `slot` of every tile
+    if (j1 > j0) {
+      if (lane < 2 * n_q) {
+        if (lane == 0) mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
+      }
+      __syncwarp();
+      if (lane < 2 * n_q)
+        tma_3d(smem + PromptSmem::q + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &map_q,
+               64 * (lane & 1), g * G, b * n + tok0 + (lane >> 1) * TT, &bars.q_full);
+      const int slot = lane >> 1, half = lane & 1;
+      auto lookup = [&](int j) {
+        if (slot >= PPT) return 0;
+        // slots behind the list's end repeat its last page (their tokens are hidden)
+        const int i = min(j * PPT + slot, list.count - 1);
+        const int lp = list.page(i);
+        int phys = p.block_table[(size_t)b * p.max_pages + lp];
+        if (phys < 0 || phys >= p.num_phys) {
+          if (half == 0) record(p, QUEST_ERR_BAD_PAGE, b, lp);
+          phys = 0;
+        }
+        return phys;
+      };
+      int unit = 0;  // K and V tiles fetched so far
+      int next = lookup(j0);
+      bool ok = true;
+      for (int j = j0; j < j1 && ok; ++j) {
+        const int phys = next;
+        if (j + 1 < j1) next = lookup(j + 1);
+        const int y = (phys * p.Hkv + g) * P;
+        for (int kv = 0; kv < 2; ++kv, ++unit) {
+          const int st = unit % kKvStages, round = unit / kKvStages;
+          if (round > 0 && !prompt_wait(p, &bars.kv_empty[st], (round - 1) & 1, give_up)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
+          __syncwarp();
+          if (slot < PPT)
+            tma_2d(smem + PromptSmem::kv + st * kTileBytes + half * kHalfBytes + slot * P * 128,
+                   kv ? &map_v : &map_k, 64 * half, y, &bars.kv_full[st]);
+        }
+      }
+      if (!ok) {  // leave only when every copy has landed
+        prompt_wait(p, &bars.q_full, 0, give_up);
+        for (int u = max(0, unit - kKvStages); u < unit; ++u)
+          for (int i = 0; i < 1 << 20; ++i)
+            if (mbar_try_wait(&bars.kv_full[u % kKvStages], (u / kKvStages) & 1)) break;
+      }
+    }
+  } else if (warp == 9) {
+    // ---- issue
+    if (j1 > j0) {
+      const uint32_t q_addr = smem_u32(smem + PromptSmem::q);
+      const uint32_t kv_addr = smem_u32(smem + PromptSmem::kv);
+      auto qk = [&](int t, int st) {
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 16; ++k) {
+            const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
+            mma_ss(tmem + t * 128, desc_k_major(q_addr + t * kTileBytes + o),
+                   desc_k_major(kv_addr + st * kTileBytes + o), kIdescQK, k > 0);
+          }
+          commit(&bars.s_full[t]);
+        }
+        __syncwarp();
+      };
+      bool ok = prompt_wait(p, &bars.q_full, 0, give_up);
+      int unit = 0;
+      ok = ok && prompt_wait(p, &bars.kv_full[0], 0, give_up);
+      fence_after();
+      if (ok) {
+        for (int t = 0; t < n_q; ++t) qk(t, 0);
+        if (lane == 0) commit(&bars.kv_empty[0]);
+      }
+      unit = 1;
+      for (int j = j0; j < j1 && ok; ++j) {
+        const int sv = unit % kKvStages;
+        ok = prompt_wait(p, &bars.kv_full[sv], (unit / kKvStages) & 1, give_up);
+        if (!ok) break;
+        ++unit;
+        // Values that no row of the CTA sees (slots behind the last token, tokens between
+        // the sinks and the first window) may be anything: 0 * NaN is not 0.
+        const int i0 = j * PPT;
+        if (i0 <= list.n_sink || (j + 1) * PPT >= list.count) {
+          bool touched = false;
+          for (int c = lane; c < kTileTokens; c += 32) {
+            const int i = i0 + c / P;
+            const int pos = list.page(min(i, list.count - 1)) * P + c % P;
+            if (i >= list.count || pos >= end || (pos >= pp.sink && pos < list.lo)) {
+              touched = true;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                *reinterpret_cast<uint4*>(smem + PromptSmem::kv + sv * kTileBytes +
+                                          (e >> 3) * kHalfBytes + c * 128 + (e & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          if (touched) fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const int sk = unit % kKvStages;
+        bool have_k = false;
+        for (int t = 0; t < n_q && ok; ++t) {
+          ok = prompt_wait(p, &bars.p_full[t], (j - j0) & 1, give_up);
+          if (!ok) break;
+          fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < kTileTokens / 16; ++k)
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                     desc_mn_major(kv_addr + sv * kTileBytes + k * 2048), kIdescPV,
+                     j > j0 || k > 0);
+            if (t == n_q - 1) commit(&bars.kv_empty[sv]);
+          }
+          __syncwarp();
+          if (j + 1 < j1) {
+            if (!have_k) {
+              ok = prompt_wait(p, &bars.kv_full[sk], (unit / kKvStages) & 1, give_up);
+              if (!ok) break;
+              have_k = true;
+              fence_after();
+            }
+            qk(t, sk);
+            if (t == n_q - 1 && lane == 0) commit(&bars.kv_empty[sk]);
+          } else if (lane == 0) {
+            commit(&bars.o_full[t]);
+          }
+          __syncwarp();
+        }
+        if (have_k) ++unit;
+      }
+      if (!ok) {  // products in flight finish before their memory goes
+        if (lane == 0) commit(&bars.drain);
+        __syncwarp();
+        for (int i = 0; i < 1 << 20; ++i)
+          if (mbar_try_wait(&bars.drain, 0)) break;
+      }
+    }
+  }
+  } else {
+    // ---- softmax: thread = row of its tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    const int tok = tok0 + t * TT + row / G;
+    const int pr = pos0 + tok;  // the row's position
+    const bool mine = tok < tok1;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + 256 + t * 128;
+    float m = -CUDART_INF_F, l = 0.f;
+    bool ok = true;
+    if (t < n_q) {
+      const int r0 = pos0 + tok0 + t * TT, r1 = min(r0 + TT, end) - 1;
+      for (int j = j0; j < j1; ++j) {
+        ok = prompt_wait(p, &bars.s_full[t], (j - j0) & 1, give_up);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        float s[kTileTokens];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          tmem_ld32(s_col + 32 * u, reinterpret_cast<uint32_t*>(s) + 32 * u);
+        tmem_wait_ld();
+        const int i0 = j * PPT;
+        const int base = list.page(i0) * P;
+        const bool whole = i0 >= list.n_sink && i0 + PPT <= list.count &&
+                           base + kTileTokens - 1 <= r0 && base > r1 - pp.window;
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < PPT; ++e) {
+            const int i = i0 + e;
+            const int at = i < list.count ? list.page(i) * P : 0x3fffffff;
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const int pos = at + k;
+              if (!(pos <= pr && (pos < pp.sink || pos > pr - pp.window)))
+                s[e * P + k] = -CUDART_INF_F;
+            }
+          }
+        }
+        float top = s[0];
+#pragma unroll
+        for (int k = 1; k < kTileTokens; ++k) top = fmaxf(top, s[k]);
+        top *= p.qscale;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          const float mn = fmaxf(m, top);
+          const float f = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
+          m = mn;
+          l *= f;
+          if (j > j0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t o[32];
+              tmem_ld32(o_col + 32 * u, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(o_col + 32 * u, o);
+            }
+          }
+        }
+        const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float a = ex2(fmaf(s[64 * u + 2 * k], p.qscale, shift));
+            const float c = ex2(fmaf(s[64 * u + 2 * k + 1], p.qscale, shift));
+            sum += a + c;
+            w[k] = pack2(a, c);
+          }
+          tmem_st32(s_col + 32 * u, w);
+        }
+        l += sum;
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t]);
+      }
+      if (j1 > j0 && ok) ok = prompt_wait(p, &bars.o_full[t], 0, give_up);
+      ok = __all_sync(0xffffffffu, ok);
+      fence_after();
+      // ---- out = O / l
+      const size_t at = ((size_t)b * n + tok) * p.Hq + (size_t)g * G + row % G;
+      const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
+      if (ok) {
+        const float inv = none ? 0.f : 1.f / l;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t o[32];
+          if (j1 > j0) {
+            tmem_ld32(o_col + 32 * u, o);
+            tmem_wait_ld();
+          }
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim + 32 * u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = none ? 0u
+                            : pack2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                    __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (mine && p.lse)
+          p.lse[at] = none ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 9) tmem_free(tmem);
+}
+
+// cuTensorMapEncodeTiled, taken from the driver at run time (nothing links against it).
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn* fn) {
+  static std::mutex mu;
+  static EncodeFn found = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!found) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r);
+    if (e != cudaSuccess) return e;
+    if (r != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    found = reinterpret_cast<EncodeFn>(f);
+  }
+  *fn = found;
+  return cudaSuccess;
+}
+
+// A map of fp16 rows of 128: boxes of 64 dims (a 128-byte swizzle span) x the given rows.
+cudaError_t make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeFn fn = nullptr;
+  const cudaError_t e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                        const_cast<void*>(base), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+long long prompt_items(const Params& p, int n_tokens) {
+  const int tokens = 2 * kTileRows / (p.Hq / p.Hkv);
+  return (long long)p.B * p.Hkv * ((n_tokens + tokens - 1) / tokens);
+}
+
+cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s) {
+  PromptParams pp{};
+  pp.p = p;
+  pp.n_tokens = n_tokens;
+  pp.sink = std::min(sink, 1 << 30);  // positions stay far below, so sums with these do too
+  pp.window = std::min(window, 1 << 30);
+  const int G = p.Hq / p.Hkv;
+  const int tokens = 2 * kTileRows / G;
+  pp.q_blocks = (n_tokens + tokens - 1) / tokens;
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * n_tokens};
+  const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
+  cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t kd[2] = {kHeadDim, (cuuint64_t)p.num_phys * p.Hkv * p.P};
+  const cuuint64_t ks[1] = {kHeadDim * 2};
+  const cuuint32_t kb[2] = {64, (cuuint32_t)p.P};
+  if ((e = make_map(&mk, p.k_pool, 2, kd, ks, kb)) != cudaSuccess) return e;
+  if ((e = make_map(&mv, p.v_pool, 2, kd, ks, kb)) != cudaSuccess) return e;
+  const void* fn = p.P == 16 ? (const void*)prompt_kernel<16> : (const void*)prompt_kernel<32>;
+  const size_t smem = PromptSmem::total + 1024;
+  if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
+  void* args[] = {&pp, &mq, &mk, &mv};
+  const long long ctas = prompt_items(p, n_tokens) * p.n_splits;
+  return launch_pdl(fn, dim3((unsigned)ctas), dim3(kPromptThreads), smem, s, args);
+}
+
+}  // namespace quest

@@ -360,6 +360,15 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
   sp.sink = sink_tokens;
   sp.window = window;
   sp.n_tokens = n_tokens;
+  if (n_tokens > 1) {
+    sp.p.q = static_cast<const __half*>(q);
+    sp.p.out = static_cast<__half*>(out);
+    sp.p.lse = lse;
+    sp.p.n_splits = 1;
+    return launched(launch_prompt(sp.p, n_tokens, sink_tokens, window,
+                                  static_cast<cudaStream_t>(stream)),
+                    what);
+  }
   return run_span(sp, false, window_pages(*cache, sink_tokens, window), opts, q, out, lse, stream,
                   what);
 }
