@@ -225,6 +225,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Packed fp32 pairs: one instruction for two lanes' worth of arithmetic.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int P>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
@@ -474,10 +499,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
         }
-        float top = s[0];
+        // four chains of three-input maxima: one chain of 127 would wait on itself
+        float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int k = 1; k < kTileTokens; ++k) top = fmaxf(top, s[k]);
-        top *= p.qscale;
+        for (int k = 4; k + 8 <= kTileTokens; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kTileTokens - 4 + e]);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float mn = fmaxf(m, top);
           const float f = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
@@ -496,20 +526,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
-        float sum = 0.f;
+        const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t w[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float a = ex2(fmaf(s[64 * u + 2 * k], p.qscale, shift));
-            const float c = ex2(fmaf(s[64 * u + 2 * k + 1], p.qscale, shift));
-            sum += a + c;
+            float a, c;
+            unpair(fma2(pair(s[64 * u + 2 * k], s[64 * u + 2 * k + 1]), scale2, shift2), a, c);
+            a = ex2(a);
+            c = ex2(c);
+            sum[k & 3] = add2(sum[k & 3], pair(a, c));
             w[k] = pack2(a, c);
           }
           tmem_st32(s_col + 32 * u, w);
         }
-        l += sum;
+        {
+          float a, c;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
+          l += a + c;
+        }
         tmem_wait_st();
         fence_before();
         __syncwarp();
