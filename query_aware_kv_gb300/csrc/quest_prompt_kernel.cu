@@ -197,6 +197,17 @@ __device__ __forceinline__ bool prompt_wait(const Params& p, uint64_t* bar, uint
   return mbar_try_wait(bar, parity) || prompt_wait_slow(p, bar, parity, give_up);
 }
 
+// One lane of the warp, the same one every time; the branch on it stays uniform for the
+// compiler, which keeps descriptors in uniform registers (behind `lane == 0` every product
+// took it about 90 cycles to issue, and a tile pair waited 4100 cycles for the issue warp).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 struct Bars {
   uint64_t q_full;
   uint64_t kv_full[kKvStages], kv_empty[kKvStages];
@@ -370,34 +381,40 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (warp == 9) {
     // ---- issue
     if (j1 > j0) {
-      const uint32_t q_addr = smem_u32(smem + PromptSmem::q);
-      const uint32_t kv_addr = smem_u32(smem + PromptSmem::kv);
+      const uint64_t q_desc = desc_k_major(smem_u32(smem + PromptSmem::q));
+      const uint64_t k_desc = desc_k_major(smem_u32(smem + PromptSmem::kv));
+      const uint64_t v_desc = desc_mn_major(smem_u32(smem + PromptSmem::kv));
+      // a descriptor's address field counts 16 bytes
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, prompt_wait(p, bar, parity, give_up)) != 0;
+      };
       auto qk = [&](int t, int st) {
-        if (lane == 0) {
+        if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint32_t o = (k >> 2) * kHalfBytes + (k & 3) * 32;
-            mma_ss(tmem + t * 128, desc_k_major(q_addr + t * kTileBytes + o),
-                   desc_k_major(kv_addr + st * kTileBytes + o), kIdescQK, k > 0);
+            const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+            mma_ss(tmem + t * 128, q_desc + (uint32_t)(t * (kTileBytes >> 4)) + o,
+                   k_desc + (uint32_t)(st * (kTileBytes >> 4)) + o, kIdescQK, k > 0);
           }
           commit(&bars.s_full[t]);
         }
         __syncwarp();
       };
-      bool ok = prompt_wait(p, &bars.q_full, 0, give_up);
-      int unit = 0;
-      ok = ok && prompt_wait(p, &bars.kv_full[0], 0, give_up);
+      auto release = [&](uint64_t* bar) {
+        if (elect_lane()) commit(bar);
+        __syncwarp();
+      };
+      bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
       fence_after();
       if (ok) {
-        for (int t = 0; t < n_q; ++t) qk(t, 0);
-        if (lane == 0) commit(&bars.kv_empty[0]);
+        qk(0, 0);
+        if (n_q > 1) qk(1, 0);
+        release(&bars.kv_empty[0]);
       }
-      unit = 1;
+      int sv = 1, sk = 2;              // stages of the V and the next K tile
+      uint32_t round_v = 0, round_k = 0;
       for (int j = j0; j < j1 && ok; ++j) {
-        const int sv = unit % kKvStages;
-        ok = prompt_wait(p, &bars.kv_full[sv], (unit / kKvStages) & 1, give_up);
-        if (!ok) break;
-        ++unit;
+        if (!(ok = wait(&bars.kv_full[sv], round_v & 1))) break;
         // Values that no row of the CTA sees (slots behind the last token, tokens between
         // the sinks and the first window) may be anything: 0 * NaN is not 0.
         const int i0 = j * PPT;
@@ -418,40 +435,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (touched) fence_proxy_async_smem();
           __syncwarp();
         }
-        const int sk = unit % kKvStages;
-        bool have_k = false;
-        for (int t = 0; t < n_q && ok; ++t) {
-          ok = prompt_wait(p, &bars.p_full[t], (j - j0) & 1, give_up);
-          if (!ok) break;
-          fence_after();
-          if (lane == 0) {
+        const bool more = j + 1 < j1;
 #pragma unroll
-            for (int k = 0; k < kTileTokens / 16; ++k)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                     desc_mn_major(kv_addr + sv * kTileBytes + k * 2048), kIdescPV,
-                     j > j0 || k > 0);
-            if (t == n_q - 1) commit(&bars.kv_empty[sv]);
-          }
-          __syncwarp();
-          if (j + 1 < j1) {
-            if (!have_k) {
-              ok = prompt_wait(p, &bars.kv_full[sk], (unit / kKvStages) & 1, give_up);
-              if (!ok) break;
-              have_k = true;
+        for (int t = 0; t < 2; ++t) {
+          if (t < n_q && ok) {
+            ok = wait(&bars.p_full[t], (j - j0) & 1);
+            if (ok) {
               fence_after();
+              if (elect_lane()) {
+#pragma unroll
+                for (int k = 0; k < kTileTokens / 16; ++k)
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                         v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2048 >> 4)), kIdescPV,
+                         j > j0 || k > 0);
+                if (t == n_q - 1) commit(&bars.kv_empty[sv]);
+                if (!more) commit(&bars.o_full[t]);
+              }
+              __syncwarp();
+              if (more) {
+                if (t == 0) {
+                  ok = wait(&bars.kv_full[sk], round_k & 1);
+                  fence_after();
+                }
+                if (ok) {
+                  qk(t, sk);
+                  if (t == n_q - 1) release(&bars.kv_empty[sk]);
+                }
+              }
             }
-            qk(t, sk);
-            if (t == n_q - 1 && lane == 0) commit(&bars.kv_empty[sk]);
-          } else if (lane == 0) {
-            commit(&bars.o_full[t]);
           }
-          __syncwarp();
         }
-        if (have_k) ++unit;
+        if ((sv += 2) >= kKvStages) {
+          sv -= kKvStages;
+          ++round_v;
+        }
+        if ((sk += 2) >= kKvStages) {
+          sk -= kKvStages;
+          ++round_k;
+        }
       }
       if (!ok) {  // products in flight finish before their memory goes
-        if (lane == 0) commit(&bars.drain);
-        __syncwarp();
+        release(&bars.drain);
         for (int i = 0; i < 1 << 20; ++i)
           if (mbar_try_wait(&bars.drain, 0)) break;
       }
