@@ -14,7 +14,7 @@
 //   P = 2^(S c - m + 8)  the tile's 128 softmax threads, one row each (no shuffles), written
 //                        back over S as fp16
 //   O += P V             tcgen05.mma, P from TMEM, V in shared memory (MN-major), O in TMEM
-// Warps 0-3 and 4-7 are the softmax of the two tiles, warp 8 fetches, warp 9 issues the
+// Warps 0-3 and 4-7 are the softmax of the two tiles, warps 8 and 10 fetch, warp 9 issues the
 // products: while one tile is in its softmax, the tensor core works for the other.  The order of
 // issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's columns.
 // The maximum m moves only when a row exceeds it by more than 2^6 (then O is rescaled in
@@ -37,8 +37,8 @@ namespace quest {
 
 namespace {
 
-// Three warpgroups: the softmax of either tile, and the fetch and issue warps (8 and 9; 10 and
-// 11 only hold their share of the registers).  Registers: 384 x 168 at launch, then 216 for
+// Three warpgroups: the softmax of either tile, and the fetch warps (8: Q and K, 10: V) with the
+// issue warp (9; 11 only holds its share of the registers).  Registers: 384 x 168 at launch, then 216 for
 // the softmax threads (a row of 128 scores each) and 72 for the others, the same total.
 constexpr int kPromptThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -135,12 +135,13 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y,
-                                       uint64_t* bar) {
+// One page of one kv head: 8-row groups `group` .. of the pool.
+__device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int group,
+                                         uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(group), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -152,16 +153,15 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
       : "memory");
 }
 
-// Shared-memory operand descriptors, 128-byte swizzle.  Rows of 128 B, 8 rows an atom of
-// 1 KiB.  K-major (Q, K): atoms 1 KiB apart along the rows.  MN-major (V, whose 64-dim spans
-// are kHalfBytes apart): atoms 1 KiB apart along the tokens.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(kHalfBytes >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory operand descriptors, 128-byte swizzle: atoms of 8 rows x 64 dims (1 KiB).
+// Q tile: the atoms of dims 0-63 of all rows, then those of dims 64-127, kHalfBytes apart.
+// K and V tiles: per 8 tokens the atoms of both halves of the dims side by side, so that a
+// whole page is one TMA box (two boxes a page took the fetch warp 3200 cycles per tile pair,
+// more than the products); 8-token groups are kGroupBytes apart.
+constexpr int kAtomBytes = 1024, kGroupBytes = 2 * kAtomBytes;
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // fp16 x fp16 -> fp32, 128 x 128 x 16; bit 16: B is MN-major.
 constexpr uint32_t kIdescQK = 1u << 4 | (kTileTokens >> 3) << 17 | (kTileRows >> 4) << 24;
@@ -328,63 +328,79 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
-    // ---- fetch: lane (slot, half) brings 64 dims of page `slot` of every tile
+    if (warp == 8 || warp == 10) {
+    // ---- fetch: warp 8 the queries and the K tiles, warp 10 the V tiles
     if (j1 > j0) {
-      if (lane < 2 * n_q) {
-        if (lane == 0) mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
+      const int kv = warp == 10;
+      if (kv == 0 && elect_lane()) {
+        mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
+        for (int i = 0; i < 2 * n_q; ++i)
+          tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
+                 64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
       }
       __syncwarp();
-      if (lane < 2 * n_q)
-        tma_3d(smem + PromptSmem::q + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &map_q,
-               64 * (lane & 1), g * G, b * n + tok0 + (lane >> 1) * TT, &bars.q_full);
-      const int slot = lane >> 1, half = lane & 1;
-      auto lookup = [&](int j) {
-        if (slot >= PPT) return 0;
+      // 32 pages of the list at a time, a page per lane, the next 32 on their way
+      auto lookup = [&](int i) {
         // slots behind the list's end repeat its last page (their tokens are hidden)
-        const int i = min(j * PPT + slot, list.count - 1);
-        const int lp = list.page(i);
-        int phys = p.block_table[(size_t)b * p.max_pages + lp];
+        const int lp = list.page(min(i, list.count - 1));
+        const int phys = p.block_table[(size_t)b * p.max_pages + lp];
         if (phys < 0 || phys >= p.num_phys) {
-          if (half == 0) record(p, QUEST_ERR_BAD_PAGE, b, lp);
-          phys = 0;
+          record(p, QUEST_ERR_BAD_PAGE, b, lp);
+          return 0;
         }
         return phys;
       };
-      int unit = 0;  // K and V tiles fetched so far
-      int next = lookup(j0);
+      int now = lookup(j0 * PPT + lane), next = lookup(j0 * PPT + 32 + lane);
+      int st = kv;
+      uint32_t round = 0;
       bool ok = true;
-      for (int j = j0; j < j1 && ok; ++j) {
-        const int phys = next;
-        if (j + 1 < j1) next = lookup(j + 1);
-        const int y = (phys * p.Hkv + g) * P;
-        for (int kv = 0; kv < 2; ++kv, ++unit) {
-          const int st = unit % kKvStages, round = unit / kKvStages;
-          if (round > 0 && !prompt_wait(p, &bars.kv_empty[st], (round - 1) & 1, give_up)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
-          __syncwarp();
-          if (slot < PPT)
-            tma_2d(smem + PromptSmem::kv + st * kTileBytes + half * kHalfBytes + slot * P * 128,
-                   kv ? &map_v : &map_k, 64 * half, y, &bars.kv_full[st]);
+      int fetched = 0;
+      for (int j = j0; j < j1; ++j) {
+        const int at = (j - j0) * PPT & 31;
+        if (at == 0 && j > j0) {
+          now = next;
+          next = lookup(j * PPT + 32 + lane);
+        }
+        if (round > 0 &&
+            !__all_sync(0xffffffffu,
+                        prompt_wait(p, &bars.kv_empty[st], (round - 1) & 1, give_up))) {
+          ok = false;
+          break;
+        }
+        const bool leader = elect_lane();
+        if (leader) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
+#pragma unroll
+        for (int e = 0; e < PPT; ++e) {
+          const int phys = __shfl_sync(0xffffffffu, now, at + e);
+          if (leader)
+            tma_page(smem + PromptSmem::kv + st * kTileBytes + e * P * kHeadDim * 2,
+                     kv ? &map_v : &map_k, (phys * p.Hkv + g) * (P / 8), &bars.kv_full[st]);
+        }
+        __syncwarp();
+        ++fetched;
+        if ((st += 2) >= kKvStages) {
+          st -= kKvStages;
+          ++round;
         }
       }
-      if (!ok) {  // leave only when every copy has landed
+      if (!ok) {  // leave only when every copy of this warp has landed
         prompt_wait(p, &bars.q_full, 0, give_up);
-        for (int u = max(0, unit - kKvStages); u < unit; ++u)
+        for (int f = max(0, fetched - kKvStages); f < fetched; ++f) {
+          const int u = 2 * f + kv;
           for (int i = 0; i < 1 << 20; ++i)
             if (mbar_try_wait(&bars.kv_full[u % kKvStages], (u / kKvStages) & 1)) break;
+        }
       }
     }
   } else if (warp == 9) {
     // ---- issue
     if (j1 > j0) {
-      const uint64_t q_desc = desc_k_major(smem_u32(smem + PromptSmem::q));
-      const uint64_t k_desc = desc_k_major(smem_u32(smem + PromptSmem::kv));
-      const uint64_t v_desc = desc_mn_major(smem_u32(smem + PromptSmem::kv));
-      // a descriptor's address field counts 16 bytes
+      // Q and K are K-major: the stride is that of 8-row groups.  V is MN-major: the lead is
+      // that of its 64-dim spans, the stride that of 8-token groups.  Address fields count
+      // 16 bytes.
+      const uint64_t q_desc = smem_desc(smem_u32(smem + PromptSmem::q), 16, kAtomBytes);
+      const uint64_t k_desc = smem_desc(smem_u32(smem + PromptSmem::kv), 16, kGroupBytes);
+      const uint64_t v_desc = smem_desc(smem_u32(smem + PromptSmem::kv), kAtomBytes, kGroupBytes);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, prompt_wait(p, bar, parity, give_up)) != 0;
       };
@@ -392,9 +408,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-            mma_ss(tmem + t * 128, q_desc + (uint32_t)(t * (kTileBytes >> 4)) + o,
-                   k_desc + (uint32_t)(st * (kTileBytes >> 4)) + o, kIdescQK, k > 0);
+            const uint32_t oq = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+            const uint32_t ok = ((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4;
+            mma_ss(tmem + t * 128, q_desc + (uint32_t)(t * (kTileBytes >> 4)) + oq,
+                   k_desc + (uint32_t)(st * (kTileBytes >> 4)) + ok, kIdescQK, k > 0);
           }
           commit(&bars.s_full[t]);
         }
@@ -428,7 +445,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 *reinterpret_cast<uint4*>(smem + PromptSmem::kv + sv * kTileBytes +
-                                          (e >> 3) * kHalfBytes + c * 128 + (e & 7) * 16) =
+                                          (c >> 3) * kGroupBytes + (e >> 3) * kAtomBytes +
+                                          (c & 7) * 128 + (e & 7) * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
             }
           }
@@ -446,7 +464,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kTileTokens / 16; ++k)
                   mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                         v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2048 >> 4)), kIdescPV,
+                         v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)), kIdescPV,
                          j > j0 || k > 0);
                 if (t == n_q - 1) commit(&bars.kv_empty[sv]);
                 if (!more) commit(&bars.o_full[t]);
@@ -639,13 +657,13 @@ cudaError_t encode_fn(EncodeFn* fn) {
   return cudaSuccess;
 }
 
-// A map of fp16 rows of 128: boxes of 64 dims (a 128-byte swizzle span) x the given rows.
+// A map of fp16 boxes whose inner 64 dims are a 128-byte swizzle span.
 cudaError_t make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
                      const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeFn fn = nullptr;
   const cudaError_t e = encode_fn(&fn);
   if (e != cudaSuccess) return e;
-  const cuuint32_t one[3] = {1, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
                         const_cast<void*>(base), dims, strides, box, one,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -675,11 +693,12 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
   cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
   if (e != cudaSuccess) return e;
-  const cuuint64_t kd[2] = {kHeadDim, (cuuint64_t)p.num_phys * p.Hkv * p.P};
-  const cuuint64_t ks[1] = {kHeadDim * 2};
-  const cuuint32_t kb[2] = {64, (cuuint32_t)p.P};
-  if ((e = make_map(&mk, p.k_pool, 2, kd, ks, kb)) != cudaSuccess) return e;
-  if ((e = make_map(&mv, p.v_pool, 2, kd, ks, kb)) != cudaSuccess) return e;
+  // a pool as [8-row group][half of the dims][row][64 dims]
+  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
+  const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
+  const cuuint32_t kb[4] = {64, 8, 2, (cuuint32_t)(p.P / 8)};
+  if ((e = make_map(&mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
+  if ((e = make_map(&mv, p.v_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
   const void* fn = p.P == 16 ? (const void*)prompt_kernel<16> : (const void*)prompt_kernel<32>;
   const size_t smem = PromptSmem::total + 1024;
   if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
