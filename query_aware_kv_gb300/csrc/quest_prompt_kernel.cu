@@ -14,8 +14,8 @@
 //   P = 2^(S c - m + 8)  the tile's 128 softmax threads, one row each (no shuffles), written
 //                        back over S as fp16
 //   O += P V             tcgen05.mma, P from TMEM, V in shared memory (MN-major), O in TMEM
-// Warps 0-3 and 4-7 are the softmax of the two tiles, warps 8 and 10 fetch, warp 9 issues the
-// products: while one tile is in its softmax, the tensor core works for the other.  The order of
+// Warps 0-3 and 4-7 are the softmax of the two tiles, warps 8 and 10 fetch, warps 9 and 11 issue the
+// products of a tile each: while one tile is in its softmax, the tensor core works for the other.  The order of
 // issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's columns.
 // The maximum m moves only when a row exceeds it by more than 2^6 (then O is rescaled in
 // TMEM by the softmax threads themselves), so weights reach 2^14 at most and keep fp16's full
@@ -38,7 +38,7 @@ namespace quest {
 namespace {
 
 // Three warpgroups: the softmax of either tile, and the fetch warps (8: Q and K, 10: V) with the
-// issue warp (9; 11 only holds its share of the registers).  Registers: 384 x 168 at launch, then 216 for
+// issue warps (9 and 11, a query tile each).  Registers: 384 x 168 at launch, then 216 for
 // the softmax threads (a row of 128 scores each) and 72 for the others, the same total.
 constexpr int kPromptThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -210,8 +210,10 @@ __device__ __forceinline__ bool elect_lane() {
 
 struct Bars {
   uint64_t q_full;
-  uint64_t kv_full[kKvStages], kv_empty[kKvStages];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t kv_full[kKvStages];
+  // S of query tile t and K / V tile j is in s_full[t][j & 1]; its completion also says that
+  // Q K^T (t, j) and P V (t, j - 1) have read their K and V tiles
+  uint64_t s_full[2][2], p_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int give_up;
 };
@@ -279,14 +281,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(&bars.q_full, 1);
     for (int i = 0; i < kKvStages; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.s_full[t][0], 1);
+      mbar_init(&bars.s_full[t][1], 1);
+      mbar_init(&bars.drain[t], 1);
       mbar_init(&bars.p_full[t], 4);
       mbar_init(&bars.o_full[t], 1);
     }
-    mbar_init(&bars.drain, 1);
     bars.give_up = 0;
     fence_mbar_init();
   }
@@ -352,7 +354,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       int now = lookup(j0 * PPT + lane), next = lookup(j0 * PPT + 32 + lane);
       int st = kv;
-      uint32_t round = 0;
       bool ok = true;
       int fetched = 0;
       for (int j = j0; j < j1; ++j) {
@@ -361,11 +362,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           now = next;
           next = lookup(j * PPT + 32 + lane);
         }
-        if (round > 0 &&
-            !__all_sync(0xffffffffu,
-                        prompt_wait(p, &bars.kv_empty[st], (round - 1) & 1, give_up))) {
-          ok = false;
-          break;
+        // K (j) takes the stage of V (j - 3), V (j) that of K (j - 2): both are free once
+        // the scores of tile j - 2 are there
+        if (j - j0 >= 2) {
+          const uint32_t ph = (uint32_t)((j - j0 - 2) >> 1) & 1;
+          bool free = prompt_wait(p, &bars.s_full[0][(j - j0) & 1], ph, give_up);
+          if (n_q > 1) free = free && prompt_wait(p, &bars.s_full[1][(j - j0) & 1], ph, give_up);
+          if (!__all_sync(0xffffffffu, free)) {
+            ok = false;
+            break;
+          }
         }
         const bool leader = elect_lane();
         if (leader) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
@@ -378,10 +384,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
         ++fetched;
-        if ((st += 2) >= kKvStages) {
-          st -= kKvStages;
-          ++round;
-        }
+        if ((st += 2) >= kKvStages) st -= kKvStages;
       }
       if (!ok) {  // leave only when every copy of this warp has landed
         prompt_wait(p, &bars.q_full, 0, give_up);
@@ -392,48 +395,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
     }
-  } else if (warp == 9) {
-    // ---- issue
-    if (j1 > j0) {
+  } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
+    // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
+    // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
+    // other tile's products fill those.)
+    {
+      const int t = warp == 11;
       // Q and K are K-major: the stride is that of 8-row groups.  V is MN-major: the lead is
       // that of its 64-dim spans, the stride that of 8-token groups.  Address fields count
       // 16 bytes.
-      const uint64_t q_desc = smem_desc(smem_u32(smem + PromptSmem::q), 16, kAtomBytes);
+      const uint64_t q_desc =
+          smem_desc(smem_u32(smem + PromptSmem::q) + t * kTileBytes, 16, kAtomBytes);
       const uint64_t k_desc = smem_desc(smem_u32(smem + PromptSmem::kv), 16, kGroupBytes);
       const uint64_t v_desc = smem_desc(smem_u32(smem + PromptSmem::kv), kAtomBytes, kGroupBytes);
+      const uint32_t s_mem = tmem + t * 128, o_mem = tmem + 256 + t * 128;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, prompt_wait(p, bar, parity, give_up)) != 0;
       };
-      auto qk = [&](int t, int st) {
+      auto qk = [&](int st, uint64_t* done) {
         if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k) {
             const uint32_t oq = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
             const uint32_t ok = ((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4;
-            mma_ss(tmem + t * 128, q_desc + (uint32_t)(t * (kTileBytes >> 4)) + oq,
-                   k_desc + (uint32_t)(st * (kTileBytes >> 4)) + ok, kIdescQK, k > 0);
+            mma_ss(s_mem, q_desc + oq, k_desc + (uint32_t)(st * (kTileBytes >> 4)) + ok, kIdescQK,
+                   k > 0);
           }
-          commit(&bars.s_full[t]);
+          commit(done);
         }
-        __syncwarp();
-      };
-      auto release = [&](uint64_t* bar) {
-        if (elect_lane()) commit(bar);
         __syncwarp();
       };
       bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
       fence_after();
-      if (ok) {
-        qk(0, 0);
-        if (n_q > 1) qk(1, 0);
-        release(&bars.kv_empty[0]);
-      }
-      int sv = 1, sk = 2;              // stages of the V and the next K tile
+      if (ok) qk(0, &bars.s_full[t][0]);
+      int sv = 1, sk = 2;  // stages of the V and the next K tile
       uint32_t round_v = 0, round_k = 0;
       for (int j = j0; j < j1 && ok; ++j) {
-        if (!(ok = wait(&bars.kv_full[sv], round_v & 1))) break;
+        const bool more = j + 1 < j1;
+        ok = wait(&bars.kv_full[sv], round_v & 1) &&
+             (!more || wait(&bars.kv_full[sk], round_k & 1));
+        if (!ok) break;
         // Values that no row of the CTA sees (slots behind the last token, tokens between
-        // the sinks and the first window) may be anything: 0 * NaN is not 0.
+        // the sinks and the first window) may be anything: 0 * NaN is not 0.  (Both issue
+        // warps store these zeros, each before its own products.)
         const int i0 = j * PPT;
         if (i0 <= list.n_sink || (j + 1) * PPT >= list.count) {
           bool touched = false;
@@ -453,36 +457,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (touched) fence_proxy_async_smem();
           __syncwarp();
         }
-        const bool more = j + 1 < j1;
+        if (!(ok = wait(&bars.p_full[t], (j - j0) & 1))) break;
+        fence_after();
+        if (elect_lane()) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t < n_q && ok) {
-            ok = wait(&bars.p_full[t], (j - j0) & 1);
-            if (ok) {
-              fence_after();
-              if (elect_lane()) {
-#pragma unroll
-                for (int k = 0; k < kTileTokens / 16; ++k)
-                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                         v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)), kIdescPV,
-                         j > j0 || k > 0);
-                if (t == n_q - 1) commit(&bars.kv_empty[sv]);
-                if (!more) commit(&bars.o_full[t]);
-              }
-              __syncwarp();
-              if (more) {
-                if (t == 0) {
-                  ok = wait(&bars.kv_full[sk], round_k & 1);
-                  fence_after();
-                }
-                if (ok) {
-                  qk(t, sk);
-                  if (t == n_q - 1) release(&bars.kv_empty[sk]);
-                }
-              }
-            }
-          }
+          for (int k = 0; k < kTileTokens / 16; ++k)
+            mma_ts(o_mem, s_mem + 8 * k,
+                   v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)),
+                   kIdescPV, j > j0 || k > 0);
+          if (!more) commit(&bars.o_full[t]);
         }
+        __syncwarp();
+        if (more) qk(sk, &bars.s_full[t][(j - j0 + 1) & 1]);
         if ((sv += 2) >= kKvStages) {
           sv -= kKvStages;
           ++round_v;
@@ -493,9 +479,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       if (!ok) {  // products in flight finish before their memory goes
-        release(&bars.drain);
+        if (elect_lane()) commit(&bars.drain[t]);
+        __syncwarp();
         for (int i = 0; i < 1 << 20; ++i)
-          if (mbar_try_wait(&bars.drain, 0)) break;
+          if (mbar_try_wait(&bars.drain[t], 0)) break;
       }
     }
   }
@@ -513,7 +500,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (t < n_q) {
       const int r0 = pos0 + tok0 + t * TT, r1 = min(r0 + TT, end) - 1;
       for (int j = j0; j < j1; ++j) {
-        ok = prompt_wait(p, &bars.s_full[t], (j - j0) & 1, give_up);
+        ok = prompt_wait(p, &bars.s_full[t][(j - j0) & 1], (uint32_t)((j - j0) >> 1) & 1, give_up);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
