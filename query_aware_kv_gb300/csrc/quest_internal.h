@@ -221,9 +221,12 @@ int span_splits(bool narrow, long long rows, int pages, int user_pps, int page_s
 // The most partials (rows * splits) that a launch of up to `rows` rows can write.
 long long span_max_parts(bool narrow, long long rows, int pages, int user_pps, int page_size);
 cudaError_t launch_span(const SpanParams& sp, bool narrow, cudaStream_t s);
-// Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu);
-// p.n_splits work items per 256 query rows, prompt_items of them without splits.
-long long prompt_items(const Params& p, int n_tokens);
+// Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
+// p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of
+// part_ml / part_acc each; splits only while items * splits is at most kPromptParts.
+constexpr int kPromptParts = 304;
+int prompt_part_rows(int G, int n_tokens);
+int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps);
 cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s);
 cudaError_t launch_narrow_prefill(const Params& p, const NarrowPtrs& nar, const __half* k,
                                   const __half* v, int n, cudaStream_t s);

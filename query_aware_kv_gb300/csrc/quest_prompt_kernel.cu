@@ -37,12 +37,12 @@ namespace quest {
 
 namespace {
 
-// Three warpgroups: the softmax of either tile, and the fetch warps (8: Q and K, 10: V) with the
-// issue warps (9 and 11, a query tile each).  Registers: 384 x 168 at launch, then 216 for
-// the softmax threads (a row of 128 scores each) and 72 for the others, the same total.
-constexpr int kPromptThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of the launch");
+// Five warpgroups: two for the softmax of either tile, and the fetch warps (16: Q and K, 18: V)
+// with the issue warps (17 and 19, a query tile each).  Registers: 640 x 96 at launch, then
+// 104 for the softmax threads (64 scores each) and 64 for the others, the same total.
+constexpr int kPromptThreads = 640;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * 96, "registers of the launch");
 constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
@@ -55,14 +55,16 @@ struct PromptSmem {
   static constexpr int q = 0;                             // [2][32 KiB]
   static constexpr int kv = 2 * kTileBytes;               // [kKvStages][32 KiB]
   static constexpr int bars = kv + kKvStages * kTileBytes;
-  static constexpr int total = bars + 256;
+  static constexpr int top = bars + 256;                  // [2][128]: running row maxima
+  static constexpr int total = top + 2 * kTileRows * 4;
 };
 static_assert(PromptSmem::total + 1024 <= (int)kMaxSmem, "shared memory of a CTA");
 
 struct PromptParams {
   Params p;
   int n_tokens, sink, window;
-  int q_blocks;  // CTAs along the tokens of a (sequence, kv head)
+  int log_g;     // log2 of the group size
+  int part_rows; // rows of a work item that partials have room for
 };
 
 // ---- tcgen05 / TMA
@@ -97,11 +99,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 // The same with A in TMEM.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+                                       uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
 #define QUEST_R8(a, i) a[i], a[i + 1], a[i + 2], a[i + 3], a[i + 4], a[i + 5], a[i + 6], a[i + 7]
@@ -179,13 +181,17 @@ __device__ __forceinline__ void record(const Params& p, int code, int b, int pag
 }
 __device__ __forceinline__ bool prompt_wait_slow(const Params& p, uint64_t* bar, uint32_t parity,
                                               volatile int* give_up) {
-  const long long t0 = global_ns();
+  // the clock is read only after many polls: reading it first made every wait that was not
+  // over yet several hundred cycles longer
+  long long t0 = 0;
   while (true) {
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 1024; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*give_up) return false;
-    if (global_ns() - t0 > p.wait_limit_ns) {
+    const long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > p.wait_limit_ns) {
       *give_up = 1;
       record(p, QUEST_ERR_TIMEOUT, -1, -1);
       return false;
@@ -216,6 +222,7 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int give_up;
+  int word[2][3];  // any_of_tile
 };
 static_assert(sizeof(Bars) <= 256, "barrier area");
 
@@ -226,6 +233,59 @@ struct PageList {
   __device__ __forceinline__ int page(int i) const { return i < n_sink ? i : first + i - n_sink; }
 };
 
+// The rows of a query tile (positions r0 .. r1) against a K / V tile that starts at list
+// entry i0: none of its tokens is visible to any row, or all are to every row.
+struct TileRows {
+  int r0, r1, window, sink, n_sink, first, count;
+  template <int P>
+  __device__ __forceinline__ int base(int i0) const { return (first + i0 - n_sink) * P; }
+  template <int P>
+  __device__ __forceinline__ bool none(int i0) const {
+    return i0 >= n_sink &&
+           (base<P>(i0) > r1 ||
+            (base<P>(i0) >= sink && base<P>(i0) + kTileTokens - 1 <= r0 - window));
+  }
+  template <int P>
+  __device__ __forceinline__ bool all(int i0) const {
+    return i0 >= n_sink && i0 + kTileTokens / P <= count && base<P>(i0) + kTileTokens - 1 <= r0 &&
+           (base<P>(i0) > r1 - window || base<P>(i0) + kTileTokens <= sink);
+  }
+};
+
+// Where split s of this CTA's work item keeps its rows' shares.
+__device__ __forceinline__ size_t part_slot(const PromptParams& pp, int s) {
+  const unsigned blocks = gridDim.x / (unsigned)pp.p.n_splits;
+  const unsigned blk = (gridDim.x - 1 - blockIdx.x) / (unsigned)pp.p.n_splits;
+  const size_t item = ((size_t)blockIdx.z * pp.p.Hkv + blockIdx.y) * blocks + blk;
+  return (item * pp.p.n_splits + s) * pp.part_rows;
+}
+
+// The 256 softmax threads of tile t meet.
+__device__ __forceinline__ void sync_tile(int t) {
+  __syncwarp();
+  __barrier_sync_count(1 + t, 2 * kTileRows);
+}
+// Whether any of them says so.  `word`: the tile's for this place in the code, in shared memory;
+// `round`: the place's count, from 1.  (A warp cannot come to a place again, and write its
+// word, before every other one has read it: in between all meet elsewhere, or wait for scores
+// that need every warp's weights.)
+__device__ __forceinline__ bool any_of_tile(int t, bool x, volatile int* word, int round) {
+  if (__any_sync(0xffffffffu, x)) *word = round;
+  sync_tile(t);
+  return *word == round;
+}
+
+// A float as an int of the same order, and back.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// The lowest x bits (0 <= x <= 32).
+__device__ __forceinline__ uint32_t low_bits(int x) { return (uint32_t)((1ull << x) - 1ull); }
 // A weight row's threads: 128 scores to weights.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -275,7 +335,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Bars& bars = *reinterpret_cast<Bars*>(smem + PromptSmem::bars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.Hq / p.Hkv, TT = kTileRows / G;  // tokens of a query tile
+  const int lg = pp.log_g, G = 1 << lg, TT = kTileRows >> lg;  // tokens of a query tile
 
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
@@ -286,13 +346,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&bars.s_full[t][0], 1);
       mbar_init(&bars.s_full[t][1], 1);
       mbar_init(&bars.drain[t], 1);
-      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.p_full[t], 8);
       mbar_init(&bars.o_full[t], 1);
     }
     bars.give_up = 0;
+    for (int i = 0; i < 6; ++i) bars.word[i / 3][i % 3] = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&bars.tmem);
+  if (threadIdx.x < 2 * kTileRows)
+    reinterpret_cast<int*>(smem + PromptSmem::top)[threadIdx.x] = ordered(-CUDART_INF_F);
+  if (warp == 17) tmem_alloc(&bars.tmem);
+  if (warp == 16 && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v)
+                 : "memory");
   fence_before();
   __syncthreads();
   fence_after();
@@ -302,13 +368,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_trigger();
 
   // ---- the CTA's work
-  const int split = (int)(blockIdx.x % (unsigned)p.n_splits);
-  const unsigned item = blockIdx.x / (unsigned)p.n_splits;  // (b * Hkv + g) * q_blocks + block
-  const int blk = pp.q_blocks - 1 - (int)(item % (unsigned)pp.q_blocks);
-  const int bg = (int)(item / (unsigned)pp.q_blocks);
-  const int b = bg / p.Hkv, g = bg % p.Hkv;
+  const int split = (int)blockIdx.x % p.n_splits;
+  const int blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
+  const int g = (int)blockIdx.y, b = (int)blockIdx.z;
   const int n = pp.n_tokens, tok0 = blk * 2 * TT;
   const int tok1 = min(n, tok0 + 2 * TT);
+  const int n_q = tok1 - tok0 > TT ? 2 : 1;  // query tiles with rows
+  if (warp == 16 && elect_lane()) {  // the queries' place does not depend on the length
+    mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
+    for (int i = 0; i < 2 * n_q; ++i)
+      tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
+             64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
+  }
+  __syncwarp();
   int L = p.seq_lens[b];
   if (L < 0 || (long long)L > (long long)p.max_pages * P) {
     if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
@@ -326,41 +398,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int tiles = (list.count + PPT - 1) / PPT;
   const int j0 = (int)((long long)tiles * split / p.n_splits);
   const int j1 = (int)((long long)tiles * (split + 1) / p.n_splits);
-  const int n_q = tok1 - tok0 > TT ? 2 : 1;  // query tiles with rows
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8 || warp == 10) {
-    // ---- fetch: warp 8 the queries and the K tiles, warp 10 the V tiles
+    if (warp == 16 || warp == 18) {
+    // ---- fetch: warp 16 the K tiles (the queries are on their way), warp 18 the V tiles
+    const int kv = warp == 18;
     if (j1 > j0) {
-      const int kv = warp == 10;
-      if (kv == 0 && elect_lane()) {
-        mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
-        for (int i = 0; i < 2 * n_q; ++i)
-          tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
-                 64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
-      }
-      __syncwarp();
-      // 32 pages of the list at a time, a page per lane, the next 32 on their way
-      auto lookup = [&](int i) {
-        // slots behind the list's end repeat its last page (their tokens are hidden)
-        const int lp = list.page(min(i, list.count - 1));
-        const int phys = p.block_table[(size_t)b * p.max_pages + lp];
-        if (phys < 0 || phys >= p.num_phys) {
-          record(p, QUEST_ERR_BAD_PAGE, b, lp);
-          return 0;
-        }
-        return phys;
+      // 32 pages of the list at a time, a page per lane, the next 32 on their way; entries
+      // behind the list's end repeat its last page (their tokens are hidden)
+      auto entry = [&](int i) {
+        return p.block_table[(size_t)b * p.max_pages + list.page(min(i, list.count - 1))];
       };
-      int now = lookup(j0 * PPT + lane), next = lookup(j0 * PPT + 32 + lane);
+      auto checked = [&](int phys, int i) {
+        if (phys >= 0 && phys < p.num_phys) return phys;
+        record(p, QUEST_ERR_BAD_PAGE, b, list.page(min(i, list.count - 1)));
+        return 0;
+      };
+      int now = entry(j0 * PPT + lane), next = entry(j0 * PPT + 32 + lane);
+      now = checked(now, j0 * PPT + lane);
       int st = kv;
       bool ok = true;
       int fetched = 0;
       for (int j = j0; j < j1; ++j) {
         const int at = (j - j0) * PPT & 31;
         if (at == 0 && j > j0) {
-          now = next;
-          next = lookup(j * PPT + 32 + lane);
+          now = checked(next, j * PPT + lane);
+          next = entry(j * PPT + 32 + lane);
         }
         // K (j) takes the stage of V (j - 3), V (j) that of K (j - 2): both are free once
         // the scores of tile j - 2 are there
@@ -387,7 +451,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if ((st += 2) >= kKvStages) st -= kKvStages;
       }
       if (!ok) {  // leave only when every copy of this warp has landed
-        prompt_wait(p, &bars.q_full, 0, give_up);
         for (int f = max(0, fetched - kKvStages); f < fetched; ++f) {
           const int u = 2 * f + kv;
           for (int i = 0; i < 1 << 20; ++i)
@@ -395,12 +458,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
     }
-  } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
-    // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
+    // (the queries too: no product waits for them where no token is visible)
+    if (kv == 0)
+      for (int i = 0; i < 1 << 20; ++i)
+        if (mbar_try_wait(&bars.q_full, 0)) break;
+  } else if (warp - 17 < 2 * n_q - 1 && j1 > j0) {
+    // ---- issue: warp 17 the products of query tile 0, warp 19 those of tile 1.  (One warp for
     // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
     // other tile's products fill those.)
     {
-      const int t = warp == 11;
+      const int t = warp == 19;
       // Q and K are K-major: the stride is that of 8-row groups.  V is MN-major: the lead is
       // that of its 64-dim spans, the stride that of 8-token groups.  Address fields count
       // 16 bytes.
@@ -412,8 +479,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, prompt_wait(p, bar, parity, give_up)) != 0;
       };
-      auto qk = [&](int st, uint64_t* done) {
-        if (elect_lane()) {
+      const int r0 = pos0 + tok0 + t * TT;
+      const TileRows rows{r0, min(r0 + TT, end) - 1, pp.window, pp.sink,
+                          list.n_sink, list.first, list.count};
+      // (a tile that no row sees only passes its barriers on; the branches around the elected
+      // lane's products depend on nothing but uniform values)
+      auto qk = [&](int st, bool live, uint64_t* done) {
+        if (!live) {
+          if (elect_lane()) commit(done);
+        } else if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k) {
             const uint32_t oq = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
@@ -427,7 +501,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
       fence_after();
-      if (ok) qk(0, &bars.s_full[t][0]);
+      bool live = !rows.none<P>(j0 * PPT);
+      uint32_t started = 0;
+      if (ok) qk(0, live, &bars.s_full[t][0]);
       int sv = 1, sk = 2;  // stages of the V and the next K tile
       uint32_t round_v = 0, round_k = 0;
       for (int j = j0; j < j1 && ok; ++j) {
@@ -459,16 +535,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (!(ok = wait(&bars.p_full[t], (j - j0) & 1))) break;
         fence_after();
-        if (elect_lane()) {
+        if (live) {
+          if (elect_lane()) {
 #pragma unroll
-          for (int k = 0; k < kTileTokens / 16; ++k)
-            mma_ts(o_mem, s_mem + 8 * k,
-                   v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)),
-                   kIdescPV, j > j0 || k > 0);
-          if (!more) commit(&bars.o_full[t]);
+            for (int k = 0; k < kTileTokens / 16; ++k)
+              mma_ts(o_mem, s_mem + 8 * k,
+                     v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)),
+                     kIdescPV, k > 0 ? 1u : started);
+          }
+          started = 1;
         }
         __syncwarp();
-        if (more) qk(sk, &bars.s_full[t][(j - j0 + 1) & 1]);
+        if (more) {
+          live = !rows.none<P>((j + 1) * PPT);
+          qk(sk, live, &bars.s_full[t][(j - j0 + 1) & 1]);
+        } else if (elect_lane()) {
+          commit(&bars.o_full[t]);
+        }
+        __syncwarp();
         if ((sv += 2) >= kKvStages) {
           sv -= kKvStages;
           ++round_v;
@@ -487,138 +571,249 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   }
   } else {
-    // ---- softmax: thread = row of its tile
+    // ---- softmax: two threads a row, 64 of a tile's tokens (and of O's dims) each
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int t = warp >> 2, row = threadIdx.x & 127;
-    const int tok = tok0 + t * TT + row / G;
+    const int t = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
+    const int tok = tok0 + t * TT + (row >> lg);
     const int pr = pos0 + tok;  // the row's position
-    const bool mine = tok < tok1;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + 256 + t * 128;
-    float m = -CUDART_INF_F, l = 0.f;
-    bool ok = true;
+    const uint32_t s_col = tmem + lanes + t * 128 + 64 * half;
+    const uint32_t p_col = tmem + lanes + t * 128 + 32 * half;
+    const uint32_t o_col = tmem + lanes + 256 + t * 128 + 64 * half;
+    int* my_top = reinterpret_cast<int*>(smem + PromptSmem::top) + t * kTileRows + row;
+    volatile int* word = bars.word[t];
+    float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens
+    bool ok = true, started = false;
     if (t < n_q) {
-      const int r0 = pos0 + tok0 + t * TT, r1 = min(r0 + TT, end) - 1;
+      const int r0 = pos0 + tok0 + t * TT;
+      const TileRows rows{r0, min(r0 + TT, end) - 1, pp.window, pp.sink,
+                          list.n_sink, list.first, list.count};
       for (int j = j0; j < j1; ++j) {
-        ok = prompt_wait(p, &bars.s_full[t][(j - j0) & 1], (uint32_t)((j - j0) >> 1) & 1, give_up);
-        if (!__all_sync(0xffffffffu, ok)) {
+        ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(j - j0) & 1],
+                                                 (uint32_t)((j - j0) >> 1) & 1, give_up));
+        const int i0 = j * PPT;
+        if (!rows.none<P>(i0)) {
+          fence_after();
+          if (!rows.all<P>(i0)) {
+            // Hidden tokens' scores become -inf in TMEM before the common path (a mask inside
+            // it costs every tile the registers and the order of its instructions).  32
+            // tokens at a time as bits: page by page those up to the row's own position that
+            // are in its window or among the sinks.
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t x[32], bits = 0;
+              tmem_ld32(s_col + 32 * u, x);
+#pragma unroll
+              for (int e = 0; e < 32 / P; ++e) {
+                const int i = i0 + (2 * half + u) * (32 / P) + e, at = list.page(i) * P;
+                const int hi = min(max(pr + 1 - at, 0), P);
+                const int lo = min(max(pr + 1 - pp.window - at, 0), P);
+                const int sk = min(max(pp.sink - at, 0), P);
+                const uint32_t b32 = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
+                bits |= (i < list.count ? b32 : 0u) << (P * e & 31);
+              }
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(bits & 1u << k)) x[k] = 0xff800000u;
+              tmem_st32(s_col + 32 * u, x);
+            }
+            tmem_wait_st();
+          }
+          uint32_t w[32];
+          float top, sum;
+          // this thread's 64 scores: their maximum, and their weights against m
+          auto weigh = [&]() {
+            float s[64];
+            tmem_ld32(s_col, reinterpret_cast<uint32_t*>(s));
+            tmem_ld32(s_col + 32, reinterpret_cast<uint32_t*>(s) + 32);
+            tmem_wait_ld();
+            const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
+            const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
+            uint64_t z[4] = {0, 0, 0, 0};
+            // four chains of three-input maxima: one chain of 63 would wait on itself
+            float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k + 8 <= 64; k += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[60 + e]);
+            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float a, c;
+              unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, shift2), a, c);
+              a = ex2(a);
+              c = ex2(c);
+              z[k & 3] = add2(z[k & 3], pair(a, c));
+              w[k] = pack2(a, c);
+            }
+            float a, c;
+            unpair(add2(add2(z[0], z[1]), add2(z[2], z[3])), a, c);
+            sum = a + c;
+          };
+          // The weights are taken against the reference as it is; where a row of the tile
+          // exceeds it by 2^kLazy the tile's rows move theirs, l and O with them, and take the
+          // weights again.  P goes where S was, so no thread stores before all have loaded.
+          // (A thread that gave up takes the whole tile's threads along: they meet at barriers.)
+          weigh();
+          const bool over = __any_sync(0xffffffffu, top > m + kLazy);
+          if (any_of_tile(t, over | !ok, word, j - j0 + 1)) {
+            if (any_of_tile(t, !ok, word + 1, j - j0 + 1)) {
+              ok = false;
+              break;
+            }
+            atomicMax(my_top, ordered(top));  // of both halves; it never falls, like m
+            sync_tile(t);
+            const float mn = unordered(*reinterpret_cast<volatile int*>(my_top));
+            const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            weigh();
+            sync_tile(t);
+            if (started) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint32_t o[32];
+                tmem_ld32(o_col + 32 * u, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st32(o_col + 32 * u, o);
+              }
+            }
+          }
+          tmem_st32(p_col, w);
+          l += sum;
+          started = true;
+          tmem_wait_st();
+          fence_before();
+        } else if (any_of_tile(t, !ok, word + 1, j - j0 + 1)) {
           ok = false;
           break;
         }
-        fence_after();
-        float s[kTileTokens];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          tmem_ld32(s_col + 32 * u, reinterpret_cast<uint32_t*>(s) + 32 * u);
-        tmem_wait_ld();
-        const int i0 = j * PPT;
-        const int base = list.page(i0) * P;
-        const bool whole = i0 >= list.n_sink && i0 + PPT <= list.count &&
-                           base + kTileTokens - 1 <= r0 && base > r1 - pp.window;
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < PPT; ++e) {
-            const int i = i0 + e;
-            const int at = i < list.count ? list.page(i) * P : 0x3fffffff;
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-              const int pos = at + k;
-              if (!(pos <= pr && (pos < pp.sink || pos > pr - pp.window)))
-                s[e * P + k] = -CUDART_INF_F;
-            }
-          }
-        }
-        // four chains of three-input maxima: one chain of 127 would wait on itself
-        float t4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int k = 4; k + 8 <= kTileTokens; k += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kTileTokens - 4 + e]);
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float mn = fmaxf(m, top);
-          const float f = mn == -CUDART_INF_F ? 1.f : exp2f(m - mn);
-          m = mn;
-          l *= f;
-          if (j > j0) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t o[32];
-              tmem_ld32(o_col + 32 * u, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(o_col + 32 * u, o);
-            }
-          }
-        }
-        const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
-        const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float a, c;
-            unpair(fma2(pair(s[64 * u + 2 * k], s[64 * u + 2 * k + 1]), scale2, shift2), a, c);
-            a = ex2(a);
-            c = ex2(c);
-            sum[k & 3] = add2(sum[k & 3], pair(a, c));
-            w[k] = pack2(a, c);
-          }
-          tmem_st32(s_col + 32 * u, w);
-        }
-        {
-          float a, c;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
-          l += a + c;
-        }
-        tmem_wait_st();
-        fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[t]);
       }
-      if (j1 > j0 && ok) ok = prompt_wait(p, &bars.o_full[t], 0, give_up);
-      ok = __all_sync(0xffffffffu, ok);
+      // (where no product ran, the queries have to land before their space is used again)
+      if (ok)
+        ok = __all_sync(0xffffffffu, prompt_wait(p, j1 > j0 ? &bars.o_full[t] : &bars.q_full, 0,
+                                                 give_up));
+      ok = !any_of_tile(t, !ok, word + 2, 1);
       fence_after();
-      // ---- out = O / l
-      const size_t at = ((size_t)b * n + tok) * p.Hq + (size_t)g * G + row % G;
+      if (ok) {  // the halves' sums, through the query space
+        float* ls = reinterpret_cast<float*>(smem + PromptSmem::q + t * kTileBytes);
+        ls[half * kTileRows + row] = l;
+        sync_tile(t);
+        l = ls[row] + ls[kTileRows + row];
+        sync_tile(t);
+      }
       const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
-      if (ok) {
+      const bool mine = tok < tok1;
+      if (ok && p.n_splits == 1) {
+        // ---- out = O / l, through the tile's own query space (its products are done): half a
+        // row of 128 B per thread goes to shared memory, four of them at a time leave
+        const size_t row0 = ((size_t)b * n + tok0 + t * TT) * p.Hq + ((size_t)g << lg);
+        unsigned char* stage = smem + PromptSmem::q + t * kTileBytes + half * kHalfBytes;
         const float inv = none ? 0.f : 1.f / l;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
           uint32_t o[32];
-          if (j1 > j0) {
+          if (started) {
+            tmem_ld32(o_col + 32 * u, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = none ? 0u
+                          : pack2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                  __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + row * 128 + (((4 * u + e) ^ (row & 7)) << 4)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        if (mine && half == 0 && p.lse)
+          p.lse[row0 + (size_t)(row >> lg) * p.Hq + (row & (G - 1))] =
+              none ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.6931471805599453f;
+        __syncwarp();
+        const int c = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = (row & ~31) + 4 * i + (lane >> 3);
+          if (tok0 + t * TT + (r >> lg) < tok1)
+            *reinterpret_cast<uint4*>(
+                p.out + (row0 + (size_t)(r >> lg) * p.Hq + (r & (G - 1))) * kHeadDim + 64 * half +
+                8 * c) = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+      } else if (ok) {
+        // ---- a split's share: O, m and l as they are (the loads are the whole warp's)
+        const size_t slot = part_slot(pp, split) + t * kTileRows + row;
+        float* dst = p.part_acc + slot * kHeadDim + 64 * half;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t o[32];
+          if (started) {
             tmem_ld32(o_col + 32 * u, o);
             tmem_wait_ld();
           }
           if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim + 32 * u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = none ? 0u
-                            : pack2(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                    __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(dst + 32 * u + 4 * e) =
+                  started ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
+                          : make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (mine && p.lse)
-          p.lse[at] = none ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.6931471805599453f;
+        if (mine && half == 0) {
+          p.part_ml[2 * slot] = m;
+          p.part_ml[2 * slot + 1] = l;
+        }
       }
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) tmem_free(tmem);
+  if (warp == 17) tmem_free(tmem);
+  if (p.n_splits == 1) return;
+
+  // ---- the last split of the work item joins the shares
+  const size_t item = ((size_t)b * p.Hkv + g) * (gridDim.x / (unsigned)p.n_splits) + blk;
+  if (!arrive_last<kPromptThreads, false>(&p.decode_arrive[item], (unsigned)p.n_splits,
+                                          &bars.give_up))
+    return;
+  for (int o = threadIdx.x; o < (tok1 - tok0) * G * (kHeadDim / 4); o += kPromptThreads) {
+    const int r = o / (kHeadDim / 4), d = o % (kHeadDim / 4) * 4;
+    float M = -CUDART_INF_F, Z = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.n_splits; ++s)
+      M = fmaxf(M, __ldcg(p.part_ml + 2 * (part_slot(pp, s) + r)));
+    for (int s = 0; s < p.n_splits; ++s) {
+      const size_t slot = part_slot(pp, s) + r;
+      const float ms = __ldcg(p.part_ml + 2 * slot);
+      if (ms == -CUDART_INF_F) continue;
+      const float f = ex2(ms - M);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot * kHeadDim + d));
+      Z = fmaf(__ldcg(p.part_ml + 2 * slot + 1), f, Z);
+      A.x = fmaf(x.x, f, A.x);
+      A.y = fmaf(x.y, f, A.y);
+      A.z = fmaf(x.z, f, A.z);
+      A.w = fmaf(x.w, f, A.w);
+    }
+    const bool none = M == -CUDART_INF_F;
+    const float inv = none ? 0.f : 1.f / Z;
+    const size_t at = ((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) + (r & (G - 1));
+    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + d) =
+        none ? make_uint2(0u, 0u)
+             : make_uint2(pack2(A.x * inv, A.y * inv), pack2(A.z * inv, A.w * inv));
+    if (d == 0 && p.lse)
+      p.lse[at] = none ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+  }
+  if (threadIdx.x == 0) p.decode_arrive[item] = 0u;
 }
 
 // cuTensorMapEncodeTiled, taken from the driver at run time (nothing links against it).
@@ -660,9 +855,23 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int rank, const cuuint6
 
 }  // namespace
 
-long long prompt_items(const Params& p, int n_tokens) {
-  const int tokens = 2 * kTileRows / (p.Hq / p.Hkv);
-  return (long long)p.B * p.Hkv * ((n_tokens + tokens - 1) / tokens);
+static int prompt_blocks(int G, int n_tokens) {
+  const int tokens = 2 * kTileRows / G;
+  return (n_tokens + tokens - 1) / tokens;
+}
+
+int prompt_part_rows(int G, int n_tokens) {
+  return (int)std::min<long long>(2 * kTileRows, (long long)n_tokens * G);
+}
+
+// Few work items share their K / V tiles with as many CTAs as fill the GPU once, at least two
+// tiles each.
+int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps) {
+  const long long items = (long long)p.B * p.Hkv * prompt_blocks(p.Hq / p.Hkv, n_tokens);
+  const int tiles = (pages * p.P + kTileTokens - 1) / kTileTokens;
+  long long s = user_pps > 0 ? (pages + user_pps - 1) / user_pps : std::max(1, tiles / 2);
+  s = std::min<long long>(s, (user_pps > 0 ? kPromptParts : kPromptParts / 2) / items);
+  return (int)std::max<long long>(1, std::min<long long>(s, std::min(tiles, 64)));
 }
 
 cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s) {
@@ -672,8 +881,8 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   pp.sink = std::min(sink, 1 << 30);  // positions stay far below, so sums with these do too
   pp.window = std::min(window, 1 << 30);
   const int G = p.Hq / p.Hkv;
-  const int tokens = 2 * kTileRows / G;
-  pp.q_blocks = (n_tokens + tokens - 1) / tokens;
+  pp.log_g = G == 8 ? 3 : G / 2;
+  pp.part_rows = prompt_part_rows(G, n_tokens);
   CUtensorMap mq, mk, mv;
   const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * n_tokens};
   const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
@@ -690,8 +899,8 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   const size_t smem = PromptSmem::total + 1024;
   if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
   void* args[] = {&pp, &mq, &mk, &mv};
-  const long long ctas = prompt_items(p, n_tokens) * p.n_splits;
-  return launch_pdl(fn, dim3((unsigned)ctas), dim3(kPromptThreads), smem, s, args);
+  return launch_pdl(fn, dim3((unsigned)(prompt_blocks(G, n_tokens) * p.n_splits), p.Hkv, p.B),
+                    dim3(kPromptThreads), smem, s, args);
 }
 
 }  // namespace quest

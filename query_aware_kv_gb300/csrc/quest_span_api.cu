@@ -62,13 +62,17 @@ struct SpanLayout {
   size_t seq_done, arrive, scores, sel_idx, sel_count, part_ml, part_acc, total;
 };
 
-SpanLayout span_layout(const quest_cache_t& c, bool narrow, int top_k, long long rows,
-                       const quest_opts_t* o) {
+SpanLayout span_layout(const quest_cache_t& c, bool narrow, int top_k, const quest_opts_t* o,
+                       int n_tokens = 1) {
+  const long long rows = (long long)c.batch * c.num_kv_heads;
   SpanLayout L{};
   const size_t nbg = (size_t)c.batch * c.num_kv_heads;
   // no call on this cache has more pages a row, or more splits, than full attention
-  const size_t parts =
+  size_t parts =
       (size_t)group_of(c) * span_max_parts(narrow, rows, c.max_pages, user_split(o), c.page_size);
+  if (n_tokens > 1)
+    parts = std::max(parts, (size_t)(user_split(o) ? kPromptParts : kPromptParts / 2) *
+                                prompt_part_rows(group_of(c), n_tokens));
   size_t off = sizeof(WsHeader);
   L.seq_done = off;  off = up256(off + (size_t)c.batch * 4);
   L.arrive = off;    off = up256(off + (size_t)kSplitRows * 4);
@@ -137,6 +141,12 @@ int window_pages(const quest_cache_t& c, int sink, int window) {
   return (int)std::min<long long>(n, c.max_pages);
 }
 
+// The same for the rows of a prompt work item, up to 256 query tokens.
+int prompt_pages(const quest_cache_t& c, int n_tokens, int sink, int window) {
+  return window_pages(c, sink, (int)std::min<long long>((long long)window + std::min(n_tokens, 256),
+                                                        0x7fffffff));
+}
+
 // One span-decode launch over `rows` rows of at most `pages` pages.
 int run_span(SpanParams& sp, bool narrow, int pages, const quest_opts_t* o, const void* q,
              void* out, float* lse, quest_stream_t stream, const char* what) {
@@ -175,7 +185,7 @@ int narrow_decode(const quest_narrow_cache_t* cache, const void* q, const void* 
   if (!aligned(k_new, 16) || !aligned(v_new, 16))
     return bad("k_new / v_new must be 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, top_k, (long long)c.batch * c.num_kv_heads, opts);
+  const SpanLayout L = span_layout(c, true, top_k, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   SpanParams sp{};
@@ -205,7 +215,7 @@ size_t quest_narrow_workspace_size(const quest_narrow_cache_t* cache, int32_t to
                                    const quest_opts_t* opts) {
   if (check_narrow(cache) || check_top_k(top_k)) return 0;
   const quest_cache_t c = shared_part(*cache);
-  return span_layout(c, true, top_k, (long long)c.batch * c.num_kv_heads, opts).total;
+  return span_layout(c, true, top_k, opts).total;
 }
 
 int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const void* v,
@@ -219,7 +229,7 @@ int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16))
     return bad("k / v must be non-NULL and 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, (long long)c.batch * c.num_kv_heads, nullptr);
+  const SpanLayout L = span_layout(c, true, 1, nullptr);
   if ((rc = check_workspace(ws, ws_bytes, L.arrive))) return rc;
   const Params p = make_params(c, ws, L, nullptr);
   return launched(launch_narrow_prefill(p, narrow_ptrs(*cache), static_cast<const __half*>(k),
@@ -236,7 +246,7 @@ int quest_narrow_append(const quest_narrow_cache_t* cache, const void* k_new, co
   if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))
     return bad("k_new / v_new must be non-NULL and 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, (long long)c.batch * c.num_kv_heads, nullptr);
+  const SpanLayout L = span_layout(c, true, 1, nullptr);
   if ((rc = check_workspace(ws, ws_bytes, L.arrive))) return rc;
   const Params p = make_params(c, ws, L, nullptr);
   return launched(launch_narrow_append(p, narrow_ptrs(*cache), static_cast<const __half*>(k_new),
@@ -257,7 +267,7 @@ int quest_narrow_sparse_decode(const quest_narrow_cache_t* cache, const void* q,
   if (!idx || !count || !aligned(idx, 4) || !aligned(count, 4))
     return bad("idx / count must be non-NULL and 4-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, top_k, (long long)c.batch * c.num_kv_heads, opts);
+  const SpanLayout L = span_layout(c, true, top_k, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
@@ -279,7 +289,7 @@ int quest_narrow_dense_decode(const quest_narrow_cache_t* cache, const void* q, 
   if (cache->batch == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, (long long)c.batch * c.num_kv_heads, opts);
+  const SpanLayout L = span_layout(c, true, 1, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
@@ -315,7 +325,7 @@ int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
   if (cache->batch == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, (long long)c.batch * c.num_kv_heads, opts);
+  const SpanLayout L = span_layout(c, true, 1, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
@@ -335,9 +345,7 @@ size_t quest_window_workspace_size(const quest_cache_t* cache, int32_t n_tokens,
     bad("n_tokens must be in [1, max_pages * page_size]");
     return 0;
   }
-  return span_layout(*cache, false, 0, (long long)cache->batch * n_tokens * cache->num_kv_heads,
-                     opts)
-      .total;
+  return span_layout(*cache, false, 0, opts, n_tokens).total;
 }
 
 static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_tokens,
@@ -351,24 +359,24 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
     return bad("n_tokens must be in [0, max_pages * page_size]");
   if (cache->batch == 0 || n_tokens == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
-  const long long rows = (long long)cache->batch * n_tokens * cache->num_kv_heads;
-  const SpanLayout L = span_layout(*cache, false, 0, rows, opts);
+  const SpanLayout L = span_layout(*cache, false, 0, opts, n_tokens);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(*cache, ws, L, nullptr);
-  sp.mode = kSpanWindow;
-  sp.sink = sink_tokens;
-  sp.window = window;
-  sp.n_tokens = n_tokens;
   if (n_tokens > 1) {
     sp.p.q = static_cast<const __half*>(q);
     sp.p.out = static_cast<__half*>(out);
     sp.p.lse = lse;
-    sp.p.n_splits = 1;
+    sp.p.n_splits = prompt_splits(sp.p, n_tokens, prompt_pages(*cache, n_tokens, sink_tokens, window),
+                                  user_split(opts));
     return launched(launch_prompt(sp.p, n_tokens, sink_tokens, window,
                                   static_cast<cudaStream_t>(stream)),
                     what);
   }
+  sp.mode = kSpanWindow;
+  sp.sink = sink_tokens;
+  sp.window = window;
+  sp.n_tokens = 1;
   return run_span(sp, false, window_pages(*cache, sink_tokens, window), opts, q, out, lse, stream,
                   what);
 }
