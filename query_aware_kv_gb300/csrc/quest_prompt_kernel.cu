@@ -37,12 +37,12 @@ namespace quest {
 
 namespace {
 
-// Five warpgroups: two for the softmax of either tile, and the fetch warps (16: Q and K, 18: V)
-// with the issue warps (17 and 19, a query tile each).  Registers: 640 x 96 at launch, then
-// 104 for the softmax threads (64 scores each) and 64 for the others, the same total.
-constexpr int kPromptThreads = 640;
-constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * 96, "registers of the launch");
+// Three warpgroups: the softmax of either tile, and the fetch warps (8: Q and K, 10: V) with the
+// issue warps (9 and 11, a query tile each).  Registers: 384 x 168 at launch, then 216 for the
+// softmax threads (a row of 128 scores each) and 72 for the others, the same total.
+constexpr int kPromptThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of the launch");
 constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
@@ -55,8 +55,7 @@ struct PromptSmem {
   static constexpr int q = 0;                             // [2][32 KiB]
   static constexpr int kv = 2 * kTileBytes;               // [kKvStages][32 KiB]
   static constexpr int bars = kv + kKvStages * kTileBytes;
-  static constexpr int top = bars + 256;                  // [2][128]: running row maxima
-  static constexpr int total = top + 2 * kTileRows * 4;
+  static constexpr int total = bars + 256;
 };
 static_assert(PromptSmem::total + 1024 <= (int)kMaxSmem, "shared memory of a CTA");
 
@@ -128,6 +127,23 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
       "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -220,9 +236,9 @@ struct Bars {
   // S of query tile t and K / V tile j is in s_full[t][j & 1]; its completion also says that
   // Q K^T (t, j) and P V (t, j - 1) have read their K and V tiles
   uint64_t s_full[2][2], p_full[2], o_full[2], drain[2];
+  uint64_t turn[2];  // the issue warp of tile t may issue its next group of products
   uint32_t tmem;
   int give_up;
-  int word[2][3];  // any_of_tile
 };
 static_assert(sizeof(Bars) <= 256, "barrier area");
 
@@ -233,55 +249,12 @@ struct PageList {
   __device__ __forceinline__ int page(int i) const { return i < n_sink ? i : first + i - n_sink; }
 };
 
-// The rows of a query tile (positions r0 .. r1) against a K / V tile that starts at list
-// entry i0: none of its tokens is visible to any row, or all are to every row.
-struct TileRows {
-  int r0, r1, window, sink, n_sink, first, count;
-  template <int P>
-  __device__ __forceinline__ int base(int i0) const { return (first + i0 - n_sink) * P; }
-  template <int P>
-  __device__ __forceinline__ bool none(int i0) const {
-    return i0 >= n_sink &&
-           (base<P>(i0) > r1 ||
-            (base<P>(i0) >= sink && base<P>(i0) + kTileTokens - 1 <= r0 - window));
-  }
-  template <int P>
-  __device__ __forceinline__ bool all(int i0) const {
-    return i0 >= n_sink && i0 + kTileTokens / P <= count && base<P>(i0) + kTileTokens - 1 <= r0 &&
-           (base<P>(i0) > r1 - window || base<P>(i0) + kTileTokens <= sink);
-  }
-};
-
 // Where split s of this CTA's work item keeps its rows' shares.
 __device__ __forceinline__ size_t part_slot(const PromptParams& pp, int s) {
   const unsigned blocks = gridDim.x / (unsigned)pp.p.n_splits;
   const unsigned blk = (gridDim.x - 1 - blockIdx.x) / (unsigned)pp.p.n_splits;
   const size_t item = ((size_t)blockIdx.z * pp.p.Hkv + blockIdx.y) * blocks + blk;
   return (item * pp.p.n_splits + s) * pp.part_rows;
-}
-
-// The 256 softmax threads of tile t meet.
-__device__ __forceinline__ void sync_tile(int t) {
-  __syncwarp();
-  __barrier_sync_count(1 + t, 2 * kTileRows);
-}
-// Whether any of them says so.  `word`: the tile's for this place in the code, in shared memory;
-// `round`: the place's count, from 1.  (A warp cannot come to a place again, and write its
-// word, before every other one has read it: in between all meet elsewhere, or wait for scores
-// that need every warp's weights.)
-__device__ __forceinline__ bool any_of_tile(int t, bool x, volatile int* word, int round) {
-  if (__any_sync(0xffffffffu, x)) *word = round;
-  sync_tile(t);
-  return *word == round;
-}
-
-// A float as an int of the same order, and back.
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int i) {
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
 // The lowest x bits (0 <= x <= 32).
@@ -346,17 +319,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&bars.s_full[t][0], 1);
       mbar_init(&bars.s_full[t][1], 1);
       mbar_init(&bars.drain[t], 1);
-      mbar_init(&bars.p_full[t], 8);
+      mbar_init(&bars.turn[t], 1);
+      mbar_init(&bars.p_full[t], 4);
       mbar_init(&bars.o_full[t], 1);
     }
     bars.give_up = 0;
-    for (int i = 0; i < 6; ++i) bars.word[i / 3][i % 3] = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x < 2 * kTileRows)
-    reinterpret_cast<int*>(smem + PromptSmem::top)[threadIdx.x] = ordered(-CUDART_INF_F);
-  if (warp == 17) tmem_alloc(&bars.tmem);
-  if (warp == 16 && lane < 3)
+  if (warp == 9) tmem_alloc(&bars.tmem);
+  if (warp == 8 && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v)
                  : "memory");
   fence_before();
@@ -374,7 +345,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int n = pp.n_tokens, tok0 = blk * 2 * TT;
   const int tok1 = min(n, tok0 + 2 * TT);
   const int n_q = tok1 - tok0 > TT ? 2 : 1;  // query tiles with rows
-  if (warp == 16 && elect_lane()) {  // the queries' place does not depend on the length
+  if (warp == 8 && elect_lane()) {  // the queries' place does not depend on the length
     mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
     for (int i = 0; i < 2 * n_q; ++i)
       tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
@@ -399,11 +370,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int j0 = (int)((long long)tiles * split / p.n_splits);
   const int j1 = (int)((long long)tiles * (split + 1) / p.n_splits);
 
-  if (warp >= 16) {
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 16 || warp == 18) {
-    // ---- fetch: warp 16 the K tiles (the queries are on their way), warp 18 the V tiles
-    const int kv = warp == 18;
+    if (warp == 8 || warp == 10) {
+    // ---- fetch: warp 8 the K tiles (the queries are on their way), warp 10 the V tiles
+    const int kv = warp == 10;
     if (j1 > j0) {
       // 32 pages of the list at a time, a page per lane, the next 32 on their way; entries
       // behind the list's end repeat its last page (their tokens are hidden)
@@ -462,12 +433,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (kv == 0)
       for (int i = 0; i < 1 << 20; ++i)
         if (mbar_try_wait(&bars.q_full, 0)) break;
-  } else if (warp - 17 < 2 * n_q - 1 && j1 > j0) {
-    // ---- issue: warp 17 the products of query tile 0, warp 19 those of tile 1.  (One warp for
+  } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
+    // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
     // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
     // other tile's products fill those.)
     {
-      const int t = warp == 19;
+      const int t = warp == 11;
       // Q and K are K-major: the stride is that of 8-row groups.  V is MN-major: the lead is
       // that of its 64-dim spans, the stride that of 8-token groups.  Address fields count
       // 16 bytes.
@@ -479,15 +450,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, prompt_wait(p, bar, parity, give_up)) != 0;
       };
-      const int r0 = pos0 + tok0 + t * TT;
-      const TileRows rows{r0, min(r0 + TT, end) - 1, pp.window, pp.sink,
-                          list.n_sink, list.first, list.count};
-      // (a tile that no row sees only passes its barriers on; the branches around the elected
-      // lane's products depend on nothing but uniform values)
-      auto qk = [&](int st, bool live, uint64_t* done) {
-        if (!live) {
-          if (elect_lane()) commit(done);
-        } else if (elect_lane()) {
+      auto qk = [&](int st, uint64_t* done) {
+        if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kHeadDim / 16; ++k) {
             const uint32_t oq = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
@@ -501,9 +465,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
       fence_after();
-      bool live = !rows.none<P>(j0 * PPT);
-      uint32_t started = 0;
-      if (ok) qk(0, live, &bars.s_full[t][0]);
+      if (ok) qk(0, &bars.s_full[t][0]);
       int sv = 1, sk = 2;  // stages of the V and the next K tile
       uint32_t round_v = 0, round_k = 0;
       for (int j = j0; j < j1 && ok; ++j) {
@@ -534,24 +496,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
         }
         if (!(ok = wait(&bars.p_full[t], (j - j0) & 1))) break;
+        // The two tiles' groups of products, P V (j) with Q K^T (j + 1), take turns: side by side
+        // they end together, the two softmaxes then run together too, and nothing overlaps (a
+        // tile pair took 4200 cycles so, against 2750 in turns).
+        if (n_q > 1 && (t == 1 || j > j0) &&
+            !(ok = wait(&bars.turn[t], (uint32_t)(j - j0 - (t == 0)) & 1)))
+          break;
         fence_after();
-        if (live) {
-          if (elect_lane()) {
+        if (elect_lane()) {
 #pragma unroll
-            for (int k = 0; k < kTileTokens / 16; ++k)
-              mma_ts(o_mem, s_mem + 8 * k,
-                     v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)),
-                     kIdescPV, k > 0 ? 1u : started);
-          }
-          started = 1;
+          for (int k = 0; k < kTileTokens / 16; ++k)
+            mma_ts(o_mem, s_mem + 8 * k,
+                   v_desc + (uint32_t)(sv * (kTileBytes >> 4) + k * (2 * kGroupBytes >> 4)),
+                   kIdescPV, j > j0 || k > 0);
+          if (!more) commit(&bars.o_full[t]);
         }
         __syncwarp();
-        if (more) {
-          live = !rows.none<P>((j + 1) * PPT);
-          qk(sk, live, &bars.s_full[t][(j - j0 + 1) & 1]);
-        } else if (elect_lane()) {
-          commit(&bars.o_full[t]);
-        }
+        if (more) qk(sk, &bars.s_full[t][(j - j0 + 1) & 1]);
+        if (n_q > 1 && lane == 0) mbar_arrive(&bars.turn[t ^ 1]);
         __syncwarp();
         if ((sv += 2) >= kKvStages) {
           sv -= kKvStages;
@@ -571,128 +533,128 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   }
   } else {
-    // ---- softmax: two threads a row, 64 of a tile's tokens (and of O's dims) each
+    // ---- softmax: a thread a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int t = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
+    const int t = warp >> 2, row = threadIdx.x & 127;
     const int tok = tok0 + t * TT + (row >> lg);
     const int pr = pos0 + tok;  // the row's position
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lanes + t * 128 + 64 * half;
-    const uint32_t p_col = tmem + lanes + t * 128 + 32 * half;
-    const uint32_t o_col = tmem + lanes + 256 + t * 128 + 64 * half;
-    int* my_top = reinterpret_cast<int*>(smem + PromptSmem::top) + t * kTileRows + row;
-    volatile int* word = bars.word[t];
-    float m = -CUDART_INF_F, l = 0.f;  // l: of this thread's tokens
-    bool ok = true, started = false;
+    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + 256 + t * 128;
+    float m = -CUDART_INF_F, l = 0.f;
+    bool ok = true;
     if (t < n_q) {
       const int r0 = pos0 + tok0 + t * TT;
-      const TileRows rows{r0, min(r0 + TT, end) - 1, pp.window, pp.sink,
-                          list.n_sink, list.first, list.count};
+      const int r1 = min(r0 + TT, end) - 1;
       for (int j = j0; j < j1; ++j) {
         ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(j - j0) & 1],
                                                  (uint32_t)((j - j0) >> 1) & 1, give_up));
+        if (!ok) break;
         const int i0 = j * PPT;
-        if (!rows.none<P>(i0)) {
-          fence_after();
-          if (!rows.all<P>(i0)) {
-            // Hidden tokens' scores become -inf in TMEM before the common path (a mask inside
-            // it costs every tile the registers and the order of its instructions).  32
-            // tokens at a time as bits: page by page those up to the row's own position that
-            // are in its window or among the sinks.
+        fence_after();
+        const int base = (list.first + i0 - list.n_sink) * P;
+        const bool whole = i0 >= list.n_sink && i0 + PPT <= list.count &&
+                           base + kTileTokens - 1 <= r0 &&
+                           (base > r1 - pp.window || base + kTileTokens <= pp.sink);
+        if (!whole) {
+          // Hidden tokens' scores become -inf in TMEM before the common path (a mask inside
+          // it costs every tile the registers and the order of its instructions).  32
+          // tokens at a time as bits: page by page those up to the row's own position that
+          // are in its window or among the sinks.
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u) {
+            uint32_t x[32], bits = 0;
+            tmem_ld32(s_col + 32 * u, x);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t x[32], bits = 0;
-              tmem_ld32(s_col + 32 * u, x);
+            for (int e = 0; e < 32 / P; ++e) {
+              const int i = i0 + u * (32 / P) + e, at = list.page(i) * P;
+              const int hi = min(max(pr + 1 - at, 0), P);
+              const int lo = min(max(pr + 1 - pp.window - at, 0), P);
+              const int sk = min(max(pp.sink - at, 0), P);
+              const uint32_t b32 = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
+              bits |= (i < list.count ? b32 : 0u) << (P * e & 31);
+            }
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32 / P; ++e) {
-                const int i = i0 + (2 * half + u) * (32 / P) + e, at = list.page(i) * P;
-                const int hi = min(max(pr + 1 - at, 0), P);
-                const int lo = min(max(pr + 1 - pp.window - at, 0), P);
-                const int sk = min(max(pp.sink - at, 0), P);
-                const uint32_t b32 = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
-                bits |= (i < list.count ? b32 : 0u) << (P * e & 31);
-              }
+            for (int k = 0; k < 32; ++k)
+              if (!(bits & 1u << k)) x[k] = 0xff800000u;
+            tmem_st32(s_col + 32 * u, x);
+          }
+          tmem_wait_st();
+        }
+        // 32 scores at s + 32 u: their weights against the reference m
+        uint32_t w[kTileTokens / 2];
+        uint64_t sum[4] = {0, 0, 0, 0};
+        auto weigh = [&](const float* s, int u) {
+          const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
+          const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a, c;
+            unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, shift2), a, c);
+            a = ex2(a);
+            c = ex2(c);
+            sum[k & 3] = add2(sum[k & 3], pair(a, c));
+            w[16 * u + k] = pack2(a, c);
+          }
+        };
+        // The weights are taken against the reference as it is, the maximum beside them (the two
+        // use different pipes).  Where a row exceeds the reference by 2^kLazy the warp's rows
+        // move theirs, l and O with them, and take the weights again from S, which P has not
+        // replaced yet.
+        float top;
+        {
+          float s[kTileTokens];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            tmem_ld32(s_col + 32 * u, reinterpret_cast<uint32_t*>(s) + 32 * u);
+          tmem_wait_ld();
+          // four chains of three-input maxima: one chain of 127 would wait on itself
+          float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int k = 4; k + 8 <= kTileTokens; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kTileTokens - 4 + e]);
+          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) weigh(s + 32 * u, u);
+        }
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          const float mn = fmaxf(m, top);
+          const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (j > j0) {
+#pragma unroll 1
+            for (int u = 0; u < 8; ++u) {
+              uint32_t o[16];
+              tmem_ld16(o_col + 16 * u, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(bits & 1u << k)) x[k] = 0xff800000u;
-              tmem_st32(s_col + 32 * u, x);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(o_col + 16 * u, o);
             }
-            tmem_wait_st();
           }
-          uint32_t w[32];
-          float top, sum;
-          // this thread's 64 scores: their maximum, and their weights against m
-          auto weigh = [&]() {
-            float s[64];
-            tmem_ld32(s_col, reinterpret_cast<uint32_t*>(s));
-            tmem_ld32(s_col + 32, reinterpret_cast<uint32_t*>(s) + 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[k] = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float s[32];
+            tmem_ld32(s_col + 32 * u, reinterpret_cast<uint32_t*>(s));
             tmem_wait_ld();
-            const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
-            const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
-            uint64_t z[4] = {0, 0, 0, 0};
-            // four chains of three-input maxima: one chain of 63 would wait on itself
-            float t4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int k = 4; k + 8 <= 64; k += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[60 + e]);
-            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float a, c;
-              unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, shift2), a, c);
-              a = ex2(a);
-              c = ex2(c);
-              z[k & 3] = add2(z[k & 3], pair(a, c));
-              w[k] = pack2(a, c);
-            }
-            float a, c;
-            unpair(add2(add2(z[0], z[1]), add2(z[2], z[3])), a, c);
-            sum = a + c;
-          };
-          // The weights are taken against the reference as it is; where a row of the tile
-          // exceeds it by 2^kLazy the tile's rows move theirs, l and O with them, and take the
-          // weights again.  P goes where S was, so no thread stores before all have loaded.
-          // (A thread that gave up takes the whole tile's threads along: they meet at barriers.)
-          weigh();
-          const bool over = __any_sync(0xffffffffu, top > m + kLazy);
-          if (any_of_tile(t, over | !ok, word, j - j0 + 1)) {
-            if (any_of_tile(t, !ok, word + 1, j - j0 + 1)) {
-              ok = false;
-              break;
-            }
-            atomicMax(my_top, ordered(top));  // of both halves; it never falls, like m
-            sync_tile(t);
-            const float mn = unordered(*reinterpret_cast<volatile int*>(my_top));
-            const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
-            m = mn;
-            l *= f;
-            weigh();
-            sync_tile(t);
-            if (started) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint32_t o[32];
-                tmem_ld32(o_col + 32 * u, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st32(o_col + 32 * u, o);
-              }
-            }
+            weigh(s, u);
           }
-          tmem_st32(p_col, w);
-          l += sum;
-          started = true;
-          tmem_wait_st();
-          fence_before();
-        } else if (any_of_tile(t, !ok, word + 1, j - j0 + 1)) {
-          ok = false;
-          break;
         }
+        tmem_st32(s_col, w);
+        tmem_st32(s_col + 32, w + 32);
+        {
+          float a, c;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
+          l += a + c;
+        }
+        tmem_wait_st();
+        fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[t]);
       }
@@ -700,27 +662,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (ok)
         ok = __all_sync(0xffffffffu, prompt_wait(p, j1 > j0 ? &bars.o_full[t] : &bars.q_full, 0,
                                                  give_up));
-      ok = !any_of_tile(t, !ok, word + 2, 1);
       fence_after();
-      if (ok) {  // the halves' sums, through the query space
-        float* ls = reinterpret_cast<float*>(smem + PromptSmem::q + t * kTileBytes);
-        ls[half * kTileRows + row] = l;
-        sync_tile(t);
-        l = ls[row] + ls[kTileRows + row];
-        sync_tile(t);
-      }
       const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
       const bool mine = tok < tok1;
       if (ok && p.n_splits == 1) {
-        // ---- out = O / l, through the tile's own query space (its products are done): half a
-        // row of 128 B per thread goes to shared memory, four of them at a time leave
+        // ---- out = O / l, through the tile's own query space (its products are done): a row
+        // of 256 B per thread goes to shared memory, two rows at a time leave as whole lines
         const size_t row0 = ((size_t)b * n + tok0 + t * TT) * p.Hq + ((size_t)g << lg);
-        unsigned char* stage = smem + PromptSmem::q + t * kTileBytes + half * kHalfBytes;
+        unsigned char* stage = smem + PromptSmem::q + t * kTileBytes;
         const float inv = none ? 0.f : 1.f / l;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
           uint32_t o[32];
-          if (started) {
+          if (j1 > j0) {
             tmem_ld32(o_col + 32 * u, o);
             tmem_wait_ld();
           }
@@ -732,43 +686,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               x[k] = none ? 0u
                           : pack2(__uint_as_float(o[8 * e + 2 * k]) * inv,
                                   __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + row * 128 + (((4 * u + e) ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(stage + row * 256 + (((4 * u + e) ^ (row & 15)) << 4)) =
                 make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
-        if (mine && half == 0 && p.lse)
+        if (mine && p.lse)
           p.lse[row0 + (size_t)(row >> lg) * p.Hq + (row & (G - 1))] =
               none ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.6931471805599453f;
         __syncwarp();
-        const int c = lane & 7;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = (row & ~31) + 4 * i + (lane >> 3);
+        const int c = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int r = (row & ~31) + 2 * i + (lane >> 4);
           if (tok0 + t * TT + (r >> lg) < tok1)
             *reinterpret_cast<uint4*>(
-                p.out + (row0 + (size_t)(r >> lg) * p.Hq + (r & (G - 1))) * kHeadDim + 64 * half +
-                8 * c) = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+                p.out + (row0 + (size_t)(r >> lg) * p.Hq + (r & (G - 1))) * kHeadDim + 8 * c) =
+                *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
         }
       } else if (ok) {
         // ---- a split's share: O, m and l as they are (the loads are the whole warp's)
         const size_t slot = part_slot(pp, split) + t * kTileRows + row;
-        float* dst = p.part_acc + slot * kHeadDim + 64 * half;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
           uint32_t o[32];
-          if (started) {
+          if (j1 > j0) {
             tmem_ld32(o_col + 32 * u, o);
             tmem_wait_ld();
           }
           if (mine) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(dst + 32 * u + 4 * e) =
-                  started ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
+              *reinterpret_cast<uint4*>(p.part_acc + slot * kHeadDim + 32 * u + 4 * e) =
+                  j1 > j0 ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
                           : make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (mine && half == 0) {
+        if (mine) {
           p.part_ml[2 * slot] = m;
           p.part_ml[2 * slot + 1] = l;
         }
@@ -778,7 +731,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 17) tmem_free(tmem);
+  if (warp == 9) tmem_free(tmem);
   if (p.n_splits == 1) return;
 
   // ---- the last split of the work item joins the shares
@@ -786,23 +739,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (!arrive_last<kPromptThreads, false>(&p.decode_arrive[item], (unsigned)p.n_splits,
                                           &bars.give_up))
     return;
+  const size_t first_slot = part_slot(pp, 0);
   for (int o = threadIdx.x; o < (tok1 - tok0) * G * (kHeadDim / 4); o += kPromptThreads) {
     const int r = o / (kHeadDim / 4), d = o % (kHeadDim / 4) * 4;
+    const float* ml = p.part_ml + 2 * (first_slot + r);
+    const float* acc = p.part_acc + (first_slot + r) * kHeadDim + d;
     float M = -CUDART_INF_F, Z = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int s = 0; s < p.n_splits; ++s)
-      M = fmaxf(M, __ldcg(p.part_ml + 2 * (part_slot(pp, s) + r)));
+      M = fmaxf(M, __ldcg(ml + (size_t)2 * s * pp.part_rows));
+    // (loads of eight splits side by side: an empty one has m = -inf, l and O 0)
+#pragma unroll 8
     for (int s = 0; s < p.n_splits; ++s) {
-      const size_t slot = part_slot(pp, s) + r;
-      const float ms = __ldcg(p.part_ml + 2 * slot);
-      if (ms == -CUDART_INF_F) continue;
-      const float f = ex2(ms - M);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot * kHeadDim + d));
-      Z = fmaf(__ldcg(p.part_ml + 2 * slot + 1), f, Z);
-      A.x = fmaf(x.x, f, A.x);
-      A.y = fmaf(x.y, f, A.y);
-      A.z = fmaf(x.z, f, A.z);
-      A.w = fmaf(x.w, f, A.w);
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + (size_t)2 * s * pp.part_rows));
+      const float4 a =
+          __ldcg(reinterpret_cast<const float4*>(acc + (size_t)s * pp.part_rows * kHeadDim));
+      const float f = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);
+      Z = fmaf(x.y, f, Z);
+      A.x = fmaf(a.x, f, A.x);
+      A.y = fmaf(a.y, f, A.y);
+      A.z = fmaf(a.z, f, A.z);
+      A.w = fmaf(a.w, f, A.w);
     }
     const bool none = M == -CUDART_INF_F;
     const float inv = none ? 0.f : 1.f / Z;
