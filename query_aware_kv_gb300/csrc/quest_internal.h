@@ -203,24 +203,23 @@ struct NarrowPtrs {
 // Which pages a span-decode row attends over.
 enum SpanMode : int { kSpanDense = 0, kSpanList = 1, kSpanWindow = 2 };
 
-// One launch of the span decode (quest_span_kernel.cu): a row is one query token and kv
-// head, its kept pages cut into n_splits runs.
+// One launch of the span decode (quest_span_kernel.cu): one query token per sequence, a row
+// per (sequence, kv head).
 struct SpanParams {
-  Params p;               // q, out, lse: [B][n_tokens][Hq][128] / [B][n_tokens][Hq];
-                          // n_splits, part_ml, part_acc, decode_arrive: per row
+  Params p;               // part_ml, part_acc: G slots per CTA; decode_arrive: one per row;
+                          // with chain_append the launch advances the lengths (exited)
   NarrowPtrs nar;         // narrow caches only
   int mode;               // SpanMode
   int sink, window;       // kSpanWindow, in tokens
-  int n_tokens;           // query tokens per sequence (the last ones); 1 but for prompts
+  int run_pages;          // pages of a split (0: the launch's choice)
 };
 
-// Splits of a span-decode launch over `rows` rows of at most `pages` pages (1 for more than
-// kSplitRows rows: the counters of a workspace are where every call expects them).
-constexpr int kSplitRows = 1024;
-int span_splits(bool narrow, long long rows, int pages, int user_pps, int page_size);
-// The most partials (rows * splits) that a launch of up to `rows` rows can write.
-long long span_max_parts(bool narrow, long long rows, int pages, int user_pps, int page_size);
-cudaError_t launch_span(const SpanParams& sp, bool narrow, cudaStream_t s);
+constexpr int kSplitRows = 1024;  // rows of a launch that splits them, at most (its counters)
+// The most parts (rows * splits) that a launch writes; `user`: with run_pages given.
+size_t span_max_parts(int batch, int hkv, bool user);
+// `pages`: the most that a row has.
+cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s);
+
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
 // p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of
 // part_ml / part_acc each; splits only while items * splits is at most kPromptParts.

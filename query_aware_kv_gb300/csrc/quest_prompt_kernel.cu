@@ -746,21 +746,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const float* acc = p.part_acc + (first_slot + r) * kHeadDim + d;
     float M = -CUDART_INF_F, Z = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int s = 0; s < p.n_splits; ++s)
-      M = fmaxf(M, __ldcg(ml + (size_t)2 * s * pp.part_rows));
-    // (loads of eight splits side by side: an empty one has m = -inf, l and O 0)
-#pragma unroll 8
-    for (int s = 0; s < p.n_splits; ++s) {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(ml + (size_t)2 * s * pp.part_rows));
-      const float4 a =
-          __ldcg(reinterpret_cast<const float4*>(acc + (size_t)s * pp.part_rows * kHeadDim));
-      const float f = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);
-      Z = fmaf(x.y, f, Z);
-      A.x = fmaf(a.x, f, A.x);
-      A.y = fmaf(a.y, f, A.y);
-      A.z = fmaf(a.z, f, A.z);
-      A.w = fmaf(a.w, f, A.w);
+    // eight splits' loads side by side, the last few too (an empty split has m = -inf, l and O 0)
+    for (int s0 = 0; s0 < p.n_splits; s0 += 8) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = s0 + e < p.n_splits ? __ldcg(ml + (size_t)2 * (s0 + e) * pp.part_rows)
+                                   : -CUDART_INF_F;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) M = fmaxf(M, x[e]);
+    }
+    for (int s0 = 0; s0 < p.n_splits; s0 += 8) {
+      float2 x[8];
+      float4 a[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const size_t o2 = (size_t)min(s0 + e, p.n_splits - 1) * pp.part_rows;
+        x[e] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * o2));
+        a[e] = __ldcg(reinterpret_cast<const float4*>(acc + o2 * kHeadDim));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f =
+            s0 + e >= p.n_splits || x[e].x == -CUDART_INF_F ? 0.f : ex2(x[e].x - M);
+        Z = fmaf(x[e].y, f, Z);
+        A.x = fmaf(a[e].x, f, A.x);
+        A.y = fmaf(a[e].y, f, A.y);
+        A.z = fmaf(a[e].z, f, A.z);
+        A.w = fmaf(a[e].w, f, A.w);
+      }
     }
     const bool none = M == -CUDART_INF_F;
     const float inv = none ? 0.f : 1.f / Z;

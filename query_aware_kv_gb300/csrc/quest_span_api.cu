@@ -55,21 +55,18 @@ int user_split(const quest_opts_t* o) {
   return o && o->pages_per_split > 0 ? o->pages_per_split : 0;
 }
 
-// Workspace of span-decode rows: the header and the counters (zero between calls, and at
-// the same place for every top_k, n_tokens and opts), what a chain step keeps between its
-// kernels, and the split-K partials.
+// Workspace: the header and the counters (zero between calls, and at the same place for every
+// top_k, n_tokens and opts), what a chain step keeps between its kernels, and the parts of
+// split rows.
 struct SpanLayout {
   size_t seq_done, arrive, scores, sel_idx, sel_count, part_ml, part_acc, total;
 };
 
-SpanLayout span_layout(const quest_cache_t& c, bool narrow, int top_k, const quest_opts_t* o,
+SpanLayout span_layout(const quest_cache_t& c, int top_k, const quest_opts_t* o,
                        int n_tokens = 1) {
-  const long long rows = (long long)c.batch * c.num_kv_heads;
   SpanLayout L{};
   const size_t nbg = (size_t)c.batch * c.num_kv_heads;
-  // no call on this cache has more pages a row, or more splits, than full attention
-  size_t parts =
-      (size_t)group_of(c) * span_max_parts(narrow, rows, c.max_pages, user_split(o), c.page_size);
+  size_t parts = span_max_parts(c.batch, c.num_kv_heads, user_split(o) > 0) * group_of(c);
   if (n_tokens > 1)
     parts = std::max(parts, (size_t)(user_split(o) ? kPromptParts : kPromptParts / 2) *
                                 prompt_part_rows(group_of(c), n_tokens));
@@ -100,6 +97,7 @@ Params make_params(const quest_cache_t& c, void* ws, const SpanLayout& L, const 
   p.seq_lens = c.seq_lens;
   unsigned char* w = static_cast<unsigned char*>(ws);
   p.status = &reinterpret_cast<WsHeader*>(w)->status;
+  p.exited = &reinterpret_cast<WsHeader*>(w)->exited;
   p.seq_done = reinterpret_cast<unsigned*>(w + L.seq_done);
   p.decode_arrive = reinterpret_cast<unsigned*>(w + L.arrive);
   p.scores = reinterpret_cast<float*>(w + L.scores);
@@ -147,15 +145,14 @@ int prompt_pages(const quest_cache_t& c, int n_tokens, int sink, int window) {
                                                         0x7fffffff));
 }
 
-// One span-decode launch over `rows` rows of at most `pages` pages.
+// One span-decode launch over rows of at most `pages` pages.
 int run_span(SpanParams& sp, bool narrow, int pages, const quest_opts_t* o, const void* q,
              void* out, float* lse, quest_stream_t stream, const char* what) {
-  const long long rows = (long long)sp.p.B * sp.n_tokens * sp.p.Hkv;
   sp.p.q = static_cast<const __half*>(q);
   sp.p.out = static_cast<__half*>(out);
   sp.p.lse = lse;
-  sp.p.n_splits = span_splits(narrow, rows, pages, user_split(o), sp.p.P);
-  return launched(launch_span(sp, narrow, static_cast<cudaStream_t>(stream)), what);
+  sp.run_pages = user_split(o);
+  return launched(launch_span(sp, narrow, pages, static_cast<cudaStream_t>(stream)), what);
 }
 
 int check_narrow_opts(const quest_opts_t* o, int top_k) {
@@ -185,14 +182,13 @@ int narrow_decode(const quest_narrow_cache_t* cache, const void* q, const void* 
   if (!aligned(k_new, 16) || !aligned(v_new, 16))
     return bad("k_new / v_new must be 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, top_k, opts);
+  const SpanLayout L = span_layout(c, top_k, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   SpanParams sp{};
   sp.p = make_params(c, ws, L, opts);
   sp.nar = narrow_ptrs(*cache);
   sp.mode = kSpanList;
-  sp.n_tokens = 1;
   if (idx_out) sp.p.sel_idx = idx_out;
   if (count_out) sp.p.sel_count = count_out;
   sp.p.top_k = top_k;
@@ -215,7 +211,7 @@ size_t quest_narrow_workspace_size(const quest_narrow_cache_t* cache, int32_t to
                                    const quest_opts_t* opts) {
   if (check_narrow(cache) || check_top_k(top_k)) return 0;
   const quest_cache_t c = shared_part(*cache);
-  return span_layout(c, true, top_k, opts).total;
+  return span_layout(c, top_k, opts).total;
 }
 
 int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const void* v,
@@ -229,7 +225,7 @@ int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16))
     return bad("k / v must be non-NULL and 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, nullptr);
+  const SpanLayout L = span_layout(c, 1, nullptr);
   if ((rc = check_workspace(ws, ws_bytes, L.arrive))) return rc;
   const Params p = make_params(c, ws, L, nullptr);
   return launched(launch_narrow_prefill(p, narrow_ptrs(*cache), static_cast<const __half*>(k),
@@ -246,7 +242,7 @@ int quest_narrow_append(const quest_narrow_cache_t* cache, const void* k_new, co
   if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16))
     return bad("k_new / v_new must be non-NULL and 16-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, nullptr);
+  const SpanLayout L = span_layout(c, 1, nullptr);
   if ((rc = check_workspace(ws, ws_bytes, L.arrive))) return rc;
   const Params p = make_params(c, ws, L, nullptr);
   return launched(launch_narrow_append(p, narrow_ptrs(*cache), static_cast<const __half*>(k_new),
@@ -267,13 +263,12 @@ int quest_narrow_sparse_decode(const quest_narrow_cache_t* cache, const void* q,
   if (!idx || !count || !aligned(idx, 4) || !aligned(count, 4))
     return bad("idx / count must be non-NULL and 4-byte aligned");
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, top_k, opts);
+  const SpanLayout L = span_layout(c, top_k, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
   sp.nar = narrow_ptrs(*cache);
   sp.mode = kSpanList;
-  sp.n_tokens = 1;
   sp.p.sel_idx = const_cast<int*>(idx);
   sp.p.sel_count = const_cast<int*>(count);
   sp.p.top_k = top_k;
@@ -289,13 +284,12 @@ int quest_narrow_dense_decode(const quest_narrow_cache_t* cache, const void* q, 
   if (cache->batch == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, opts);
+  const SpanLayout L = span_layout(c, 1, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
   sp.nar = narrow_ptrs(*cache);
   sp.mode = kSpanDense;
-  sp.n_tokens = 1;
   return run_span(sp, true, c.max_pages, opts, q, out, lse, stream, "quest_narrow_dense_decode");
 }
 
@@ -325,7 +319,7 @@ int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
   if (cache->batch == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
   const quest_cache_t c = shared_part(*cache);
-  const SpanLayout L = span_layout(c, true, 1, opts);
+  const SpanLayout L = span_layout(c, 1, opts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(c, ws, L, nullptr);
@@ -333,7 +327,6 @@ int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
   sp.mode = kSpanWindow;
   sp.sink = sink_tokens;
   sp.window = window;
-  sp.n_tokens = 1;
   return run_span(sp, true, window_pages(c, sink_tokens, window), opts, q, out, lse, stream,
                   "quest_narrow_window_decode");
 }
@@ -345,7 +338,7 @@ size_t quest_window_workspace_size(const quest_cache_t* cache, int32_t n_tokens,
     bad("n_tokens must be in [1, max_pages * page_size]");
     return 0;
   }
-  return span_layout(*cache, false, 0, opts, n_tokens).total;
+  return span_layout(*cache, 0, opts, n_tokens).total;
 }
 
 static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_tokens,
@@ -359,7 +352,7 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
     return bad("n_tokens must be in [0, max_pages * page_size]");
   if (cache->batch == 0 || n_tokens == 0) return QUEST_OK;
   if ((rc = check_io(q, out, lse))) return rc;
-  const SpanLayout L = span_layout(*cache, false, 0, opts, n_tokens);
+  const SpanLayout L = span_layout(*cache, 0, opts, n_tokens);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   SpanParams sp{};
   sp.p = make_params(*cache, ws, L, nullptr);
@@ -376,7 +369,6 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
   sp.mode = kSpanWindow;
   sp.sink = sink_tokens;
   sp.window = window;
-  sp.n_tokens = 1;
   return run_span(sp, false, window_pages(*cache, sink_tokens, window), opts, q, out, lse, stream,
                   what);
 }

@@ -36,10 +36,9 @@ namespace quest {
 
 namespace {
 
-constexpr int kSpanWarps = 8;
-constexpr int kSpanThreads = 32 * kSpanWarps;
-constexpr int kMaxSpanSplits = 64;
 constexpr int kSms = 152;  // of a GB300
+constexpr int kMaxSplitsSpan = 64;
+constexpr int kMinBlocks = 4;  // 16-token blocks of a split, at least
 constexpr float kBias = 8.f;
 constexpr float kLazy = 6.f;
 
@@ -318,54 +317,66 @@ __device__ __forceinline__ void accumulate(State& st, const Block<N8>& x, uint32
   }
 }
 
-// grid rows * n_splits (split fastest), kSpanThreads threads.  Split `s` of a row takes its
-// s-th share of the row's pages; warp w of the CTA every kSpanWarps-th page of it.
-template <bool N8>
-__global__ void __launch_bounds__(kSpanThreads, N8 ? 2 : 1) span_kernel(SpanParams sp) {
+// What a query token of sequence b attends over: `count` pages, in the row's order.
+struct RowShape {
+  Visible vis;
+  int L, N, n_sink, first, count;
+};
+
+__device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b) {
+  const Params& p = sp.p;
+  RowShape x;
+  x.L = step_len(p, b, p.seq_lens[b], kSiteSpan);
+  x.N = (x.L + p.P - 1) / p.P;
+  x.vis = Visible{x.L, 0, 0};
+  x.n_sink = x.first = 0;
+  x.count = x.N;
+  if (sp.mode == kSpanWindow) {
+    x.vis.lo = max(0, x.L - sp.window);
+    x.vis.sink_end = min(sp.sink, x.vis.lo);
+    x.first = x.vis.lo / p.P;
+    x.n_sink = min((x.vis.sink_end + p.P - 1) / p.P, x.first);
+    x.count = x.n_sink + x.N - x.first;
+  } else if (sp.mode == kSpanList) {
+    x.count = min(p.top_k, x.N);  // at most
+  }
+  return x;
+}
+
+// grid rows * n_splits (split fastest): split s of a row takes the s-th share of its pages,
+// warp w of the CTA every kSpanWarps-th page of that; a split row's parts are joined by the CTA
+// that comes last to it.
+template <bool N8, int kSpanWarps, int kCtas, int kDepth>
+__global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams sp) {
+  constexpr int kSpanThreads = 32 * kSpanWarps;
   __shared__ float s_m[kSpanWarps][8], s_l[kSpanWarps][8];
-  __shared__ float s_red[kSpanWarps][8 * kHeadDim];
+  __shared__ __align__(16) float s_red[kSpanWarps][8 * kHeadDim];
   __shared__ int s_flag;
   const Params& p = sp.p;
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();  // the next call's CTAs may take the places that this one's free
   const int split = (int)(blockIdx.x % (unsigned)p.n_splits);
-  const unsigned row = blockIdx.x / (unsigned)p.n_splits;  // (b * n_tokens + i) * Hkv + g
-  const int g = (int)(row % (unsigned)p.Hkv);
-  const int b = (int)(row / ((unsigned)p.Hkv * (unsigned)sp.n_tokens));
-  const int i_tok = (int)((row / (unsigned)p.Hkv) % (unsigned)sp.n_tokens);
+  const int row = (int)(blockIdx.x / (unsigned)p.n_splits);  // b * Hkv + g
+  const int b = row / p.Hkv, g = row % p.Hkv;
   const int G = p.Hq / p.Hkv, P = p.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 
-  // ---- the row's pages
-  const int L = load_len(p, b, kSiteSpan);
-  const int N = (L + P - 1) / P;
-  Visible vis;
-  vis.end = max(0, L - sp.n_tokens + i_tok + 1);
-  vis.lo = 0;
-  vis.sink_end = 0;
-  int n_sink = 0, first = 0, count = N;
+  const RowShape shape = row_shape(sp, b);
+  const int L = shape.L, N = shape.N, n_sink = shape.n_sink, first = shape.first;
+  const Visible vis = shape.vis;
+  int count = shape.count;
   const int* list = nullptr;
-  if (sp.mode == kSpanWindow) {
-    vis.lo = max(0, vis.end - sp.window);
-    vis.sink_end = min(sp.sink, vis.lo);
-    first = vis.lo / P;
-    n_sink = min((vis.sink_end + P - 1) / P, first);
-    count = vis.end > 0 ? n_sink + (vis.end + P - 1) / P - first : 0;
-  } else if (sp.mode == kSpanList) {
-    list = p.sel_idx + (size_t)row * p.top_k;  // n_tokens is 1: the row is (b, g)
-    count = p.sel_count[row];
-    const int cap = min(p.top_k, N);
-    if (count < 0 || count > cap) {
-      if (threadIdx.x == 0 && split == 0)
-        report(p, QUEST_ERR_BAD_SELECTION, b, count, kSiteSelection);
-      count = max(0, min(count, cap));
-    }
+  if (sp.mode == kSpanList) {
+    list = p.sel_idx + (size_t)row * p.top_k;
+    const int given = p.sel_count[row];
+    if ((given < 0 || given > count) && threadIdx.x == 0 && split == 0)
+      report(p, QUEST_ERR_BAD_SELECTION, b, given, kSiteSelection);
+    count = max(0, min(given, count));
   }
-  const int i0 = (int)((long long)count * split / p.n_splits);
-  const int i1 = (int)((long long)count * (split + 1) / p.n_splits);
+  const int i0 = count * split / p.n_splits, i1 = count * (split + 1) / p.n_splits;
 
   // ---- the query: head r of the group in lane (r, c)'s K Q^T columns
-  const size_t head0 = (size_t)(b * sp.n_tokens + i_tok) * p.Hq + (size_t)g * G;
+  const size_t head0 = (size_t)b * p.Hq + (size_t)g * G;
   uint32_t qf[8][2];
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
@@ -425,41 +436,60 @@ __global__ void __launch_bounds__(kSpanThreads, N8 ? 2 : 1) span_kernel(SpanPara
     // blocks of the pages to stream; a page that is not (unmapped, open) is left out
     unsigned live = __ballot_sync(0xffffffffu, ok == 1);
     if (!live) continue;
-    Block<N8> x;
-    int j = __ffs(live) - 1, sub = 0;
-    size_t off = ((size_t)__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * P * row_bytes;
-    load_k<N8>(x, k_pool + off, r, c);
-    load_v<N8>(x, v_pool + off, r, c);
-    while (true) {
-      const int t0 = __shfl_sync(0xffffffffu, lp, j) * P + 16 * sub;
-      const float kscale = __shfl_sync(0xffffffffu, ks, j);
-      const float vscale = N8 ? __shfl_sync(0xffffffffu, vs, j) : 1.f;
-      // the next block
+    // kDepth blocks on their way: K of the next one is asked for as soon as the scores are
+    // taken, V once the values are
+    Block<N8> x[kDepth];
+    struct Next {
+      size_t off;
+      int t0, valid;
+      float ks, vs;
+    } nx[kDepth];
+    int sub = 0;
+    auto take = [&]() {
+      Next n;
+      n.valid = live != 0u;
+      const int j = n.valid ? __ffs(live) - 1 : 0;
+      n.off = (((size_t)__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * P + 16 * sub) * row_bytes;
+      n.t0 = __shfl_sync(0xffffffffu, lp, j) * P + 16 * sub;
+      n.ks = N8 ? __shfl_sync(0xffffffffu, ks, j) : p.qscale;
+      n.vs = N8 ? __shfl_sync(0xffffffffu, vs, j) : 1.f;
       if (++sub == per_page) {
         sub = 0;
         live &= live - 1u;
       }
-      const bool more = live != 0u;
-      j = more ? __ffs(live) - 1 : 0;
-      const size_t next =
-          (((size_t)__shfl_sync(0xffffffffu, phys, j) * p.Hkv + g) * P + 16 * sub) * row_bytes;
-      float s[4];
-      scores<N8>(x, qf, s);
-      if (more) load_k<N8>(x, k_pool + next, r, c);
-      const bool whole = vis.all16(t0);
+      return n;
+    };
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] *= kscale;
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!vis.token(t0 + r + 8 * (i >> 1))) s[i] = -CUDART_INF_F;
-        zero_hidden<N8>(x, vis, t0, c);
+    for (int d = 0; d < kDepth; ++d) {
+      nx[d] = take();
+      if (nx[d].valid) {
+        load_k<N8>(x[d], k_pool + nx[d].off, r, c);
+        load_v<N8>(x[d], v_pool + nx[d].off, r, c);
       }
-      uint32_t h0, h1, l0, l1;
-      weigh(st, s, h0, h1, l0, l1);
-      accumulate<N8>(st, x, h0, h1, l0, l1, vscale);
-      if (!more) break;
-      load_v<N8>(x, v_pool + next, r, c);
+    }
+    while (nx[0].valid) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (nx[d].valid) {
+          const Next now = nx[d];
+          float s[4];
+          scores<N8>(x[d], qf, s);
+          nx[d] = take();
+          if (nx[d].valid) load_k<N8>(x[d], k_pool + nx[d].off, r, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] *= now.ks;
+          if (!vis.all16(now.t0)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!vis.token(now.t0 + r + 8 * (i >> 1))) s[i] = -CUDART_INF_F;
+            zero_hidden<N8>(x[d], vis, now.t0, c);
+          }
+          uint32_t h0, h1, l0, l1;
+          weigh(st, s, h0, h1, l0, l1);
+          accumulate<N8>(st, x[d], h0, h1, l0, l1, now.vs);
+          if (nx[d].valid) load_v<N8>(x[d], v_pool + nx[d].off, r, c);
+        }
+      }
     }
   }
   if (N8 && has_open) {
@@ -500,7 +530,8 @@ __global__ void __launch_bounds__(kSpanThreads, N8 ? 2 : 1) span_kernel(SpanPara
     }
   }
   __syncthreads();
-  const size_t slot0 = ((size_t)row * G) * p.n_splits;  // partials: [row][head][split]
+  const size_t slot0 = (size_t)row * p.n_splits * G;  // parts: [row][split][head]
+  const size_t mine = slot0 + (size_t)split * G;
   for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
     const int h = o / kHeadDim, d = o % kHeadDim;
     float M = -CUDART_INF_F, Z = 0.f, A = 0.f;
@@ -518,86 +549,121 @@ __global__ void __launch_bounds__(kSpanThreads, N8 ? 2 : 1) span_kernel(SpanPara
                                ? -CUDART_INF_F
                                : (M - kBias + log2f(Z)) * 0.6931471805599453f;
     } else {
-      const size_t slot = slot0 + (size_t)h * p.n_splits + split;
-      p.part_acc[slot * kHeadDim + d] = A;
+      p.part_acc[(mine + h) * kHeadDim + d] = A;
       if (d == 0) {
-        p.part_ml[2 * slot] = M;
-        p.part_ml[2 * slot + 1] = Z;
+        p.part_ml[2 * (mine + h)] = M;
+        p.part_ml[2 * (mine + h) + 1] = Z;
       }
     }
   }
-  if (p.n_splits == 1) return;
+  if (p.n_splits > 1) {
+    // ---- the last CTA of the row joins its parts
+    const int n = p.n_splits;
+    if (arrive_last<kSpanThreads, false>(&p.decode_arrive[row], (unsigned)n, &s_flag)) {
+      auto slot = [&](int s, int h) { return slot0 + (size_t)s * G + h; };
+      float* msc = &s_red[0][0];  // [G][n] scales
+      for (int h = warp; h < G; h += kSpanWarps) {
+        float M = -CUDART_INF_F, Z = 0.f;
+        for (int s = lane; s < n; s += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * slot(s, h)));
+        M = warp_max(M);
+        for (int s = lane; s < n; s += 32) {
+          const float ms = __ldcg(p.part_ml + 2 * slot(s, h));
+          const float f = ms == -CUDART_INF_F ? 0.f : exp2f(ms - M);
+          msc[h * n + s] = f;
+          Z = fmaf(__ldcg(p.part_ml + 2 * slot(s, h) + 1), f, Z);
+        }
+        Z = warp_sum(Z);
+        if (lane == 0) {
+          s_m[0][h] = M;
+          s_l[0][h] = Z;
+        }
+      }
+      __syncthreads();
+      for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
+        const int h = o / kHeadDim, d = o % kHeadDim;
+        float A = 0.f;
+        for (int s0 = 0; s0 < n; s0 += 8) {  // eight loads side by side, the last few too
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = s0 + e < n ? __ldcg(p.part_acc + slot(s0 + e, h) * kHeadDim + d) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) A = fmaf(x[e], s0 + e < n ? msc[h * n + s0 + e] : 0.f, A);
+        }
+        const float M = s_m[0][h], Z = s_l[0][h];
+        p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
+        if (d == 0 && p.lse)
+          p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
+                                                : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+      }
+      if (threadIdx.x == 0) p.decode_arrive[row] = 0u;
+    }
+  }
 
-  // ---- the last split of the row merges the partials
-  if (!arrive_last<kSpanThreads, false>(&p.decode_arrive[row], (unsigned)p.n_splits, &s_flag))
-    return;
-  float* msc = &s_red[0][0];  // [G][n_splits] scales, then per head Z and M
-  if (warp < G) {
-    const float* ml = p.part_ml + 2 * (slot0 + (size_t)warp * p.n_splits);
-    float M = -CUDART_INF_F, Z = 0.f;
-    for (int s = lane; s < p.n_splits; s += 32) M = fmaxf(M, __ldcg(ml + 2 * s));
-    M = warp_max(M);
-    for (int s = lane; s < p.n_splits; s += 32) {
-      const float ms = __ldcg(ml + 2 * s);
-      const float f = ms == -CUDART_INF_F ? 0.f : exp2f(ms - M);
-      msc[warp * p.n_splits + s] = f;
-      Z = fmaf(__ldcg(ml + 2 * s + 1), f, Z);
+  // ---- a step that appended: the last CTA of the launch (all have read the lengths by then)
+  // advances every sequence that had room and a mapped page for its token
+  if (p.chain_append && arrive_last<kSpanThreads, false>(p.exited, gridDim.x, &s_flag)) {
+    for (int b = threadIdx.x; b < p.B; b += kSpanThreads) {
+      const int L0 = p.seq_lens[b];
+      if (L0 >= 0 && (long long)L0 + 1 <= (long long)p.max_pages * P) {
+        const int phys = p.block_table[(size_t)b * p.max_pages + L0 / P];
+        if (phys >= 0 && phys < p.num_phys) p.seq_lens[b] = L0 + 1;
+      }
     }
-    Z = warp_sum(Z);
-    if (lane == 0) {
-      s_m[0][warp] = M;
-      s_l[0][warp] = Z;
-    }
+    if (threadIdx.x == 0) *p.exited = 0u;
   }
-  __syncthreads();
-  for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
-    const int h = o / kHeadDim, d = o % kHeadDim;
-    const float* pa = p.part_acc + (slot0 + (size_t)h * p.n_splits) * kHeadDim + d;
-    float A = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < p.n_splits; ++s) {
-      A = fmaf(__ldcg(pa + (size_t)s * kHeadDim), msc[h * p.n_splits + s], A);
-    }
-    const float M = s_m[0][h], Z = s_l[0][h];
-    p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
-    if (d == 0 && p.lse)
-      p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
-                                            : (M - kBias + log2f(Z)) * 0.6931471805599453f;
-  }
-  if (threadIdx.x == 0) p.decode_arrive[row] = 0u;
 }
 
 }  // namespace
 
-// With few rows a row's pages are shared by enough CTAs to fill the GPU once, each with at
-// least four pages a warp.
-static long long span_slots(bool narrow) { return (long long)kSms * (narrow ? 2 : 1); }
+// Launch shapes: warps of a CTA, CTAs that an SM holds, blocks in flight a warp.  A narrow
+// block is 32 registers a lane and leaves room for 16 warps of one block; an fp16 block is 64,
+// for 8 warps of two.  With more rows than SMs the fp16 rows get CTAs of four warps, two of
+// which share an SM: eight sequences of 32 heads with a 4K window took 85.6 us at 8 warps and
+// 81.4 at 4, one sequence of 8 heads over 64K tokens 48.4 at 8 and 55.2 at 4.
+struct SpanShape {
+  int warps, ctas;
+  const void* fn;
+};
 
-int span_splits(bool narrow, long long rows, int pages, int user_pps, int page_size) {
-  if (rows <= 0 || rows > kSplitRows) return 1;
-  long long s;
-  if (user_pps > 0) {
-    s = (pages + user_pps - 1) / user_pps;
-  } else {
-    const long long most = std::max(1, pages * (page_size / 16) / (4 * kSpanWarps));
-    s = std::min(most, span_slots(narrow) / rows);
-  }
-  return (int)std::max<long long>(1, std::min<long long>(s, kMaxSpanSplits));
+static SpanShape span_shape(bool narrow, long long rows) {
+  if (narrow) return {8, 2, (const void*)span_kernel<true, 8, 2, 1>};
+  if (rows > kSms) return {4, 2, (const void*)span_kernel<false, 4, 2, 2>};
+  return {8, 1, (const void*)span_kernel<false, 8, 1, 2>};
 }
 
-long long span_max_parts(bool narrow, long long rows, int pages, int user_pps, int page_size) {
-  rows = std::min<long long>(rows, kSplitRows);
-  if (user_pps > 0) return rows * span_splits(narrow, rows, pages, user_pps, page_size);
-  // fewer rows get more splits, up to the slots of the GPU together
-  return std::min(span_slots(narrow), rows * kMaxSpanSplits);
+// Splits of a row: as many as fit the GPU together with the other rows' in one wave, with a few
+// blocks for every split.  A second wave costs more than the places that stay empty in the
+// first (32 rows of 64K tokens: 96 us at 9 splits, 288 CTAs on 304 places, 143 us at 10), unless
+// two waves fill much better than one (64 rows: 84 % and 95 %; ragged ones took 86 us at 4
+// splits and 66 at 9).
+static int span_splits(const SpanParams& sp, const SpanShape& shape, int pages) {
+  const long long rows = (long long)sp.p.B * sp.p.Hkv;
+  if (rows > kSplitRows) return 1;
+  if (sp.run_pages)
+    return std::max(1, std::min((pages + sp.run_pages - 1) / sp.run_pages, kMaxSplitsSpan));
+  const long long slots = (long long)kSms * shape.ctas;
+  long long s = std::max<long long>(1, slots / rows);
+  const long long two = 2 * slots / rows;
+  if (rows * s * 100 < slots * 88 && rows * two * 100 >= 2 * slots * 94) s = two;
+  const int blocks = pages * (sp.p.P / 16);
+  return (int)std::max<long long>(1, std::min<long long>({s, blocks / kMinBlocks, kMaxSplitsSpan}));
 }
 
-cudaError_t launch_span(const SpanParams& sp, bool narrow, cudaStream_t s) {
+size_t span_max_parts(int batch, int hkv, bool user) {
+  const long long rows = (long long)batch * hkv;
+  if (rows > kSplitRows) return 0;
+  return user ? rows * kMaxSplitsSpan : std::min<long long>(rows * kMaxSplitsSpan, 4 * kSms);
+}
+
+cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s) {
+  const long long rows = (long long)sp.p.B * sp.p.Hkv;
+  const SpanShape shape = span_shape(narrow, rows);
   SpanParams pp = sp;
+  pp.p.n_splits = span_splits(sp, shape, pages);
   void* args[] = {&pp};
-  const long long rows = (long long)sp.p.B * sp.n_tokens * sp.p.Hkv;
-  const void* fn = narrow ? (const void*)span_kernel<true> : (const void*)span_kernel<false>;
-  return launch_pdl(fn, dim3((unsigned)(rows * sp.p.n_splits)), dim3(kSpanThreads), 0, s, args);
+  return launch_pdl(shape.fn, dim3((unsigned)(rows * pp.p.n_splits)), dim3(32 * shape.warps), 0, s,
+                    args);
 }
 
 }  // namespace quest

@@ -7,6 +7,11 @@ import query_aware_kv_gb300 as q
 import span_reference as R
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(0)
 BIG = 2 ** 31 - 1
 
 
