@@ -96,6 +96,8 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load libquest.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -156,9 +158,10 @@ def _check(rc: int) -> None:
         raise QuestError(rc, lib.quest_last_error().decode() or lib.quest_status_string(rc).decode())
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -166,6 +169,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+            (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -579,6 +585,7 @@ def narrow_prefill(cache: NarrowCache, k: torch.Tensor, v: torch.Tensor, ws: tor
     shape = (cache.batch, k.shape[1], cache.num_kv_heads, HEAD_DIM)
     _need(k, "k", torch.float16, shape)
     _need(v, "v", torch.float16, shape)
+    _here(cache)
     _check(load().quest_narrow_prefill(ctypes.byref(cache.desc), k.data_ptr(), v.data_ptr(),
                                        int(k.shape[1]), ws.data_ptr(), ws.numel(),
                                        _stream(stream)))
@@ -590,6 +597,7 @@ def narrow_append(cache: NarrowCache, k_new: torch.Tensor, v_new: torch.Tensor,
     shape = (cache.batch, cache.num_kv_heads, HEAD_DIM)
     _need(k_new, "k_new", torch.float16, shape)
     _need(v_new, "v_new", torch.float16, shape)
+    _here(cache)
     _check(load().quest_narrow_append(ctypes.byref(cache.desc), k_new.data_ptr(),
                                       v_new.data_ptr(), ws.data_ptr(), ws.numel(),
                                       _stream(stream)))
@@ -604,6 +612,7 @@ def narrow_sparse_decode(cache: NarrowCache, q: torch.Tensor, idx: torch.Tensor,
     _need(idx, "idx", torch.int32, (cache.batch, cache.num_kv_heads, top_k))
     _need(count, "count", torch.int32, (cache.batch, cache.num_kv_heads))
     out, lse = _out(cache, q, out, lse, want_lse)
+    _here(cache)
     _check(load().quest_narrow_sparse_decode(
         ctypes.byref(cache.desc), q.data_ptr(), idx.data_ptr(), count.data_ptr(), int(top_k),
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
@@ -643,11 +652,21 @@ def narrow_window_decode(cache: NarrowCache, q: torch.Tensor, sink_tokens: int, 
     return WindowPlan(cache, sink_tokens, window, ws, o, out, lse, want_lse, stream).decode(q)
 
 
+def _here(cache) -> None:
+    """The calls go to the current device's stream: the cache has to be on it."""
+    if cache.k_pool.get_device() != torch._C._cuda_getDevice():
+        raise ValueError("the cache is on another device than the current one")
+
+
 class NarrowPlan(DecodePlan):
     """``DecodePlan`` for a narrow cache: ``decode`` and ``step`` as there, ``dense`` for
     attention over every token."""
 
     _decode_fn, _step_fn = "quest_narrow_decode", "quest_narrow_decode_step"
+
+    def __init__(self, cache: NarrowCache, *args, **kw):
+        _here(cache)
+        super().__init__(cache, *args, **kw)
 
     def dense(self, q: torch.Tensor):
         """quest_narrow_dense_decode of this step's queries; returns (out, lse)."""
@@ -680,6 +699,7 @@ class WindowPlan:
     def __init__(self, cache, sink_tokens: int, window: int, ws: torch.Tensor,
                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
                  stream=None):
+        _here(cache)
         self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
         self._dev = cache.k_pool.get_device()
         probe = torch.empty(0, dtype=torch.float16, device=cache.k_pool.device)
@@ -730,6 +750,7 @@ def window_prefill(cache: PagedCache, q: torch.Tensor, sink_tokens: int, window:
         lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, shape[:3])
+    _here(cache)
     _check(load().quest_window_prefill(
         ctypes.byref(cache.desc), q.data_ptr(), int(shape[1]), int(sink_tokens), int(window),
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))

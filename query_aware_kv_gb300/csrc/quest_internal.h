@@ -229,6 +229,8 @@ int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps);
 cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s);
 cudaError_t launch_narrow_prefill(const Params& p, const NarrowPtrs& nar, const __half* k,
                                   const __half* v, int n, cudaStream_t s);
+// The estimate of a step that appends p.k_new / p.v_new (p.chain_append).
+cudaError_t launch_narrow_estimate(const Params& p, const NarrowPtrs& nar, int G, cudaStream_t s);
 cudaError_t launch_narrow_append(const Params& p, const NarrowPtrs& nar, const __half* k_new,
                                  const __half* v_new, cudaStream_t s);
 // Host checks shared with quest_api.cu (status code, error text set).

@@ -286,7 +286,68 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_append_kernel(Params p,
   }
 }
 
+// The page bounds of a decode step that appends: the estimate (as quest_estimate's, boxes
+// through L2), whose CTA that has the new token's page first lets a warp write the token and
+// its box, so that the step needs no launch of its own for them.  grid (scoring tiles, B * Hkv).
+// The lengths stay: every kernel of the step sees the token (chain_append), the last one
+// advances them.
+template <int G, int P>
+__global__ void __launch_bounds__(kConsumerThreads) narrow_estimate_kernel(Params p,
+                                                                           NarrowPtrs nar) {
+  pdl_wait();
+  const int tile = blockIdx.x, bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv;
+  bool appended = false;
+  const int L = load_len_step(p, b, kSiteScore, &appended);
+  const int N = (L + P - 1) / P;
+  const int p0 = tile * p.score_tile_pages;
+  const int np = min(p.score_tile_pages, p.max_pages - p0);
+  const int n_live = max(0, min(N - p0, np));
+  float* row = p.scores + (size_t)bg * p.max_pages + p0;
+  for (int i = n_live + (int)threadIdx.x; i < np; i += blockDim.x) row[i] = -CUDART_INF_F;
+  if (!appended) {
+    if ((long long)L == (long long)p.max_pages * P && tile == 0 && g == 0 && threadIdx.x == 0)
+      report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);  // no room for the new token
+  } else {
+    const int page = (L - 1) / P, slot = (L - 1) % P;
+    if (page >= p0 && page < p0 + n_live) {  // block-uniform
+      if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int phys = p.block_table[(size_t)b * p.max_pages + page];
+        const size_t in = ((size_t)b * p.Hkv + g) * kHeadDim;
+        if (phys < 0 || phys >= p.num_phys) {
+          if (lane == 0) report(p, QUEST_ERR_BAD_PAGE, b, page, kSiteAppend);
+        } else if (slot == P - 1) {
+          encode_page<P>(p, nar, b, g, page, phys, slot, p.k_new + in, p.v_new + in, 0, lane);
+        } else {
+          fill_open<P>(p, nar, b, g, page, slot, slot + 1, p.k_new + in, p.v_new + in, 0, lane);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (n_live > 0) score_tile<G, false, true>(p, b, g, p0, n_live, row, (size_t)p.max_pages);
+}
+
+template <int P>
+const void* narrow_estimate_fn(int G) {
+  switch (G) {
+    case 1: return (const void*)narrow_estimate_kernel<1, P>;
+    case 2: return (const void*)narrow_estimate_kernel<2, P>;
+    case 4: return (const void*)narrow_estimate_kernel<4, P>;
+    default: return (const void*)narrow_estimate_kernel<8, P>;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_narrow_estimate(const Params& p, const NarrowPtrs& nar, int G,
+                                   cudaStream_t s) {
+  Params pp = p;
+  NarrowPtrs np = nar;
+  void* args[] = {&pp, &np};
+  return launch_pdl(p.P == 16 ? narrow_estimate_fn<16>(G) : narrow_estimate_fn<32>(G),
+                    dim3(p.n_score_tiles, p.B * p.Hkv), dim3(kConsumerThreads), 0, s, args);
+}
 
 cudaError_t launch_narrow_prefill(const Params& p, const NarrowPtrs& nar, const __half* k,
                                   const __half* v, int n, cudaStream_t s) {

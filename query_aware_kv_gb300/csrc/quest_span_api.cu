@@ -193,11 +193,12 @@ int narrow_decode(const quest_narrow_cache_t* cache, const void* q, const void* 
   if (count_out) sp.p.sel_count = count_out;
   sp.p.top_k = top_k;
   sp.p.q = static_cast<const __half*>(q);
-  cudaError_t e = cudaSuccess;
-  if (k_new)
-    e = launch_narrow_append(sp.p, sp.nar, static_cast<const __half*>(k_new),
-                             static_cast<const __half*>(v_new), s);
-  if (e == cudaSuccess) e = launch_estimate(sp.p, group_of(c), false, s);
+  // a step that appends writes the token in the estimate and advances the lengths at its end
+  sp.p.k_new = static_cast<const __half*>(k_new);
+  sp.p.v_new = static_cast<const __half*>(v_new);
+  sp.p.chain_append = k_new ? 1 : 0;
+  cudaError_t e = k_new ? launch_narrow_estimate(sp.p, sp.nar, group_of(c), s)
+                        : launch_estimate(sp.p, group_of(c), false, s);
   if (e == cudaSuccess) e = launch_topk(sp.p, s);
   if (e != cudaSuccess) return launched(e, what);
   return run_span(sp, true, std::min(top_k, c.max_pages), opts, q, out, lse, stream, what);
