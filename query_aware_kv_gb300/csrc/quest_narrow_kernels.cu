@@ -172,12 +172,25 @@ __device__ __forceinline__ void fill_open(const Params& p, const NarrowPtrs& nar
   box.any = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) box.mn[i] = box.mx[i] = __float2half2_rn(0.f);
-  for (int t = s0 + hw; t < e; t += 2) {
-    const uint4 kk = *reinterpret_cast<const uint4*>(k + (size_t)(t - s0) * stride + 8 * c);
-    const uint4 vv = *reinterpret_cast<const uint4*>(v + (size_t)(t - s0) * stride + 8 * c);
-    *reinterpret_cast<uint4*>(nar.k_open + open + t * kHeadDim) = kk;
-    *reinterpret_cast<uint4*>(nar.v_open + open + t * kHeadDim) = vv;
-    widen_box(box, kk);
+  constexpr int R = 4;  // rows of a half-warp on their way together
+#pragma unroll 1
+  for (int tb = s0 + hw; tb < e; tb += 2 * R) {
+    uint4 kk[R], vv[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const size_t at = (size_t)(min(tb + 2 * i, e - 1) - s0) * stride + 8 * c;
+      kk[i] = *reinterpret_cast<const uint4*>(k + at);
+      vv[i] = *reinterpret_cast<const uint4*>(v + at);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int t = tb + 2 * i;
+      if (t < e) {
+        *reinterpret_cast<uint4*>(nar.k_open + open + t * kHeadDim) = kk[i];
+        *reinterpret_cast<uint4*>(nar.v_open + open + t * kHeadDim) = vv[i];
+        widen_box(box, kk[i]);
+      }
+    }
   }
   store_box(p, box, b, g, page, s0 > 0, lane);
 }
@@ -190,6 +203,7 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_pages_kernel(Params p, 
                                                                       const __half* k,
                                                                       const __half* v, int n) {
   pdl_wait();
+  pdl_trigger();
   const int b = blockIdx.z, lane = threadIdx.x & 31;
   const int g = blockIdx.x * kNarrowWarps + (threadIdx.x >> 5);
   const int L = p.seq_lens[b];
@@ -213,25 +227,32 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_open_kernel(Params p, N
                                                                      const __half* k,
                                                                      const __half* v, int n) {
   __shared__ int s_flag;
-  pdl_wait();
+  // (nothing read before the wait is written by the pages' kernel, which starts this one only
+  // after its own wait)
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int g = blockIdx.x * kNarrowWarps + (threadIdx.x >> 5);
   const int L = p.seq_lens[b];
   const bool fits = L >= 0 && (long long)L + n <= (long long)p.max_pages * P;
-  int bad = 0;
+  int bad = -1;  // a touched page that is not mapped
   if (fits) {
     const int last = (L + n - 1) / P;
-    for (int pg = L / P + (int)threadIdx.x; pg <= last; pg += kNarrowThreads) {
-      const int phys = p.block_table[(size_t)b * p.max_pages + pg];
-      if (phys < 0 || phys >= p.num_phys) {
-        if (blockIdx.x == 0) report(p, QUEST_ERR_BAD_PAGE, b, pg, kSiteAppend);
-        bad = 1;
-      }
+    const int* table = p.block_table + (size_t)b * p.max_pages;
+    // eight entries a thread on their way together (one at a time, a 32K prompt's 2048 entries
+    // took 10 us)
+    for (int pg = L / P + (int)threadIdx.x; pg <= last; pg += 8 * kNarrowThreads) {
+      int phys[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) phys[i] = table[min(pg + i * kNarrowThreads, last)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (phys[i] < 0 || phys[i] >= p.num_phys) bad = min(pg + i * kNarrowThreads, last);
     }
+    if (bad >= 0 && blockIdx.x == 0) report(p, QUEST_ERR_BAD_PAGE, b, bad, kSiteAppend);
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
     report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);
   }
-  const bool ok = fits && !__syncthreads_or(bad);
+  pdl_wait();
+  const bool ok = fits && !__syncthreads_or(bad >= 0);
   const int e = ok ? (L + n) % P : 0;
   if (e > 0 && g < p.Hkv) {
     const int page = (L + n) / P;
