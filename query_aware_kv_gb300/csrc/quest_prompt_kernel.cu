@@ -236,7 +236,6 @@ struct Bars {
   // S of query tile t and K / V tile j is in s_full[t][j & 1]; its completion also says that
   // Q K^T (t, j) and P V (t, j - 1) have read their K and V tiles
   uint64_t s_full[2][2], p_full[2], o_full[2], drain[2];
-  uint64_t turn[2];  // the issue warp of tile t may issue its next group of products
   uint32_t tmem;
   int give_up;
 };
@@ -310,6 +309,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = pp.log_g, G = 1 << lg, TT = kTileRows >> lg;  // tokens of a query tile
 
+  const int blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
+  const int n = pp.n_tokens, tok0 = blk * 2 * TT;
+  const int tok1 = min(n, tok0 + 2 * TT);
+  const bool two = tok1 - tok0 > TT;
+  const int n_q = two ? 2 : 1;  // query tiles with rows
+
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
     for (int i = 0; i < kKvStages; ++i) {
@@ -319,8 +324,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&bars.s_full[t][0], 1);
       mbar_init(&bars.s_full[t][1], 1);
       mbar_init(&bars.drain[t], 1);
-      mbar_init(&bars.turn[t], 1);
-      mbar_init(&bars.p_full[t], 4);
+      mbar_init(&bars.p_full[t], two ? 5 : 4);
       mbar_init(&bars.o_full[t], 1);
     }
     bars.give_up = 0;
@@ -340,11 +344,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   // ---- the CTA's work
   const int split = (int)blockIdx.x % p.n_splits;
-  const int blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
   const int g = (int)blockIdx.y, b = (int)blockIdx.z;
-  const int n = pp.n_tokens, tok0 = blk * 2 * TT;
-  const int tok1 = min(n, tok0 + 2 * TT);
-  const int n_q = tok1 - tok0 > TT ? 2 : 1;  // query tiles with rows
   if (warp == 8 && elect_lane()) {  // the queries' place does not depend on the length
     mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
     for (int i = 0; i < 2 * n_q; ++i)
@@ -465,6 +465,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       };
       bool ok = wait(&bars.q_full, 0) && wait(&bars.kv_full[0], 0);
       fence_after();
+      // The two tiles' groups of products, P V (j) with Q K^T (j + 1), take turns: side by side
+      // they end together, the two softmaxes then run together too, and nothing overlaps (a
+      // tile pair took 4200 cycles so, against 3100 in turns).  The turn is the fifth arrival on
+      // p_full, beside the softmax warps': one wait for both.
+      if (two && t == 0 && lane == 0) mbar_arrive(&bars.p_full[0]);
       if (ok) qk(0, &bars.s_full[t][0]);
       int sv = 1, sk = 2;  // stages of the V and the next K tile
       uint32_t round_v = 0, round_k = 0;
@@ -496,12 +501,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           __syncwarp();
         }
         if (!(ok = wait(&bars.p_full[t], (j - j0) & 1))) break;
-        // The two tiles' groups of products, P V (j) with Q K^T (j + 1), take turns: side by side
-        // they end together, the two softmaxes then run together too, and nothing overlaps (a
-        // tile pair took 4200 cycles so, against 2750 in turns).
-        if (n_q > 1 && (t == 1 || j > j0) &&
-            !(ok = wait(&bars.turn[t], (uint32_t)(j - j0 - (t == 0)) & 1)))
-          break;
         fence_after();
         if (elect_lane()) {
 #pragma unroll
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
         if (more) qk(sk, &bars.s_full[t][(j - j0 + 1) & 1]);
-        if (n_q > 1 && lane == 0) mbar_arrive(&bars.turn[t ^ 1]);
+        if (two && lane == 0) mbar_arrive(&bars.p_full[t ^ 1]);
         __syncwarp();
         if ((sv += 2) >= kKvStages) {
           sv -= kKvStages;
