@@ -38,11 +38,11 @@ namespace quest {
 namespace {
 
 // Three warpgroups: the softmax of either tile, and the fetch warps (8: Q and K, 10: V) with the
-// issue warps (9 and 11, a query tile each).  Registers: 384 x 168 at launch, then 216 for the
-// softmax threads (a row of 128 scores each) and 72 for the others, the same total.
+// issue warps (9 and 11, a query tile each).  168 registers a thread hold a softmax row's 128
+// scores half by half without a spill; moving registers from the third warpgroup to the others
+// made the compiler spill in all of them (a few bytes cost 4 %: local memory waits behind the
+// tensor core's reads of shared memory).
 constexpr int kPromptThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers of the launch");
 constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
@@ -186,8 +186,7 @@ constexpr uint32_t kIdescQK = 1u << 4 | (kTileTokens >> 3) << 17 | (kTileRows >>
 constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kTileRows >> 4) << 24;
 
 // ---- bounded waits: a wait that runs out sets the CTA's give-up flag, and everyone leaves
-// (Everything this kernel calls is inlined: around a call the compiler keeps to the registers
-// that the smallest warpgroup has, and a row of scores would spill.)
+// (Everything this kernel calls is inlined: no call makes the compiler save registers.)
 __device__ __forceinline__ void record(const Params& p, int code, int b, int page) {
   if (atomicCAS(p.status, 0, code) == 0) {
     p.status[1] = b;
@@ -295,6 +294,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ bool not_finite(const uint32_t* o) {
+  bool x = false;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x |= (o[k] & 0x7f800000u) == 0x7f800000u;
+  return x;
+}
+
 template <int P>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
@@ -367,11 +373,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     list.count = list.n_sink + (end + P - 1) / P - list.first;
   }
   const int tiles = (list.count + PPT - 1) / PPT;
-  const int j0 = (int)((long long)tiles * split / p.n_splits);
-  const int j1 = (int)((long long)tiles * (split + 1) / p.n_splits);
+  const int j0 = tiles * split / p.n_splits, j1 = tiles * (split + 1) / p.n_splits;
 
+  bool again = false;
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8 || warp == 10) {
     // ---- fetch: warp 8 the K tiles (the queries are on their way), warp 10 the V tiles
     const int kv = warp == 10;
@@ -533,7 +538,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   } else {
     // ---- softmax: a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2, row = threadIdx.x & 127;
     const int tok = tok0 + t * TT + (row >> lg);
     const int pr = pos0 + tok;  // the row's position
@@ -602,22 +606,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // replaced yet.
         float top;
         {
-          float s[kTileTokens];
+          float best[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            tmem_ld32(s_col + 32 * u, reinterpret_cast<uint32_t*>(s) + 32 * u);
-          tmem_wait_ld();
-          // four chains of three-input maxima: one chain of 127 would wait on itself
-          float t4[4] = {s[0], s[1], s[2], s[3]};
+          for (int h = 0; h < 2; ++h) {
+            float s[64];
+            tmem_ld32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
+            tmem_ld32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
+            tmem_wait_ld();
+            // four chains of three-input maxima: one chain of 127 would wait on itself
 #pragma unroll
-          for (int k = 4; k + 8 <= kTileTokens; k += 8)
+            for (int k = 0; k < 64; k += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[k + e], s[k + 4 + e]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kTileTokens - 4 + e]);
-          top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.qscale;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) weigh(s + 32 * u, u);
+              for (int e = 0; e < 4; ++e) best[e] = max3(best[e], s[k + e], s[k + 4 + e]);
+            weigh(s, 2 * h);
+            weigh(s + 32, 2 * h + 1);
+          }
+          top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * p.qscale;
         }
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float mn = fmaxf(m, top);
@@ -664,6 +668,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       fence_after();
       const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
       const bool mine = tok < tok1;
+      bool odd = false;  // some of the row's O is not finite
       if (ok && p.n_splits == 1) {
         // ---- out = O / l, through the tile's own query space (its products are done): a row
         // of 256 B per thread goes to shared memory, two rows at a time leave as whole lines
@@ -676,6 +681,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (j1 > j0) {
             tmem_ld32(o_col + 32 * u, o);
             tmem_wait_ld();
+            odd |= not_finite(o);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -711,6 +717,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (j1 > j0) {
             tmem_ld32(o_col + 32 * u, o);
             tmem_wait_ld();
+            odd |= not_finite(o);
           }
           if (mine) {
 #pragma unroll
@@ -725,12 +732,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           p.part_ml[2 * slot + 1] = l;
         }
       }
+      // (m and l of a row that has to be taken again, below; the K / V tiles are done with)
+      if (ok && mine && j1 > j0 && odd && !none && l <= 3.4e38f) {
+        again = true;
+        *reinterpret_cast<float2*>(smem + PromptSmem::kv + 8 * (t * kTileRows + row)) =
+            make_float2(m, l);
+      } else {
+        *reinterpret_cast<float2*>(smem + PromptSmem::kv + 8 * (t * kTileRows + row)) =
+            make_float2(0.f, -1.f);
+      }
     }
   }
   fence_before();
-  __syncthreads();
+  const bool any_again = __syncthreads_or(again);
   fence_after();
   if (warp == 9) tmem_free(tmem);
+
+  // An infinity or NaN among the values of a tile reaches all of its rows, as 0 * NaN, those too
+  // that do not see its token.  Such a row (its scores are finite, its O is not) is taken again
+  // from what it sees, by a warp, a token at a time.
+  if (any_again) {
+    const float2* stash = reinterpret_cast<const float2*>(smem + PromptSmem::kv);
+    for (int r = warp; r < (tok1 - tok0) * G; r += kPromptThreads / 32) {
+      const float m_r = stash[r].x, l_r = stash[r].y;
+      if (l_r < 0.f) continue;  // warp-uniform
+      const int pos_r = pos0 + tok0 + (r >> lg);
+      const size_t at = (((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) +
+                         (r & (G - 1))) * kHeadDim + 4 * lane;
+      const uint2 qw = *reinterpret_cast<const uint2*>(p.q + at);
+      const float2 qa = h2f(qw.x), qb = h2f(qw.y);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const int last = min(j1 * PPT, list.count);
+#pragma unroll 1
+      for (int e = j0 * PPT; e < last; ++e) {
+        const int lp = list.page(e);
+        const int phys = p.block_table[(size_t)b * p.max_pages + lp];
+        if (phys < 0 || phys >= p.num_phys) continue;
+        const size_t from = ((size_t)phys * p.Hkv + g) * P * kHeadDim + 4 * lane;
+#pragma unroll 4
+        for (int k = 0; k < P; ++k) {
+          const int pos = lp * P + k;
+          if (pos > pos_r || (pos >= pp.sink && pos <= pos_r - pp.window)) continue;
+          const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + from + k * kHeadDim);
+          const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + from + k * kHeadDim);
+          const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
+          const float x = warp_sum(fmaf(qa.x, ka.x, qa.y * ka.y) + fmaf(qb.x, kb.x, qb.y * kb.y));
+          const float w = ex2(fmaf(x, p.qscale, kBias - m_r));
+          acc[0] = fmaf(w, va.x, acc[0]);
+          acc[1] = fmaf(w, va.y, acc[1]);
+          acc[2] = fmaf(w, vb.x, acc[2]);
+          acc[3] = fmaf(w, vb.y, acc[3]);
+        }
+      }
+      if (p.n_splits == 1)
+        *reinterpret_cast<uint2*>(p.out + at) =
+            make_uint2(pack2(acc[0] / l_r, acc[1] / l_r), pack2(acc[2] / l_r, acc[3] / l_r));
+      else
+        *reinterpret_cast<float4*>(p.part_acc + (part_slot(pp, split) + r) * kHeadDim + 4 * lane) =
+            make_float4(acc[0], acc[1], acc[2], acc[3]);
+    }
+  }
   if (p.n_splits == 1) return;
 
   // ---- the last split of the work item joins the shares

@@ -169,6 +169,39 @@ def test_hidden_tokens_do_not_reach_a_result(value):
         check(cache, qq, out, lse, sink, window, True)
 
 
+@pytest.mark.parametrize("n", [40, 300])
+@pytest.mark.parametrize("pps", [0, 3])
+def test_odd_values_reach_only_the_rows_that_see_them(n, pps):
+    """A NaN and an infinity among the values: rows before them, and rows whose window has
+    passed them, are as if they were 0; the others are not finite there."""
+    sink, window, L = 3, 70, 700
+    cache = make([L], 8, 2, 16, seed=14)
+    o = q.opts(pages_per_split=pps)
+    ws = q.window_workspace(cache, n, o)
+    qq = torch.randn((1, n, 8, 128), device="cuda").half()
+    clean = cache.v_pool.clone()
+    at = [(L - n + 9, 5, float("nan")), (L - 25, 77, float("inf"))]
+    for t, d, value in at:
+        cache.v_pool[int(cache.block_table[0, t // 16]), :, t % 16, d] = value
+    out, lse = q.window_prefill(cache, qq, sink, window, ws, o)
+    ok(ws)
+    cache.v_pool.copy_(clean)
+    for t, d, _ in at:
+        cache.v_pool[int(cache.block_table[0, t // 16]), :, t % 16, d] = 0
+    allowed = R.window_mask(L, n, sink, window, "cuda")
+    for g in range(2):
+        k, v = logical(cache, 0, g, "k_pool"), logical(cache, 0, g, "v_pool")
+        for h in range(g * 4, g * 4 + 4):
+            got = out[0, :, h].clone()
+            ref = R.attend(qq[0, :, h], k, v, allowed)
+            for t, d, _ in at:
+                sees = allowed[:, t]
+                assert not torch.isfinite(got[sees, d]).any()
+                assert torch.isfinite(got[~sees, d]).all()
+                got[sees, d] = ref[0][sees, d].half()
+            R.assert_close(got, lse[0, :, h], ref, True)
+
+
 def test_large_scores_and_values():
     """Scores far from 0 (both signs) and a maximum that comes last: the running maximum
     moves, small weights vanish."""
