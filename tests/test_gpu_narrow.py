@@ -389,3 +389,77 @@ def test_selection_is_that_of_the_fp16_cache():
         sel.append((idx, out, lse))
     assert torch.equal(narrow.meta, wide.meta)
     assert torch.equal(sel[0][0], sel[1][0])
+
+
+def test_rows_behind_the_open_page_are_left_as_they_were():
+    P = 16
+    cache = empty(1, 2, 2, P, 6, seed=4)
+    ws = q.narrow_workspace(cache)
+    k, v = tokens(1, 60, 2, seed=31)
+    at = 0
+    for n in (5, 3, 20, 1):
+        before = cache.k_open.clone(), cache.v_open.clone()
+        q.narrow_prefill(cache, k[:, at:at + n].contiguous().cuda(), v[:, at:at + n].contiguous().cuda(), ws)
+        at += n
+        rows = at % P
+        for now, was in ((cache.k_open, before[0]), (cache.v_open, before[1])):
+            assert torch.equal(now[0, :, rows:].view(torch.int16), was[0, :, rows:].view(torch.int16))
+    q.narrow_append(cache, k[:, at].contiguous().cuda(), v[:, at].contiguous().cuda(), ws)
+    ok(ws)
+    assert int(cache.seq_lens[0]) == 30
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond the first 4 GiB of each pool: written, then read."""
+    hkv, P, hq, L = 8, 32, 16, 300
+    nph = (5 << 30) // (hkv * P * 128)
+    pages = -(-L // P) + 1
+    bt = torch.arange(nph - pages, nph, device="cuda").int().flip(0)[None].contiguous()
+    cache = q.NarrowCache.allocate(nph, hkv, P, bt, torch.zeros(1, dtype=torch.int32, device="cuda"), hq)
+    ws = q.narrow_workspace(cache)
+    k, v = tokens(1, L, hkv, seed=41)
+    q.narrow_prefill(cache, k.cuda(), v.cuda(), ws)
+    ok(ws)
+    ref = R.NarrowReference(1, hkv, P)
+    ref.write(k, v)
+    assert_cache(cache, ref)
+    qq = torch.randn((1, hq, 128), device="cuda").half()
+    out, lse = q.narrow_dense_decode(cache, qq, ws)
+    ok(ws)
+    check(cache, ref, qq, out, lse, lambda b, g: torch.ones((1, L), dtype=torch.bool))
+
+
+def test_hidden_and_unwritten_slots_hold_anything():
+    """NaN codes and scales in pages and slots that no call may read as tokens."""
+    cache, ref = filled((8, 2, 32), [500, 90])
+    lo = 500 - 70
+    at = cache.block_table.long()
+    pool = cache.k_pool.view(torch.uint8), cache.v_pool.view(torch.uint8)
+    for t in range(lo // 32 * 32, lo):  # before the window, in its first page
+        for x in pool:
+            x[at[0, t // 32], :, t % 32] = 0x7f
+    for p in range(1, lo // 32):  # between the sinks and the window
+        cache.k_scale[at[0, p]] = float("nan")
+        cache.v_scale[at[0, p]] = float("nan")
+    ws = q.narrow_workspace(cache)
+    qq = torch.randn((2, 8, 128), device="cuda").half()
+    out, lse = q.narrow_window_decode(cache, qq, 4, 70, ws)
+    ok(ws)
+    check(cache, ref, qq, out, lse, lambda b, g: R.window_mask(ref.length(b), 1, 4, 70, "cpu"))
+
+
+def test_a_step_without_room_keeps_its_length():
+    cache, ref = filled((4, 4, 16), [64, 20], pages=4)
+    ws = q.narrow_workspace(cache, 3)
+    kn, vn = (x[:, 0].cuda() for x in tokens(2, 1, 4, seed=1))
+    qq = torch.randn((2, 4, 128), device="cuda").half()
+    q.narrow_decode_step(cache, qq, kn, vn, 3, ws)
+    rc, detail = q.read_status(ws)
+    assert rc == q.QUEST_ERR_BAD_LENGTH and detail[0] == 0
+    assert cache.seq_lens.tolist() == [64, 21]
+    q.workspace_init(ws)
+    cache.block_table[1, 1] = cache.k_pool.shape[0]
+    q.narrow_decode_step(cache, qq, kn, vn, 3, ws)
+    rc, _ = q.read_status(ws)
+    assert rc in (q.QUEST_ERR_BAD_LENGTH, q.QUEST_ERR_BAD_PAGE)
+    assert cache.seq_lens.tolist() == [64, 21]

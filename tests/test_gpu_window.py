@@ -299,3 +299,47 @@ def test_empty_batch_and_no_lse():
     assert torch.equal(a, b)
     out, lse = q.window_prefill(cache, qq[:, :0].contiguous(), 0, 9, ws)
     assert out.numel() == 0 and lse.numel() == 0
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond the first 4 GiB of each pool, and the last page of it."""
+    hkv, P, hq, L, n = 8, 32, 16, 300, 20
+    nph = (5 << 30) // (hkv * P * 128 * 2)
+    k = torch.empty((nph, hkv, P, 128), dtype=torch.float16, device="cuda")
+    v = torch.empty_like(k)
+    pages = -(-L // P)
+    bt = torch.arange(nph - pages, nph, device="cuda").int().flip(0)[None].contiguous()
+    k[-pages:] = torch.randn((pages, hkv, P, 128), device="cuda").half()
+    v[-pages:] = torch.randn((pages, hkv, P, 128), device="cuda").half()
+    cache = q.PagedCache.allocate_meta(k, v, bt, torch.tensor([L], dtype=torch.int32).cuda(), hq)
+    ws = q.window_workspace(cache, n)
+    qq = torch.randn((1, n, hq, 128), device="cuda").half()
+    out, lse = q.window_prefill(cache, qq, 4, 90, ws)
+    ok(ws)
+    check(cache, qq, out, lse, 4, 90, True)
+    out, lse = q.window_decode(cache, qq[:, -1].contiguous(), 4, 90, ws)
+    ok(ws)
+    check(cache, qq[:, -1:], out[:, None], lse[:, None], 4, 90, False)
+
+
+@pytest.mark.parametrize("batch,hkv", [(20, 8), (70, 16)], ids=["160_rows", "1120_rows"])
+def test_many_rows(batch, hkv):
+    """More rows than SMs (CTAs of four warps), and more than are ever split."""
+    lens = [(37 * b) % 211 for b in range(batch)]
+    cache = make(lens, hkv, hkv, 16, seed=15)
+    ws = q.window_workspace(cache)
+    qq = torch.randn((batch, hkv, 128), device="cuda").half()
+    out, lse = q.window_decode(cache, qq, 3, 50, ws)
+    ok(ws)
+    check(cache, qq[:, None], out[:, None], lse[:, None], 3, 50, False)
+
+
+def test_one_workspace_for_every_length():
+    """A workspace sized for a long chunk serves shorter ones, split or not, in any order."""
+    cache = make([1500, 800], 8, 2, 16, seed=16)
+    ws = q.window_workspace(cache, 600)
+    for n in (600, 1, 7, 300, 1, 600, 40):
+        qq = torch.randn((2, n, 8, 128), device="cuda").half()
+        out, lse = q.window_prefill(cache, qq, 4, 900, ws)
+        ok(ws)
+        check(cache, qq, out, lse, 4, 900, True)

@@ -133,3 +133,26 @@ def test_window_mask_by_hand():
                           [True, False, False, True, True, False],
                           [True, False, False, False, True, True]]
     assert R.window_mask(1, 3, 4, 9, "cpu").tolist() == [[False], [False], [True]]
+
+
+def test_binding_refuses_what_is_not_a_cuda_cache():
+    """Tensors of the host, another type, another shape or another order are refused before any
+    call of the library."""
+    bt, sl = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        q.NarrowCache.allocate(4, 2, 16, bt, sl, 4)
+    from query_aware_kv_gb300 import _lib
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        _lib._need([1], "q", torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        _lib._need(torch.zeros(2, dtype=torch.float16), "q", torch.float16)
+
+
+def test_workspaces_do_not_shrink_with_more_tokens(lib):
+    """A workspace for n query tokens holds what fewer need; options that split more need more."""
+    d = ctypes.byref(desc(batch=2, num_q_heads=8, num_kv_heads=4))
+    sizes = [lib.quest_window_workspace_size(d, n, None) for n in (1, 2, 5, 31, 64, 300, 1000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    assert lib.quest_window_workspace_size(d, 5, ctypes.byref(q.opts(pages_per_split=1))) >= sizes[2]
+    n = ctypes.byref(narrow())
+    assert lib.quest_narrow_workspace_size(n, 64, None) > lib.quest_narrow_workspace_size(n, 1, None)
