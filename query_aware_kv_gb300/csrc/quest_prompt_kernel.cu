@@ -14,17 +14,24 @@
 //   P = 2^(S c - m + 8)  the tile's 128 softmax threads, one row each (no shuffles), written
 //                        back over S as fp16
 //   O += P V             tcgen05.mma, P from TMEM, V in shared memory (MN-major), O in TMEM
-// Warps 0-3 and 4-7 are the softmax of the two tiles, warps 8 and 10 fetch, warps 9 and 11 issue the
-// products of a tile each: while one tile is in its softmax, the tensor core works for the other.  The order of
-// issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's columns.
+// Warps 0-3 and 4-7 are the softmax of the two tiles, warps 8 and 10 fetch, warps 9 and 11
+// issue the products of a tile each: while one tile is in its softmax, the tensor core works
+// for the other.  The order of issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's
+// columns.  Few query rows leave most SMs without work, so then the K / V tiles of a work item
+// are shared by several CTAs, whose shares the last one joins.
 // The maximum m moves only when a row exceeds it by more than 2^6 (then O is rescaled in
 // TMEM by the softmax threads themselves), so weights reach 2^14 at most and keep fp16's full
 // precision down to 2^-22 of the largest.  P enters the second product as one fp16 number:
 // a rounding of 2^-11 per weight, random in sign, against the final rounding to fp16 of the
 // same size; its sum l is taken in fp32 before that rounding.
 //
-// What bounds it: the tensor core and the exponentials together.  A tile pair is 4 products
-// of 128 x 128 x 128 (1024 cycles at the dense rate) and 2 * 128 * 128 exponentials.
+// What bounds it: the chain softmax -> P V -> Q K^T -> softmax of a tile.  A tile pair is 4
+// products of 128 x 128 x 128 (2048 cycles at the dense rate) and 2 * 128 * 128 exponentials
+// (1024 cycles); a tile's softmax takes 1100 cycles, its two products 1024, and each of the two
+// hand-overs through a barrier some 300, so a pair takes about 2700, the tensor core busy for
+// three quarters of them.  Measured: an 8K prompt of 32 heads with a 4K window 331 us (1.24
+// PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 104 us (1.32), five tokens over a 32K
+// window 38 us (3.5 TB/s).
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -378,71 +385,70 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   bool again = false;
   if (warp >= 8) {
     if (warp == 8 || warp == 10) {
-    // ---- fetch: warp 8 the K tiles (the queries are on their way), warp 10 the V tiles
-    const int kv = warp == 10;
-    if (j1 > j0) {
-      // 32 pages of the list at a time, a page per lane, the next 32 on their way; entries
-      // behind the list's end repeat its last page (their tokens are hidden)
-      auto entry = [&](int i) {
-        return p.block_table[(size_t)b * p.max_pages + list.page(min(i, list.count - 1))];
-      };
-      auto checked = [&](int phys, int i) {
-        if (phys >= 0 && phys < p.num_phys) return phys;
-        record(p, QUEST_ERR_BAD_PAGE, b, list.page(min(i, list.count - 1)));
-        return 0;
-      };
-      int now = entry(j0 * PPT + lane), next = entry(j0 * PPT + 32 + lane);
-      now = checked(now, j0 * PPT + lane);
-      int st = kv;
-      bool ok = true;
-      int fetched = 0;
-      for (int j = j0; j < j1; ++j) {
-        const int at = (j - j0) * PPT & 31;
-        if (at == 0 && j > j0) {
-          now = checked(next, j * PPT + lane);
-          next = entry(j * PPT + 32 + lane);
+      // ---- fetch: warp 8 the K tiles (the queries are on their way), warp 10 the V tiles
+      const int kv = warp == 10;
+      if (j1 > j0) {
+        // 32 pages of the list at a time, a page per lane, the next 32 on their way; entries
+        // behind the list's end repeat its last page (their tokens are hidden)
+        auto entry = [&](int i) {
+          return p.block_table[(size_t)b * p.max_pages + list.page(min(i, list.count - 1))];
+        };
+        auto checked = [&](int phys, int i) {
+          if (phys >= 0 && phys < p.num_phys) return phys;
+          record(p, QUEST_ERR_BAD_PAGE, b, list.page(min(i, list.count - 1)));
+          return 0;
+        };
+        int now = entry(j0 * PPT + lane), next = entry(j0 * PPT + 32 + lane);
+        now = checked(now, j0 * PPT + lane);
+        int st = kv;
+        bool ok = true;
+        int fetched = 0;
+        for (int j = j0; j < j1; ++j) {
+          const int at = (j - j0) * PPT & 31;
+          if (at == 0 && j > j0) {
+            now = checked(next, j * PPT + lane);
+            next = entry(j * PPT + 32 + lane);
+          }
+          // K (j) takes the stage of V (j - 3), V (j) that of K (j - 2): both are free once
+          // the scores of tile j - 2 are there
+          if (j - j0 >= 2) {
+            const uint32_t ph = (uint32_t)((j - j0 - 2) >> 1) & 1;
+            bool free = prompt_wait(p, &bars.s_full[0][(j - j0) & 1], ph, give_up);
+            if (n_q > 1) free = free && prompt_wait(p, &bars.s_full[1][(j - j0) & 1], ph, give_up);
+            if (!__all_sync(0xffffffffu, free)) {
+              ok = false;
+              break;
+            }
+          }
+          const bool leader = elect_lane();
+          if (leader) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
+#pragma unroll
+          for (int e = 0; e < PPT; ++e) {
+            const int phys = __shfl_sync(0xffffffffu, now, at + e);
+            if (leader)
+              tma_page(smem + PromptSmem::kv + st * kTileBytes + e * P * kHeadDim * 2,
+                       kv ? &map_v : &map_k, (phys * p.Hkv + g) * (P / 8), &bars.kv_full[st]);
+          }
+          __syncwarp();
+          ++fetched;
+          if ((st += 2) >= kKvStages) st -= kKvStages;
         }
-        // K (j) takes the stage of V (j - 3), V (j) that of K (j - 2): both are free once
-        // the scores of tile j - 2 are there
-        if (j - j0 >= 2) {
-          const uint32_t ph = (uint32_t)((j - j0 - 2) >> 1) & 1;
-          bool free = prompt_wait(p, &bars.s_full[0][(j - j0) & 1], ph, give_up);
-          if (n_q > 1) free = free && prompt_wait(p, &bars.s_full[1][(j - j0) & 1], ph, give_up);
-          if (!__all_sync(0xffffffffu, free)) {
-            ok = false;
-            break;
+        if (!ok) {  // leave only when every copy of this warp has landed
+          for (int f = max(0, fetched - kKvStages); f < fetched; ++f) {
+            const int u = 2 * f + kv;
+            for (int i = 0; i < 1 << 20; ++i)
+              if (mbar_try_wait(&bars.kv_full[u % kKvStages], (u / kKvStages) & 1)) break;
           }
         }
-        const bool leader = elect_lane();
-        if (leader) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
-#pragma unroll
-        for (int e = 0; e < PPT; ++e) {
-          const int phys = __shfl_sync(0xffffffffu, now, at + e);
-          if (leader)
-            tma_page(smem + PromptSmem::kv + st * kTileBytes + e * P * kHeadDim * 2,
-                     kv ? &map_v : &map_k, (phys * p.Hkv + g) * (P / 8), &bars.kv_full[st]);
-        }
-        __syncwarp();
-        ++fetched;
-        if ((st += 2) >= kKvStages) st -= kKvStages;
       }
-      if (!ok) {  // leave only when every copy of this warp has landed
-        for (int f = max(0, fetched - kKvStages); f < fetched; ++f) {
-          const int u = 2 * f + kv;
-          for (int i = 0; i < 1 << 20; ++i)
-            if (mbar_try_wait(&bars.kv_full[u % kKvStages], (u / kKvStages) & 1)) break;
-        }
-      }
-    }
-    // (the queries too: no product waits for them where no token is visible)
-    if (kv == 0)
-      for (int i = 0; i < 1 << 20; ++i)
-        if (mbar_try_wait(&bars.q_full, 0)) break;
-  } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
-    // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
-    // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
-    // other tile's products fill those.)
-    {
+      // (the queries too: no product waits for them where no token is visible)
+      if (kv == 0)
+        for (int i = 0; i < 1 << 20; ++i)
+          if (mbar_try_wait(&bars.q_full, 0)) break;
+    } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
+      // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
+      // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
+      // other tile's products fill those.)
       const int t = warp == 11;
       // Q and K are K-major: the stride is that of 8-row groups.  V is MN-major: the lead is
       // that of its 64-dim spans, the stride that of 8-token groups.  Address fields count
@@ -535,7 +541,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (mbar_try_wait(&bars.drain[t], 0)) break;
       }
     }
-  }
   } else {
     // ---- softmax: a thread a row
     const int t = warp >> 2, row = threadIdx.x & 127;

@@ -361,8 +361,9 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
     sp.p.q = static_cast<const __half*>(q);
     sp.p.out = static_cast<__half*>(out);
     sp.p.lse = lse;
-    sp.p.n_splits = prompt_splits(sp.p, n_tokens, prompt_pages(*cache, n_tokens, sink_tokens, window),
-                                  user_split(opts));
+    sp.p.n_splits =
+        prompt_splits(sp.p, n_tokens, prompt_pages(*cache, n_tokens, sink_tokens, window),
+                      user_split(opts));
     return launched(launch_prompt(sp.p, n_tokens, sink_tokens, window,
                                   static_cast<cudaStream_t>(stream)),
                     what);
