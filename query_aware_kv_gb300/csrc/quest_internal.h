@@ -218,6 +218,8 @@ constexpr int kSplitRows = 1024;  // rows of a launch that splits them, at most 
 // The most parts (rows * splits) that a launch writes; `user`: with run_pages given.
 size_t span_max_parts(int batch, int hkv, bool user);
 // `pages`: the most that a row has.
+// Whether the launch of a narrow chain step takes the selection itself (p.chain_select).
+bool span_selects(const SpanParams& sp, int pages);
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s);
 
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):

@@ -199,9 +199,12 @@ int narrow_decode(const quest_narrow_cache_t* cache, const void* q, const void* 
   sp.p.chain_append = k_new ? 1 : 0;
   cudaError_t e = k_new ? launch_narrow_estimate(sp.p, sp.nar, group_of(c), s)
                         : launch_estimate(sp.p, group_of(c), false, s);
-  if (e == cudaSuccess) e = launch_topk(sp.p, s);
+  const int pages = std::min(top_k, c.max_pages);
+  sp.run_pages = user_split(opts);
+  sp.p.chain_select = span_selects(sp, pages) ? 1 : 0;
+  if (e == cudaSuccess && !sp.p.chain_select) e = launch_topk(sp.p, s);
   if (e != cudaSuccess) return launched(e, what);
-  return run_span(sp, true, std::min(top_k, c.max_pages), opts, q, out, lse, stream, what);
+  return run_span(sp, true, pages, opts, q, out, lse, stream, what);
 }
 
 }  // namespace

@@ -340,7 +340,9 @@ __device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b) {
 // grid rows * n_splits (split fastest): split s of a row takes the s-th share of its pages,
 // warp w of the CTA every kSpanWarps-th page of that; a split row's parts are joined by the CTA
 // that comes last to it.
-template <bool N8, int kSpanWarps, int kCtas, int kDepth>
+// kSelect (a chain step without a top-K kernel): every CTA of a row takes the row's selection from
+// the scores itself, the same in each; split 0 also writes the caller's copy.
+template <bool N8, int kSpanWarps, int kCtas, int kDepth, bool kSelect>
 __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams sp) {
   constexpr int kSpanThreads = 32 * kSpanWarps;
   __shared__ float s_m[kSpanWarps][8], s_l[kSpanWarps][8];
@@ -361,8 +363,26 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
   int count = shape.count;
   const int* list = nullptr;
   if (sp.mode == kSpanList) {
-    list = p.sel_idx + (size_t)row * p.top_k;
-    const int given = p.sel_count[row];
+    int given = 0;
+    if constexpr (kSelect) {
+      extern __shared__ __align__(16) unsigned char s_sel[];
+      int* scratch = reinterpret_cast<int*>(s_sel + topk_smem_bytes(p.max_pages));  // [256]
+      int* kept = scratch + 256;                                                    // [top_k]
+      topk_row<kSpanThreads, false>(p.scores + (size_t)row * p.max_pages, N, p.top_k,
+                                    p.sink_pages, p.local_pages, kept, &s_flag,
+                                    topk_smem_at(s_sel, p.max_pages), scratch);
+      __syncthreads();
+      list = kept;
+      given = s_flag;
+      if (split == 0) {
+        for (int i = threadIdx.x; i < p.top_k; i += kSpanThreads)
+          p.sel_idx[(size_t)row * p.top_k + i] = kept[i];
+        if (threadIdx.x == 0) p.sel_count[row] = given;
+      }
+    } else {
+      list = p.sel_idx + (size_t)row * p.top_k;
+      given = p.sel_count[row];
+    }
     if ((given < 0 || given > count) && threadIdx.x == 0 && split == 0)
       report(p, QUEST_ERR_BAD_SELECTION, b, given, kSiteSelection);
     count = max(0, min(given, count));
@@ -623,9 +643,9 @@ struct SpanShape {
 };
 
 static SpanShape span_shape(bool narrow, long long rows) {
-  if (narrow) return {8, 2, (const void*)span_kernel<true, 8, 2, 1>};
-  if (rows > kSms) return {4, 2, (const void*)span_kernel<false, 4, 2, 2>};
-  return {8, 1, (const void*)span_kernel<false, 8, 1, 2>};
+  if (narrow) return {8, 2, (const void*)span_kernel<true, 8, 2, 1, false>};
+  if (rows > kSms) return {4, 2, (const void*)span_kernel<false, 4, 2, 2, false>};
+  return {8, 1, (const void*)span_kernel<false, 8, 1, 2, false>};
 }
 
 // Splits of a row: as many as fit the GPU together with the other rows' in one wave, with a few
@@ -652,14 +672,29 @@ size_t span_max_parts(int batch, int hkv, bool user) {
   return user ? rows * kMaxSplitsSpan : std::min<long long>(rows * kMaxSplitsSpan, 4 * kSms);
 }
 
+// Where a narrow chain step selects: for MHA rows of at most 4096 pages whose CTAs are all
+// resident, in the span decode's own CTAs (one launch less: 1K tokens and 4 heads 12.7 -> 11.2
+// us), otherwise in a kernel of its own.
+bool span_selects(const SpanParams& sp, int pages) {
+  const long long rows = (long long)sp.p.B * sp.p.Hkv;
+  const SpanShape shape = span_shape(true, rows);
+  return sp.p.Hq == sp.p.Hkv && sp.p.max_pages <= 4096 &&
+         rows * span_splits(sp, shape, pages) <= (long long)kSms * shape.ctas;
+}
+
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s) {
   const long long rows = (long long)sp.p.B * sp.p.Hkv;
   const SpanShape shape = span_shape(narrow, rows);
   SpanParams pp = sp;
   pp.p.n_splits = span_splits(sp, shape, pages);
   void* args[] = {&pp};
-  return launch_pdl(shape.fn, dim3((unsigned)(rows * pp.p.n_splits)), dim3(32 * shape.warps), 0, s,
-                    args);
+  const dim3 grid((unsigned)(rows * pp.p.n_splits)), block(32 * shape.warps);
+  if (!sp.p.chain_select) return launch_pdl(shape.fn, grid, block, 0, s, args);
+  const void* fn = (const void*)span_kernel<true, 8, 2, 1, true>;
+  const size_t smem = topk_smem_bytes(sp.p.max_pages) + 256 * 4 + (size_t)sp.p.top_k * 4;
+  const cudaError_t e = ensure_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, grid, block, smem, s, args);
 }
 
 }  // namespace quest
