@@ -382,6 +382,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int tiles = (list.count + PPT - 1) / PPT;
   const int j0 = tiles * split / p.n_splits, j1 = tiles * (split + 1) / p.n_splits;
 
+  // A place per row that nothing else uses once the last product of the row's tile is done (the
+  // other tile may still be at work on the K / V tiles): the row's start in the tile's queries.
+  auto stash = [&](int t, int row) {
+    return reinterpret_cast<float2*>(smem + PromptSmem::q + t * kTileBytes + 256 * row);
+  };
   bool again = false;
   if (warp >= 8) {
     if (warp == 8 || warp == 10) {
@@ -737,15 +742,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           p.part_ml[2 * slot + 1] = l;
         }
       }
-      // (m and l of a row that has to be taken again, below; the K / V tiles are done with)
-      if (ok && mine && j1 > j0 && odd && !none && l <= 3.4e38f) {
-        again = true;
-        *reinterpret_cast<float2*>(smem + PromptSmem::kv + 8 * (t * kTileRows + row)) =
-            make_float2(m, l);
-      } else {
-        *reinterpret_cast<float2*>(smem + PromptSmem::kv + 8 * (t * kTileRows + row)) =
-            make_float2(0.f, -1.f);
-      }
+      // (m and l of a row that has to be taken again, below; l < 0: it has not)
+      again = ok && mine && j1 > j0 && odd && !none && l <= 3.4e38f;
+      __syncwarp();
+      *stash(t, row) = again ? make_float2(m, l) : make_float2(0.f, -1.f);
     }
   }
   fence_before();
@@ -757,9 +757,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   // that do not see its token.  Such a row (its scores are finite, its O is not) is taken again
   // from what it sees, by a warp, a token at a time.
   if (any_again) {
-    const float2* stash = reinterpret_cast<const float2*>(smem + PromptSmem::kv);
     for (int r = warp; r < (tok1 - tok0) * G; r += kPromptThreads / 32) {
-      const float m_r = stash[r].x, l_r = stash[r].y;
+      const float2 ml = *stash(r / kTileRows, r % kTileRows);
+      const float m_r = ml.x, l_r = ml.y;
       if (l_r < 0.f) continue;  // warp-uniform
       const int pos_r = pos0 + tok0 + (r >> lg);
       const size_t at = (((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) +
