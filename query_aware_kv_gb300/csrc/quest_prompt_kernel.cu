@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         // 32 scores at s + 32 u: their weights against the reference m
         uint32_t w[kTileTokens / 2];
-        uint64_t sum[4] = {0, 0, 0, 0};
+        uint64_t sum[2] = {0, 0};
         auto weigh = [&](const float* s, int u) {
           const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
           const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, shift2), a, c);
             a = ex2(a);
             c = ex2(c);
-            sum[k & 3] = add2(sum[k & 3], pair(a, c));
+            sum[k & 1] = add2(sum[k & 1], pair(a, c));
             w[16 * u + k] = pack2(a, c);
           }
         };
@@ -616,22 +616,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // replaced yet.
         float top;
         {
-          float best[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+          float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float s[64];
             tmem_ld32(s_col + 64 * h, reinterpret_cast<uint32_t*>(s));
             tmem_ld32(s_col + 64 * h + 32, reinterpret_cast<uint32_t*>(s) + 32);
             tmem_wait_ld();
-            // four chains of three-input maxima: one chain of 127 would wait on itself
+            // two chains of three-input maxima and two of sums: four of each spill, one waits on
+            // itself
 #pragma unroll
-            for (int k = 0; k < 64; k += 8)
+            for (int k = 0; k < 64; k += 4)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) best[e] = max3(best[e], s[k + e], s[k + 4 + e]);
+              for (int e = 0; e < 2; ++e) best[e] = max3(best[e], s[k + e], s[k + 2 + e]);
             weigh(s, 2 * h);
             weigh(s + 32, 2 * h + 1);
           }
-          top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * p.qscale;
+          top = fmaxf(best[0], best[1]) * p.qscale;
         }
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           const float mn = fmaxf(m, top);
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sum[k] = 0;
+          for (int k = 0; k < 2; ++k) sum[k] = 0;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float s[32];
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tmem_st32(s_col + 32, w + 32);
         {
           float a, c;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
+          unpair(add2(sum[0], sum[1]), a, c);
           l += a + c;
         }
         tmem_wait_st();
