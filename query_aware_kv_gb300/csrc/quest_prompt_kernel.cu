@@ -29,8 +29,8 @@
 // products of 128 x 128 x 128 (2048 cycles at the dense rate) and 2 * 128 * 128 exponentials
 // (1024 cycles); a tile's softmax takes 1100 cycles, its two products 1024, and each of the two
 // hand-overs through a barrier some 300, so a pair takes about 2700, the tensor core busy for
-// three quarters of them.  Measured: an 8K prompt of 32 heads with a 4K window 331 us (1.24
-// PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 104 us (1.32), five tokens over a 32K
+// three quarters of them.  Measured: an 8K prompt of 32 heads with a 4K window 330 us (1.25
+// PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 103 us (1.34), five tokens over a 32K
 // window 38 us (3.5 TB/s).
 #include <cuda.h>
 #include <math_constants.h>
@@ -734,8 +734,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               *reinterpret_cast<uint4*>(p.part_acc + slot * kHeadDim + 32 * u + 4 * e) =
-                  j1 > j0 ? make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3])
-                          : make_uint4(0u, 0u, 0u, 0u);
+                  none ? make_uint4(0u, 0u, 0u, 0u)  // (its O may be 0 * NaN)
+                       : make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         if (mine) {

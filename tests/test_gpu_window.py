@@ -202,6 +202,28 @@ def test_odd_values_reach_only_the_rows_that_see_them(n, pps):
             R.assert_close(got, lse[0, :, h], ref, True)
 
 
+def test_odd_values_in_a_share_that_a_row_does_not_see():
+    """The K / V axis split: rows that see nothing of a split's tokens, NaN among which other
+    rows see, are as if the NaN were 0."""
+    n, window, L = 250, 40, 900
+    cache = make([L], 2, 2, 16, seed=15)
+    o = q.opts(pages_per_split=8)  # 128 tokens a split
+    ws = q.window_workspace(cache, n, o)
+    qq = torch.randn((1, n, 2, 128), device="cuda").half()
+    slot = (int(cache.block_table[0, (L - 1) // 16]), slice(None), (L - 1) % 16)
+    clean = cache.v_pool[slot].clone()
+    cache.v_pool[slot] = float("nan")
+    out, lse = q.window_prefill(cache, qq, 0, window, ws, o)
+    ok(ws)
+    assert torch.isnan(out[0, -1]).all()
+    cache.v_pool[slot] = clean
+    want, want_lse = q.window_prefill(cache, qq, 0, window, ws, o)
+    ok(ws)
+    assert torch.equal(lse, want_lse)
+    out[0, -1] = want[0, -1]
+    check(cache, qq, out, lse, 0, window, True)
+
+
 def test_large_scores_and_values():
     """Scores far from 0 (both signs) and a maximum that comes last: the running maximum
     moves, small weights vanish."""
