@@ -424,14 +424,16 @@ typedef struct quest_narrow_cache {
 } quest_narrow_cache_t;
 
 /* Bytes of workspace for every quest_narrow_* call on this cache with this top_k and opts;
- * 0 if the arguments are invalid.  Conventions as for quest_workspace_size. */
+ * 0 if the arguments are invalid.  Conventions as for quest_workspace_size; one workspace
+ * serves caches of one batch size, and no calls but quest_narrow_*. */
 size_t quest_narrow_workspace_size(const quest_narrow_cache_t* cache, int32_t top_k,
                                    const quest_opts_t* opts);
 
 /* quest_prefill into a narrow cache: k, v: fp16 [batch][n_tokens][num_kv_heads][128] at
  * positions seq_lens[b] .. seq_lens[b] + n_tokens - 1.  The same cache, bit for bit, as
  * n_tokens quest_narrow_append calls.  A sequence with no room, or with a touched page
- * outside [0, num_phys), is reported; its open page and its length are left unchanged. */
+ * outside [0, num_phys), is reported; its open page, that page's box and its length are left
+ * unchanged. */
 int quest_narrow_prefill(const quest_narrow_cache_t* cache, const void* k, const void* v,
                          int32_t n_tokens, void* ws, size_t ws_bytes, quest_stream_t stream);
 
@@ -478,7 +480,8 @@ int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, c
  */
 
 /* Bytes of workspace of quest_window_decode (n_tokens = 1) and of quest_window_prefill with
- * up to n_tokens query tokens per sequence; 0 if the arguments are invalid. */
+ * up to n_tokens query tokens per sequence; 0 if the arguments are invalid.  One workspace
+ * serves caches of one batch size, and no calls but quest_window_*. */
 size_t quest_window_workspace_size(const quest_cache_t* cache, int32_t n_tokens,
                                    const quest_opts_t* opts);
 

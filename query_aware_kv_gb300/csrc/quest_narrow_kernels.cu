@@ -214,6 +214,16 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_pages_kernel(Params p, 
   const int phys = p.block_table[(size_t)b * p.max_pages + page];
   if (phys < 0 || phys >= p.num_phys) return;
   const int s0 = max(0, L - page * P);
+  if (s0 > 0) {  // the open page becomes complete: not where the chunk meets an unmapped page
+    const int last = (L + n - 1) / P;
+    bool bad = false;
+#pragma unroll 8
+    for (int pg = page + lane; pg <= last; pg += 32) {
+      const int at = p.block_table[(size_t)b * p.max_pages + pg];
+      bad |= at < 0 || at >= p.num_phys;
+    }
+    if (__any_sync(0xffffffffu, bad)) return;
+  }
   const size_t stride = (size_t)p.Hkv * kHeadDim;
   const size_t in = ((size_t)b * n + (page * P + s0 - L)) * stride + (size_t)g * kHeadDim;
   encode_page<P>(p, nar, b, g, page, phys, s0, k + in, v + in, stride, lane);

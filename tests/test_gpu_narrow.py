@@ -305,6 +305,32 @@ def test_a_chunk_that_does_not_fit_changes_nothing_live():
     assert cache.seq_lens.tolist() == [38, 60]
 
 
+def test_a_chunk_that_meets_an_unmapped_page_leaves_the_sequence():
+    """The first page that the chunk would complete is mapped, a later one is not: tokens, box
+    and length stay, and the same chunk goes in once the page is mapped."""
+    cache, ref = filled((8, 2, 16), [37, 21], pages=40)
+    ws = q.narrow_workspace(cache)
+    held = int(cache.block_table[0, 37])
+    cache.block_table[0, 37] = -1
+    box = cache.meta[0, :, 2].clone()
+    k, v = tokens(2, 590, 2, seed=12)
+    q.narrow_prefill(cache, k.cuda(), v.cuda(), ws)
+    rc, detail = q.read_status(ws)
+    assert rc == q.QUEST_ERR_BAD_PAGE and detail[:2] == (0, 37)
+    assert cache.seq_lens.tolist() == [37, 611]
+    assert torch.equal(cache.meta[0, :, 2], box)
+    assert torch.equal(cache.k_open[0, :, :5].cpu(), ref.k[0][:, 32:37])
+    assert torch.equal(cache.v_open[0, :, :5].cpu(), ref.v[0][:, 32:37])
+    cache.block_table[0, 37] = held
+    cache.seq_lens[1] = 37  # (any length with room: sequence 1 is not looked at again)
+    q.narrow_prefill(cache, k.cuda(), v.cuda(), ws)
+    ok(ws)
+    both = torch.cat((ref.k[0], k[0].transpose(0, 1)), 1)
+    for p in range(627 // 16):
+        page = both[:, p * 16:p * 16 + 16]
+        assert torch.equal(cache.meta[0, :, p, 0].cpu(), page.amin(1)), p
+
+
 def test_bad_selection_is_reported():
     cache, _ = filled((4, 4, 16), [100])
     ws = q.narrow_workspace(cache, 3)
