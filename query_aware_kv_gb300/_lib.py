@@ -585,7 +585,7 @@ def narrow_prefill(cache: NarrowCache, k: torch.Tensor, v: torch.Tensor, ws: tor
     shape = (cache.batch, k.shape[1], cache.num_kv_heads, HEAD_DIM)
     _need(k, "k", torch.float16, shape)
     _need(v, "v", torch.float16, shape)
-    _here(cache)
+    _here(cache, ws, k, v)
     _check(load().quest_narrow_prefill(ctypes.byref(cache.desc), k.data_ptr(), v.data_ptr(),
                                        int(k.shape[1]), ws.data_ptr(), ws.numel(),
                                        _stream(stream)))
@@ -597,7 +597,7 @@ def narrow_append(cache: NarrowCache, k_new: torch.Tensor, v_new: torch.Tensor,
     shape = (cache.batch, cache.num_kv_heads, HEAD_DIM)
     _need(k_new, "k_new", torch.float16, shape)
     _need(v_new, "v_new", torch.float16, shape)
-    _here(cache)
+    _here(cache, ws, k_new, v_new)
     _check(load().quest_narrow_append(ctypes.byref(cache.desc), k_new.data_ptr(),
                                       v_new.data_ptr(), ws.data_ptr(), ws.numel(),
                                       _stream(stream)))
@@ -612,7 +612,7 @@ def narrow_sparse_decode(cache: NarrowCache, q: torch.Tensor, idx: torch.Tensor,
     _need(idx, "idx", torch.int32, (cache.batch, cache.num_kv_heads, top_k))
     _need(count, "count", torch.int32, (cache.batch, cache.num_kv_heads))
     out, lse = _out(cache, q, out, lse, want_lse)
-    _here(cache)
+    _here(cache, ws, q, idx, count, out, lse)
     _check(load().quest_narrow_sparse_decode(
         ctypes.byref(cache.desc), q.data_ptr(), idx.data_ptr(), count.data_ptr(), int(top_k),
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
@@ -652,10 +652,16 @@ def narrow_window_decode(cache: NarrowCache, q: torch.Tensor, sink_tokens: int, 
     return WindowPlan(cache, sink_tokens, window, ws, o, out, lse, want_lse, stream).decode(q)
 
 
-def _here(cache) -> None:
-    """The calls go to the current device's stream: the cache has to be on it."""
-    if cache.k_pool.get_device() != torch._C._cuda_getDevice():
+def _here(cache, ws: torch.Tensor, *others: torch.Tensor) -> None:
+    """The calls go to the current device's stream: the cache, the workspace and the other
+    tensors have to be on it."""
+    _need(ws, "ws", torch.uint8)
+    dev = torch._C._cuda_getDevice()
+    if cache.k_pool.get_device() != dev:
         raise ValueError("the cache is on another device than the current one")
+    for t in (ws, *others):
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on another device than the cache")
 
 
 class NarrowPlan(DecodePlan):
@@ -665,8 +671,8 @@ class NarrowPlan(DecodePlan):
     _decode_fn, _step_fn = "quest_narrow_decode", "quest_narrow_decode_step"
 
     def __init__(self, cache: NarrowCache, *args, **kw):
-        _here(cache)
         super().__init__(cache, *args, **kw)
+        _here(cache, self._keep[1], self.out, self.lse, self.idx_out, self.count_out)
 
     def dense(self, q: torch.Tensor):
         """quest_narrow_dense_decode of this step's queries; returns (out, lse)."""
@@ -699,12 +705,11 @@ class WindowPlan:
     def __init__(self, cache, sink_tokens: int, window: int, ws: torch.Tensor,
                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
                  stream=None):
-        _here(cache)
         self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
         self._dev = cache.k_pool.get_device()
         probe = torch.empty(0, dtype=torch.float16, device=cache.k_pool.device)
         self.out, self.lse = _out(cache, probe, out, lse, want_lse)
-        _need(ws, "ws", torch.uint8)
+        _here(cache, ws, self.out, self.lse)
         self._keep = (cache, ws, o)  # alive as long as the plan
         self._lib = load()
         self._fn = (self._lib.quest_narrow_window_decode if isinstance(cache, NarrowCache)
@@ -750,7 +755,7 @@ def window_prefill(cache: PagedCache, q: torch.Tensor, sink_tokens: int, window:
         lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, shape[:3])
-    _here(cache)
+    _here(cache, ws, q, out, lse)
     _check(load().quest_window_prefill(
         ctypes.byref(cache.desc), q.data_ptr(), int(shape[1]), int(sink_tokens), int(window),
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
