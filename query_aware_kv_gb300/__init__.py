@@ -1,6 +1,7 @@
 """Quest decode-time hot path for GB300 (sm_103a): paged fp16 KV cache with per-page key
 min/max boxes, query-aware page scoring, per-head top-K page selection and split-K
-sparse flash-decode, as a C-ABI library (``libquest.so``) with a thin ctypes binding.
+sparse flash-decode, as a C-ABI library (``libquest.so``) with a thin ctypes binding; caches
+of 8-bit pages (``NarrowCache``) and attention with a sliding window and sink tokens.
 
 The names below mirror the C entry points of ``include/quest.h``.
 """
