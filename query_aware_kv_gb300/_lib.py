@@ -431,13 +431,13 @@ def topk(cache: PagedCache, scores: torch.Tensor, top_k: int, ws: torch.Tensor,
     return idx, cnt
 
 
-def _out(cache: PagedCache, q: torch.Tensor, out, lse, want_lse: bool):
+def _out(cache, on: torch.Tensor, out, lse, want_lse: bool):
     B, Hq = cache.batch, cache.desc.num_q_heads
     if out is None:
-        out = torch.empty((B, Hq, HEAD_DIM), dtype=torch.float16, device=q.device)
+        out = torch.empty((B, Hq, HEAD_DIM), dtype=torch.float16, device=on.device)
     _need(out, "out", torch.float16, (B, Hq, HEAD_DIM))
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=on.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq))
     return out, lse
@@ -520,8 +520,7 @@ class DecodePlan:
         self._qshape = torch.Size((B, Hq, HEAD_DIM))
         self._kvshape = torch.Size((B, Hkv, HEAD_DIM))
         self._dev = cache.k_pool.get_device()
-        probe = torch.empty(0, dtype=torch.float16, device=cache.k_pool.device)
-        self.out, self.lse = _out(cache, probe, out, lse, want_lse)
+        self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
         if idx_out is not None:
             _need(idx_out, "idx_out", torch.int32, (B, Hkv, _sel_row(cache, top_k, o)))
         if count_out is not None:
@@ -707,8 +706,7 @@ class WindowPlan:
                  stream=None):
         self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
         self._dev = cache.k_pool.get_device()
-        probe = torch.empty(0, dtype=torch.float16, device=cache.k_pool.device)
-        self.out, self.lse = _out(cache, probe, out, lse, want_lse)
+        self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
         _here(cache, ws, self.out, self.lse)
         self._keep = (cache, ws, o)  # alive as long as the plan
         self._lib = load()
