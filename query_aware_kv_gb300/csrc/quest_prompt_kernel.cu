@@ -301,6 +301,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void store8(float* to, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 __device__ __forceinline__ bool not_finite(const uint32_t* o) {
   bool x = false;
 #pragma unroll
@@ -730,12 +737,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_wait_ld();
             odd |= not_finite(o);
           }
-          if (mine) {
+          if (none) {  // (its O may be 0 * NaN)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(p.part_acc + slot * kHeadDim + 32 * u + 4 * e) =
-                  none ? make_uint4(0u, 0u, 0u, 0u)  // (its O may be 0 * NaN)
-                       : make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (mine) {  // whole sectors: a lane's row is 512 B from its neighbour's
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              store8(p.part_acc + slot * kHeadDim + 32 * u + 8 * e, o + 8 * e);
           }
         }
         if (mine) {
@@ -798,60 +807,60 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
   }
-  if (p.n_splits == 1) return;
+}
 
-  // ---- the last split of the work item joins the shares
-  const size_t item = ((size_t)b * p.Hkv + g) * (gridDim.x / (unsigned)p.n_splits) + blk;
-  if (!arrive_last<kPromptThreads, false>(&p.decode_arrive[item], (unsigned)p.n_splits,
-                                          &bars.give_up))
-    return;
-  const size_t first_slot = part_slot(pp, 0);
-  for (int o = threadIdx.x; o < (tok1 - tok0) * G * (kHeadDim / 4); o += kPromptThreads) {
-    const int r = o / (kHeadDim / 4), d = o % (kHeadDim / 4) * 4;
-    const float* ml = p.part_ml + 2 * (first_slot + r);
-    const float* acc = p.part_acc + (first_slot + r) * kHeadDim + d;
-    float M = -CUDART_INF_F, Z = 0.f;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    // eight splits' loads side by side, the last few too (an empty split has m = -inf, l and O 0)
-    for (int s0 = 0; s0 < p.n_splits; s0 += 8) {
-      float x[8];
+// The shares of the rows' splits into out and lse: a warp a row, lane l the dims 4 l .. 4 l + 3
+// and the maxima and sums of splits l and l + 32, eight shares on their way together.  A kernel
+// of its own because the work items are few: joined by the last CTA of each, 20 rows of 19
+// splits took 6 us and 256 rows of 5 splits 27 us, more than the products.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams pp, int rows,
+                                                                   int blocks) {
+  pdl_wait();
+  pdl_trigger();
+  const Params& p = pp.p;
+  const int lane = threadIdx.x & 31, lg = pp.log_g, G = 1 << lg, n = p.n_splits;
+  const int at = (int)blockIdx.x * (kJoinThreads / 32) + (int)(threadIdx.x >> 5);
+  if (at >= rows) return;  // (row of q, out and lse; the warp's)
+  const int h = at % p.Hq, tok = at / p.Hq % pp.n_tokens, b = at / p.Hq / pp.n_tokens;
+  const int per = 2 * kTileRows >> lg;  // tokens of a work item
+  const size_t item = ((size_t)b * p.Hkv + (h >> lg)) * blocks + tok / per;
+  const size_t slot = item * n * pp.part_rows + (tok % per) * G + (h & (G - 1));
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot;
+  const float4* acc = reinterpret_cast<const float4*>(p.part_acc + slot * kHeadDim) + lane;
+  const float2 nothing = make_float2(-CUDART_INF_F, 0.f);
+  const float2 x = lane < n ? __ldcg(ml + (size_t)lane * pp.part_rows) : nothing;
+  const float2 y = lane + 32 < n ? __ldcg(ml + (size_t)(lane + 32) * pp.part_rows) : nothing;
+  float fx = 0.f, fy = 0.f, M = 0.f, Z = 0.f;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < n; s0 += 8) {
+    float4 a[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = s0 + e < p.n_splits ? __ldcg(ml + (size_t)2 * (s0 + e) * pp.part_rows)
-                                   : -CUDART_INF_F;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) M = fmaxf(M, x[e]);
+    for (int e = 0; e < 8; ++e)
+      a[e] = s0 + e < n ? __ldcg(acc + (size_t)(s0 + e) * pp.part_rows * (kHeadDim / 4))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s0 == 0) {
+      M = warp_max(fmaxf(x.x, y.x));
+      fx = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);  // an empty split has m = -inf, l and O 0
+      fy = y.x == -CUDART_INF_F ? 0.f : ex2(y.x - M);
+      Z = warp_sum(fmaf(x.y, fx, y.y * fy));
     }
-    for (int s0 = 0; s0 < p.n_splits; s0 += 8) {
-      float2 x[8];
-      float4 a[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const size_t o2 = (size_t)min(s0 + e, p.n_splits - 1) * pp.part_rows;
-        x[e] = __ldcg(reinterpret_cast<const float2*>(ml + 2 * o2));
-        a[e] = __ldcg(reinterpret_cast<const float4*>(acc + o2 * kHeadDim));
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f =
-            s0 + e >= p.n_splits || x[e].x == -CUDART_INF_F ? 0.f : ex2(x[e].x - M);
-        Z = fmaf(x[e].y, f, Z);
-        A.x = fmaf(a[e].x, f, A.x);
-        A.y = fmaf(a[e].y, f, A.y);
-        A.z = fmaf(a[e].z, f, A.z);
-        A.w = fmaf(a[e].w, f, A.w);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int s = s0 + e;
+      const float f = __shfl_sync(0xffffffffu, s < 32 ? fx : fy, s & 31);
+      A.x = fmaf(a[e].x, f, A.x);
+      A.y = fmaf(a[e].y, f, A.y);
+      A.z = fmaf(a[e].z, f, A.z);
+      A.w = fmaf(a[e].w, f, A.w);
     }
-    const bool none = M == -CUDART_INF_F;
-    const float inv = none ? 0.f : 1.f / Z;
-    const size_t at = ((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) + (r & (G - 1));
-    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + d) =
-        none ? make_uint2(0u, 0u)
-             : make_uint2(pack2(A.x * inv, A.y * inv), pack2(A.z * inv, A.w * inv));
-    if (d == 0 && p.lse)
-      p.lse[at] = none ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
   }
-  if (threadIdx.x == 0) p.decode_arrive[item] = 0u;
+  const bool none = M == -CUDART_INF_F;
+  const float inv = none ? 0.f : 1.f / Z;
+  reinterpret_cast<uint2*>(p.out + (size_t)at * kHeadDim)[lane] =
+      none ? make_uint2(0u, 0u) : make_uint2(pack2(A.x * inv, A.y * inv), pack2(A.z * inv, A.w * inv));
+  if (lane == 0 && p.lse)
+    p.lse[at] = none ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
 }
 
 // cuTensorMapEncodeTiled, taken from the driver at run time (nothing links against it).
@@ -937,8 +946,15 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   const size_t smem = PromptSmem::total + 1024;
   if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
   void* args[] = {&pp, &mq, &mk, &mv};
-  return launch_pdl(fn, dim3((unsigned)(prompt_blocks(G, n_tokens) * p.n_splits), p.Hkv, p.B),
-                    dim3(kPromptThreads), smem, s, args);
+  int blocks = prompt_blocks(G, n_tokens);
+  e = launch_pdl(fn, dim3((unsigned)(blocks * p.n_splits), p.Hkv, p.B), dim3(kPromptThreads), smem,
+                 s, args);
+  if (e != cudaSuccess || p.n_splits == 1) return e;
+  int rows = p.B * n_tokens * p.Hq;  // at most kPromptParts work items of 256
+  void* join_args[] = {&pp, &rows, &blocks};
+  constexpr int per = kJoinThreads / 32;
+  return launch_pdl((const void*)prompt_join_kernel, dim3((unsigned)((rows + per - 1) / per)),
+                    dim3(kJoinThreads), 0, s, join_args);
 }
 
 }  // namespace quest
