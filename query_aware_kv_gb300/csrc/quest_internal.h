@@ -224,7 +224,8 @@ cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream
 
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
 // p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of
-// part_ml / part_acc each; splits only while items * splits is at most kPromptParts.
+// part_ml / part_acc each; splits only while items * splits is at most kPromptParts.  Two
+// launches where rows are split (the second joins their shares), one otherwise.
 constexpr int kPromptParts = 304;
 int prompt_part_rows(int G, int n_tokens);
 int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps);

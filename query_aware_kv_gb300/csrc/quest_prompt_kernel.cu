@@ -18,7 +18,7 @@
 // issue the products of a tile each: while one tile is in its softmax, the tensor core works
 // for the other.  The order of issue P V (t, j), Q K^T (t, j + 1) per tile t lets P live in S's
 // columns.  Few query rows leave most SMs without work, so then the K / V tiles of a work item
-// are shared by several CTAs, whose shares the last one joins.
+// are shared by several CTAs, whose shares a second kernel joins.
 // The maximum m moves only when a row exceeds it by more than 2^6 (then O is rescaled in
 // TMEM by the softmax threads themselves), so weights reach 2^14 at most and keep fp16's full
 // precision down to 2^-22 of the largest.  P enters the second product as one fp16 number:
@@ -28,10 +28,11 @@
 // What bounds it: the chain softmax -> P V -> Q K^T -> softmax of a tile.  A tile pair is 4
 // products of 128 x 128 x 128 (2048 cycles at the dense rate) and 2 * 128 * 128 exponentials
 // (1024 cycles); a tile's softmax takes 1100 cycles, its two products 1024, and each of the two
-// hand-overs through a barrier some 300, so a pair takes about 2700, the tensor core busy for
-// three quarters of them.  Measured: an 8K prompt of 32 heads with a 4K window 330 us (1.25
+// hand-overs through a barrier some 300, so a pair takes about 2700; over a whole 8K prompt the
+// tensor core is busy for 63 % of the time.  Measured: an 8K prompt of 32 heads with a 4K window 330 us (1.25
 // PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 103 us (1.34), five tokens over a 32K
-// window 38 us (3.5 TB/s).
+// window 33 us (4.1 TB/s: 19 us of them the stream of K and V at the copy rate, the rest its start
+// and the join).
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -354,24 +355,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == 8 && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v)
                  : "memory");
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
-  volatile int* give_up = &bars.give_up;
   pdl_wait();
   pdl_trigger();
 
-  // ---- the CTA's work
+  // ---- the CTA's work (its length and first pages are looked up while the barriers and TMEM
+  // are set up)
   const int split = (int)blockIdx.x % p.n_splits;
   const int g = (int)blockIdx.y, b = (int)blockIdx.z;
-  if (warp == 8 && elect_lane()) {  // the queries' place does not depend on the length
-    mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
-    for (int i = 0; i < 2 * n_q; ++i)
-      tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
-             64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
-  }
-  __syncwarp();
   int L = p.seq_lens[b];
   if (L < 0 || (long long)L > (long long)p.max_pages * P) {
     if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
@@ -389,6 +379,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int tiles = (list.count + PPT - 1) / PPT;
   const int j0 = tiles * split / p.n_splits, j1 = tiles * (split + 1) / p.n_splits;
 
+  // Pages of the list, for the fetch warps: 32 at a time, a page per lane, the next 32 on their
+  // way; entries behind the list's end repeat its last page (their tokens are hidden).
+  auto entry = [&](int i) {
+    return p.block_table[(size_t)b * p.max_pages + list.page(min(i, list.count - 1))];
+  };
+  int now = 0, next = 0;
+  if ((warp == 8 || warp == 10) && j1 > j0) {
+    now = entry(j0 * PPT + lane);
+    next = entry(j0 * PPT + 32 + lane);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+  volatile int* give_up = &bars.give_up;
+  if (warp == 8 && elect_lane()) {
+    mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
+    for (int i = 0; i < 2 * n_q; ++i)
+      tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
+             64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
+  }
+  __syncwarp();
+
   // A place per row that nothing else uses once the last product of the row's tile is done (the
   // other tile may still be at work on the K / V tiles): the row's start in the tile's queries.
   auto stash = [&](int t, int row) {
@@ -400,17 +413,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // ---- fetch: warp 8 the K tiles (the queries are on their way), warp 10 the V tiles
       const int kv = warp == 10;
       if (j1 > j0) {
-        // 32 pages of the list at a time, a page per lane, the next 32 on their way; entries
-        // behind the list's end repeat its last page (their tokens are hidden)
-        auto entry = [&](int i) {
-          return p.block_table[(size_t)b * p.max_pages + list.page(min(i, list.count - 1))];
-        };
         auto checked = [&](int phys, int i) {
           if (phys >= 0 && phys < p.num_phys) return phys;
           record(p, QUEST_ERR_BAD_PAGE, b, list.page(min(i, list.count - 1)));
           return 0;
         };
-        int now = entry(j0 * PPT + lane), next = entry(j0 * PPT + 32 + lane);
         now = checked(now, j0 * PPT + lane);
         int st = kv;
         bool ok = true;
@@ -810,10 +817,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 }
 
 // The shares of the rows' splits into out and lse: a warp a row, lane l the dims 4 l .. 4 l + 3
-// and the maxima and sums of splits l and l + 32, eight shares on their way together.  A kernel
-// of its own because the work items are few: joined by the last CTA of each, 20 rows of 19
-// splits took 6 us and 256 rows of 5 splits 27 us, more than the products.
+// and the maxima and sums of splits l and l + 32, kTogether shares on their way together.  A
+// kernel of its own because the work items are few: joined by the last CTA of each, 20 rows of
+// 19 splits took 6 us and 256 rows of 5 splits 27 us, more than the products.
 constexpr int kJoinThreads = 128;
+template <int kTogether>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams pp, int rows,
                                                                    int blocks) {
   pdl_wait();
@@ -833,10 +841,10 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
   const float2 y = lane + 32 < n ? __ldcg(ml + (size_t)(lane + 32) * pp.part_rows) : nothing;
   float fx = 0.f, fy = 0.f, M = 0.f, Z = 0.f;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 8) {
-    float4 a[8];
+  for (int s0 = 0; s0 < n; s0 += kTogether) {
+    float4 a[kTogether];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < kTogether; ++e)
       a[e] = s0 + e < n ? __ldcg(acc + (size_t)(s0 + e) * pp.part_rows * (kHeadDim / 4))
                         : make_float4(0.f, 0.f, 0.f, 0.f);
     if (s0 == 0) {
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
       Z = warp_sum(fmaf(x.y, fx, y.y * fy));
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kTogether; ++e) {
       const int s = s0 + e;
       const float f = __shfl_sync(0xffffffffu, s < 32 ? fx : fy, s & 31);
       A.x = fmaf(a[e].x, f, A.x);
@@ -953,7 +961,11 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   int rows = p.B * n_tokens * p.Hq;  // at most kPromptParts work items of 256
   void* join_args[] = {&pp, &rows, &blocks};
   constexpr int per = kJoinThreads / 32;
-  return launch_pdl((const void*)prompt_join_kernel, dim3((unsigned)((rows + per - 1) / per)),
+  // (333 tokens of 4 kv heads, 5 splits: 16.2 us in all with eight shares together, 17.5 with
+  // sixteen; five tokens over a 32K window, 19 splits: 34.5 and 32.9)
+  const void* join = p.n_splits <= 8 ? (const void*)prompt_join_kernel<8>
+                                     : (const void*)prompt_join_kernel<16>;
+  return launch_pdl(join, dim3((unsigned)((rows + per - 1) / per)),
                     dim3(kJoinThreads), 0, s, join_args);
 }
 
