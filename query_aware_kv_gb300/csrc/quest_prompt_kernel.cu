@@ -29,10 +29,10 @@
 // products of 128 x 128 x 128 (2048 cycles at the dense rate) and 2 * 128 * 128 exponentials
 // (1024 cycles); a tile's softmax takes 1100 cycles, its two products 1024, and each of the two
 // hand-overs through a barrier some 300, so a pair takes about 2700; over a whole 8K prompt the
-// tensor core is busy for 63 % of the time.  Measured: an 8K prompt of 32 heads with a 4K window 330 us (1.25
-// PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 103 us (1.34), five tokens over a 32K
-// window 33 us (4.1 TB/s: 19 us of them the stream of K and V at the copy rate, the rest its start
-// and the join).
+// tensor core is busy for 63 % of the time.  Measured: an 8K prompt of 32 heads with a 4K window
+// 328 us (1.26 PFLOP/s of visible pairs), a 2K chunk of 32 / 8 heads 103 us (1.34), five tokens
+// over a 32K window 33 us (4.1 TB/s: 19 us of them the stream of K and V at the copy rate, the
+// rest its start and the join).
 #include <cuda.h>
 #include <math_constants.h>
 
