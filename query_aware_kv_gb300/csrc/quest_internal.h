@@ -119,17 +119,21 @@ struct Params {
 // previous kernel on the stream finishes; every kernel calls griddepcontrol.wait before
 // touching memory an earlier kernel wrote.
 inline cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t s, void** args) {
+                              cudaStream_t s, void** args, int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -212,6 +216,7 @@ struct SpanParams {
   int mode;               // SpanMode
   int sink, window;       // kSpanWindow, in tokens
   int run_pages;          // pages of a split (0: the launch's choice)
+  int cluster;            // a row's CTAs are a cluster (the launch's choice)
 };
 
 constexpr int kSplitRows = 1024;  // rows of a launch that splits them, at most (its counters)

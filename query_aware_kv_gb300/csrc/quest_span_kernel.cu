@@ -46,6 +46,7 @@ namespace {
 constexpr int kSms = 152;  // of a GB300
 constexpr int kMaxSplitsSpan = 64;
 constexpr int kMinBlocks = 4;  // 16-token blocks of a split, at least
+constexpr int kClusterSplits = 8;  // splits of a row whose CTAs are a cluster, at most
 constexpr float kBias = 8.f;
 constexpr float kLazy = 6.f;
 
@@ -78,6 +79,24 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
 __device__ __forceinline__ uint32_t pack(__half a, __half b) {
   const __half2 h = __halves2half2(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The address of `local` in the shared memory of CTA `rank` of the cluster, and a float there.
+__device__ __forceinline__ uint32_t peer_at(const void* local, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float peer_float(uint32_t at) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  __syncthreads();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
 }
 
 // Which dims a lane holds.  k-step s of K Q^T multiplies dims dk .. dk + 3 of lane column c;
@@ -338,8 +357,8 @@ __device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b) {
 }
 
 // grid rows * n_splits (split fastest): split s of a row takes the s-th share of its pages,
-// warp w of the CTA every kSpanWarps-th page of that; a split row's parts are joined by the CTA
-// that comes last to it.
+// warp w of the CTA every kSpanWarps-th page of that.  A split row's parts are joined through
+// the shared memory of a cluster (the row's CTAs), or by the CTA that comes last to the row.
 // kSelect (a chain step without a top-K kernel): every CTA of a row takes the row's selection from
 // the scores itself, the same in each; split 0 also writes the caller's copy.
 template <bool N8, int kSpanWarps, int kCtas, int kDepth, bool kSelect>
@@ -347,6 +366,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
   constexpr int kSpanThreads = 32 * kSpanWarps;
   __shared__ float s_m[kSpanWarps][8], s_l[kSpanWarps][8];
   __shared__ __align__(16) float s_red[kSpanWarps][8 * kHeadDim];
+  __shared__ float s_part[2][8];  // a part's maxima and sums, for the cluster
   __shared__ int s_flag;
   const Params& p = sp.p;
   pdl_wait();
@@ -564,6 +584,12 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
         p.lse[head0 + h] = M == -CUDART_INF_F
                                ? -CUDART_INF_F
                                : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+    } else if (sp.cluster) {
+      s_red[0][o] = A;  // (this thread's alone to read and write)
+      if (d == 0) {
+        s_part[0][h] = M;
+        s_part[1][h] = Z;
+      }
     } else {
       p.part_acc[(mine + h) * kHeadDim + d] = A;
       if (d == 0) {
@@ -572,7 +598,37 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
       }
     }
   }
-  if (p.n_splits > 1) {
+  if (p.n_splits > 1 && sp.cluster) {
+    // ---- every CTA of the row (rank = split) joins its share of the outputs
+    const int n = p.n_splits;
+    cluster_barrier();
+    for (int o = split * kSpanThreads + (int)threadIdx.x; o < G * kHeadDim;
+         o += n * kSpanThreads) {
+      const int h = o / kHeadDim, d = o % kHeadDim;
+      float m[kClusterSplits], z[kClusterSplits], a[kClusterSplits];
+#pragma unroll
+      for (int e = 0; e < kClusterSplits; ++e) {
+        const int from = min(e, n - 1);
+        m[e] = peer_float(peer_at(&s_part[0][h], from));
+        z[e] = peer_float(peer_at(&s_part[1][h], from));
+        a[e] = peer_float(peer_at(&s_red[0][o], from));
+      }
+      float M = -CUDART_INF_F, Z = 0.f, A = 0.f;
+#pragma unroll
+      for (int e = 0; e < kClusterSplits; ++e) M = fmaxf(M, m[e]);
+#pragma unroll
+      for (int e = 0; e < kClusterSplits; ++e) {
+        const float f = e >= n || m[e] == -CUDART_INF_F ? 0.f : exp2f(m[e] - M);
+        Z = fmaf(z[e], f, Z);
+        A = fmaf(a[e], f, A);
+      }
+      p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
+      if (d == 0 && p.lse)
+        p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
+                                              : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+    }
+    cluster_barrier();  // no CTA leaves while another may still read its shared memory
+  } else if (p.n_splits > 1) {
     // ---- the last CTA of the row joins its parts
     const int n = p.n_splits;
     if (arrive_last<kSpanThreads, false>(&p.decode_arrive[row], (unsigned)n, &s_flag)) {
@@ -653,17 +709,31 @@ static SpanShape span_shape(bool narrow, long long rows) {
 // first (32 rows of 64K tokens: 96 us at 9 splits, 288 CTAs on 304 places, 143 us at 10), unless
 // two waves fill much better than one (64 rows: 84 % and 95 %; ragged ones took 86 us at 4
 // splits and 66 at 9).
-static int span_splits(const SpanParams& sp, const SpanShape& shape, int pages) {
+struct SpanSplits {
+  int n;
+  bool cluster;
+};
+
+static SpanSplits span_splits(const SpanParams& sp, const SpanShape& shape, int pages) {
   const long long rows = (long long)sp.p.B * sp.p.Hkv;
-  if (rows > kSplitRows) return 1;
+  if (rows > kSplitRows) return {1, false};
   if (sp.run_pages)
-    return std::max(1, std::min((pages + sp.run_pages - 1) / sp.run_pages, kMaxSplitsSpan));
+    return {std::max(1, std::min((pages + sp.run_pages - 1) / sp.run_pages, kMaxSplitsSpan)),
+            false};
   const long long slots = (long long)kSms * shape.ctas;
   long long s = std::max<long long>(1, slots / rows);
   const long long two = 2 * slots / rows;
   if (rows * s * 100 < slots * 88 && rows * two * 100 >= 2 * slots * 94) s = two;
   const int blocks = pages * (sp.p.P / 16);
-  return (int)std::max<long long>(1, std::min<long long>({s, blocks / kMinBlocks, kMaxSplitsSpan}));
+  const int n =
+      (int)std::max<long long>(1, std::min<long long>({s, blocks / kMinBlocks, kMaxSplitsSpan}));
+  // Short rows (a warp of eight splits has four blocks at most) wait on latencies, and two of
+  // them are those of the parts through global memory: their CTAs are a cluster instead.  Up
+  // to 128 SMs' worth, which clusters of eight find room for at once.
+  const int few = std::min(n, kClusterSplits);
+  if (few > 1 && blocks <= few * shape.warps * 4 && rows * few <= 128LL * shape.ctas)
+    return {few, true};
+  return {n, false};
 }
 
 size_t span_max_parts(int batch, int hkv, bool user) {
@@ -679,22 +749,25 @@ bool span_selects(const SpanParams& sp, int pages) {
   const long long rows = (long long)sp.p.B * sp.p.Hkv;
   const SpanShape shape = span_shape(true, rows);
   return sp.p.Hq == sp.p.Hkv && sp.p.max_pages <= 4096 &&
-         rows * span_splits(sp, shape, pages) <= (long long)kSms * shape.ctas;
+         rows * span_splits(sp, shape, pages).n <= (long long)kSms * shape.ctas;
 }
 
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s) {
   const long long rows = (long long)sp.p.B * sp.p.Hkv;
   const SpanShape shape = span_shape(narrow, rows);
   SpanParams pp = sp;
-  pp.p.n_splits = span_splits(sp, shape, pages);
+  const SpanSplits splits = span_splits(sp, shape, pages);
+  pp.p.n_splits = splits.n;
+  pp.cluster = splits.cluster ? 1 : 0;
   void* args[] = {&pp};
-  const dim3 grid((unsigned)(rows * pp.p.n_splits)), block(32 * shape.warps);
-  if (!sp.p.chain_select) return launch_pdl(shape.fn, grid, block, 0, s, args);
+  const dim3 grid((unsigned)(rows * splits.n)), block(32 * shape.warps);
+  const int together = splits.cluster ? splits.n : 1;
+  if (!sp.p.chain_select) return launch_pdl(shape.fn, grid, block, 0, s, args, together);
   const void* fn = (const void*)span_kernel<true, 8, 2, 1, true>;
   const size_t smem = topk_smem_bytes(sp.p.max_pages) + 256 * 4 + (size_t)sp.p.top_k * 4;
   const cudaError_t e = ensure_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, grid, block, smem, s, args);
+  return launch_pdl(fn, grid, block, smem, s, args, together);
 }
 
 }  // namespace quest
