@@ -651,18 +651,42 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
         }
       }
       __syncthreads();
+      // four outputs a thread; threads left over take every groups-th part of the same ones (one
+      // output a thread took 27 us where this takes 17: four e4m3 rows of eight heads, 64 splits)
+      const int units = G * kHeadDim / 4, groups = max(1, kSpanThreads / units);
+      float4* shares = reinterpret_cast<float4*>(&s_red[1][0]);  // [groups][units]
+      for (int u0 = 0; u0 < units; u0 += kSpanThreads) {
+        const int u = groups > 1 ? (int)threadIdx.x % units : u0 + (int)threadIdx.x;
+        const int grp = groups > 1 ? (int)threadIdx.x / units : 0;
+        const int h = u / (kHeadDim / 4);
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = grp; s0 < n; s0 += 8 * groups) {  // eight loads side by side
+          float4 x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int s = s0 + e * groups;
+            x[e] = s < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s, h) * kHeadDim) +
+                                  u % (kHeadDim / 4))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float f = msc[h * n + min(s0 + e * groups, n - 1)];
+            A.x = fmaf(x[e].x, f, A.x);
+            A.y = fmaf(x[e].y, f, A.y);
+            A.z = fmaf(x[e].z, f, A.z);
+            A.w = fmaf(x[e].w, f, A.w);
+          }
+        }
+        shares[grp * units + u] = A;
+      }
+      __syncthreads();
       for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
         const int h = o / kHeadDim, d = o % kHeadDim;
-        float A = 0.f;
-        for (int s0 = 0; s0 < n; s0 += 8) {  // eight loads side by side, the last few too
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = s0 + e < n ? __ldcg(p.part_acc + slot(s0 + e, h) * kHeadDim + d) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) A = fmaf(x[e], s0 + e < n ? msc[h * n + s0 + e] : 0.f, A);
-        }
         const float M = s_m[0][h], Z = s_l[0][h];
+        float A = 0.f;
+        for (int grp = 0; grp < groups; ++grp)
+          A += reinterpret_cast<const float*>(shares)[grp * units * 4 + o];
         p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
         if (d == 0 && p.lse)
           p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
@@ -727,11 +751,12 @@ static SpanSplits span_splits(const SpanParams& sp, const SpanShape& shape, int 
   const int blocks = pages * (sp.p.P / 16);
   const int n =
       (int)std::max<long long>(1, std::min<long long>({s, blocks / kMinBlocks, kMaxSplitsSpan}));
-  // Short rows (a warp of eight splits has four blocks at most) wait on latencies, and two of
-  // them are those of the parts through global memory: their CTAs are a cluster instead.  Up
-  // to 128 SMs' worth, which clusters of eight find room for at once.
+  // Short rows (a warp of eight splits has eight blocks at most) wait on latencies, and three of
+  // them are those of the parts through global memory: their CTAs are a cluster instead (e4m3,
+  // 12 rows of eight heads, window 1000: 8.7 us against 12.5, 8000: 17.0 and 17.6, 16000: 26.1
+  // and 21.0).  Up to 128 SMs' worth, which clusters of eight find room for at once.
   const int few = std::min(n, kClusterSplits);
-  if (few > 1 && blocks <= few * shape.warps * 4 && rows * few <= 128LL * shape.ctas)
+  if (few > 1 && blocks <= few * shape.warps * 8 && rows * few <= 128LL * shape.ctas)
     return {few, true};
   return {n, false};
 }
