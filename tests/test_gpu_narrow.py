@@ -173,6 +173,19 @@ def test_dense(geom, pps):
     check(cache, ref, qq, out, lse, lambda b, g: torch.ones((1, LENS[b]), dtype=torch.bool))
 
 
+@pytest.mark.parametrize("geom", [(2, 2, 16), (4, 2, 16), (4, 1, 32), (8, 1, 16)], ids=str)
+@pytest.mark.parametrize("window", [700, 6000, 2 ** 31 - 1])
+def test_a_row_over_many_work_items(geom, window):
+    """A row that a few work items share (their CTAs a cluster), and one that many do."""
+    lens = [11003]
+    cache, ref = filled(geom, lens)
+    ws = q.narrow_workspace(cache)
+    qq = torch.randn((1, geom[0], 128), device="cuda").half()
+    out, lse = q.narrow_window_decode(cache, qq, 3, window, ws)
+    ok(ws)
+    check(cache, ref, qq, out, lse, lambda b, g: R.window_mask(lens[b], 1, 3, window, "cpu"))
+
+
 @pytest.mark.parametrize("sink,window", [(0, 1), (4, 7), (3, 100), (40, 33), (300, 64), (0, 2 ** 31 - 1)])
 @pytest.mark.parametrize("geom", GEOMS, ids=str)
 def test_window(geom, sink, window):

@@ -356,6 +356,33 @@ def test_many_rows(batch, hkv):
     check(cache, qq[:, None], out[:, None], lse[:, None], 3, 50, False)
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 3), (8, 2), (8, 1)])
+@pytest.mark.parametrize("window", [600, 5000, 12000])
+def test_a_row_over_many_work_items(hq, hkv, window):
+    """Rows that a few work items share, those that many do, and one that sees one token."""
+    lens = [12500, 1]
+    cache = make(lens, hq, hkv, 16, seed=17)
+    ws = q.window_workspace(cache)
+    qq = torch.randn((2, hq, 128), device="cuda").half()
+    out, lse = q.window_decode(cache, qq, 4, window, ws)
+    ok(ws)
+    check(cache, qq[:, None], out[:, None], lse[:, None], 4, window, False)
+
+
+@pytest.mark.parametrize("hq,hkv,pps", [(8, 1, 2), (8, 1, 0), (4, 2, 1), (1, 1, 3)])
+def test_many_split_rows(hq, hkv, pps):
+    """More rows than SMs, each over several work items."""
+    batch = 200
+    lens = [(37 * b) % 411 for b in range(batch)]
+    cache = make(lens, hq, hkv, 16, seed=18)
+    o = q.opts(pages_per_split=pps)
+    ws = q.window_workspace(cache, 1, o)
+    qq = torch.randn((batch, hq, 128), device="cuda").half()
+    out, lse = q.window_decode(cache, qq, 3, 350, ws, o)
+    ok(ws)
+    check(cache, qq[:, None], out[:, None], lse[:, None], 3, 350, False)
+
+
 def test_one_workspace_for_every_length():
     """A workspace sized for a long chunk serves shorter ones, split or not, in any order."""
     cache = make([1500, 800], 8, 2, 16, seed=16)
