@@ -214,7 +214,10 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_pages_kernel(Params p, 
   const int phys = p.block_table[(size_t)b * p.max_pages + page];
   if (phys < 0 || phys >= p.num_phys) return;
   const int s0 = max(0, L - page * P);
-  if (s0 > 0) {  // the open page becomes complete: not where the chunk meets an unmapped page
+  // The open page becomes complete: not where the chunk meets an unmapped page.  (Asked of the
+  // first page alone, and by the block index: by s0 every block paid, 155 us for the 32K prompt's
+  // 150.)
+  if (blockIdx.y == 0 && s0 > 0) {
     const int last = (L + n - 1) / P;
     bool bad = false;
 #pragma unroll 8
