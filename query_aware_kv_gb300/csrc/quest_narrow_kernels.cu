@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_open_kernel(Params p, N
                                                                      const __half* k,
                                                                      const __half* v, int n) {
   __shared__ int s_flag;
-  // (nothing read before the wait is written by the pages' kernel, which starts this one only
-  // after its own wait)
+  pdl_wait();  // before any read: the lengths and the table may be an earlier call's work
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int g = blockIdx.x * kNarrowWarps + (threadIdx.x >> 5);
   const int L = p.seq_lens[b];
@@ -265,7 +264,6 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_open_kernel(Params p, N
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
     report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);
   }
-  pdl_wait();
   const bool ok = fits && !__syncthreads_or(bad >= 0);
   const int e = ok ? (L + n) % P : 0;
   if (e > 0 && g < p.Hkv) {
