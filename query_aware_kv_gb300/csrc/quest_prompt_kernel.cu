@@ -55,6 +55,7 @@ constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
 constexpr int kKvStages = 5;         // K and V tiles in flight, alternating
+constexpr int kScores = 3;           // barriers of a query tile's scores, in turn
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 dims of every row: one 128-byte swizzle span
 constexpr float kBias = 8.f;
 constexpr float kLazy = 6.f;
@@ -240,9 +241,13 @@ __device__ __forceinline__ bool elect_lane() {
 struct Bars {
   uint64_t q_full;
   uint64_t kv_full[kKvStages];
-  // S of query tile t and K / V tile j is in s_full[t][j & 1]; its completion also says that
-  // Q K^T (t, j) and P V (t, j - 1) have read their K and V tiles
-  uint64_t s_full[2][2], p_full[2], o_full[2], drain[2];
+  // S of query tile t and K / V tile j is in s_full[t][j % 3]; its completion also says that
+  // Q K^T (t, j) and P V (t, j - 1) have read their K and V tiles.  Three of them, so that none
+  // completes a further phase while someone still has to ask for the one before: the fetch of
+  // tile j waits for the scores of tile j - 2, and the next phase there, tile j + 1's, comes
+  // after P V (j) and so after the fetch of both its tiles (with two, tile j's scores, which V (j)
+  // has no part in, could overtake a V warp that was late, whose wait then never ended).
+  uint64_t s_full[2][kScores], p_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int give_up;
 };
@@ -342,8 +347,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&bars.kv_full[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.s_full[t][0], 1);
-      mbar_init(&bars.s_full[t][1], 1);
+      for (int i = 0; i < kScores; ++i) mbar_init(&bars.s_full[t][i], 1);
       mbar_init(&bars.drain[t], 1);
       mbar_init(&bars.p_full[t], two ? 5 : 4);
       mbar_init(&bars.o_full[t], 1);
@@ -419,7 +423,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           return 0;
         };
         now = checked(now, j0 * PPT + lane);
-        int st = kv;
+        int st = kv, sc = 0;  // the stage; the barrier and phase of the scores of tile j - 2
+        uint32_t ph = 0;
         bool ok = true;
         int fetched = 0;
         for (int j = j0; j < j1; ++j) {
@@ -431,9 +436,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // K (j) takes the stage of V (j - 3), V (j) that of K (j - 2): both are free once
           // the scores of tile j - 2 are there
           if (j - j0 >= 2) {
-            const uint32_t ph = (uint32_t)((j - j0 - 2) >> 1) & 1;
-            bool free = prompt_wait(p, &bars.s_full[0][(j - j0) & 1], ph, give_up);
-            if (n_q > 1) free = free && prompt_wait(p, &bars.s_full[1][(j - j0) & 1], ph, give_up);
+            bool free = prompt_wait(p, &bars.s_full[0][sc], ph, give_up);
+            if (n_q > 1) free = free && prompt_wait(p, &bars.s_full[1][sc], ph, give_up);
+            if (++sc == kScores) {
+              sc = 0;
+              ph ^= 1u;
+            }
             if (!__all_sync(0xffffffffu, free)) {
               ok = false;
               break;
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // p_full, beside the softmax warps': one wait for both.
       if (two && t == 0 && lane == 0) mbar_arrive(&bars.p_full[0]);
       if (ok) qk(0, &bars.s_full[t][0]);
-      int sv = 1, sk = 2;  // stages of the V and the next K tile
+      int sv = 1, sk = 2, sc = 1;  // stages of the V and the next K tile, the next scores' barrier
       uint32_t round_v = 0, round_k = 0;
       for (int j = j0; j < j1 && ok; ++j) {
         const bool more = j + 1 < j1;
@@ -541,7 +549,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (!more) commit(&bars.o_full[t]);
         }
         __syncwarp();
-        if (more) qk(sk, &bars.s_full[t][(j - j0 + 1) & 1]);
+        if (more) qk(sk, &bars.s_full[t][sc]);
+        if (++sc == kScores) sc = 0;
         if (two && lane == 0) mbar_arrive(&bars.p_full[t ^ 1]);
         __syncwarp();
         if ((sv += 2) >= kKvStages) {
@@ -573,8 +582,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int r0 = pos0 + tok0 + t * TT;
       const int r1 = min(r0 + TT, end) - 1;
       for (int j = j0; j < j1; ++j) {
-        ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(j - j0) & 1],
-                                                 (uint32_t)((j - j0) >> 1) & 1, give_up));
+        const uint32_t turn = (uint32_t)(j - j0) / kScores;  // (counters would spill here)
+        ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(uint32_t)(j - j0) - turn * kScores],
+                                                 turn & 1, give_up));
         if (!ok) break;
         const int i0 = j * PPT;
         fence_after();
