@@ -194,6 +194,9 @@ int quest_decode_launches(const quest_cache_t* cache, int32_t top_k, const quest
  * decode work item's bounded wait runs out and the call reports QUEST_ERR_TIMEOUT.  For
  * testing the timeout path; outputs are then unspecified. */
 #define QUEST_DEBUG_WITHHOLD_SELECTION 1
+/* quest_window_prefill of more than one token only: never fetch the last tile of values, so
+ * that the bounded wait for it runs out (QUEST_ERR_TIMEOUT).  As above. */
+#define QUEST_DEBUG_WITHHOLD_VALUES 2
 
 /* Bytes of workspace the calls below need for this cache, top_k and opts; 0 if the
  * arguments are invalid (see quest_last_error). */
@@ -503,7 +506,7 @@ int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
  * seq_lens[b] - n_tokens + i; out: fp16 of the same shape; lse: fp32
  * [batch][n_tokens][num_q_heads] or NULL.  In a sequence with fewer than n_tokens tokens
  * the rows at negative positions see nothing.  n_tokens = 0 does nothing.
- * opts: pages_per_split. */
+ * opts: pages_per_split, wait_limit_ns, debug_flags. */
 int quest_window_prefill(const quest_cache_t* cache, const void* q, int32_t n_tokens,
                          int32_t sink_tokens, int32_t window, void* out, float* lse, void* ws,
                          size_t ws_bytes, const quest_opts_t* opts, quest_stream_t stream);

@@ -6,7 +6,7 @@ of 8-bit pages (``NarrowCache``) and attention with a sliding window and sink to
 The names below mirror the C entry points of ``include/quest.h``.
 """
 from ._lib import (  # noqa: F401
-    EXPORTS, HEAD_DIM, QUEST_DEBUG_WITHHOLD_SELECTION, QUEST_ERR_BAD_LENGTH,
+    EXPORTS, HEAD_DIM, QUEST_DEBUG_WITHHOLD_SELECTION, QUEST_DEBUG_WITHHOLD_VALUES, QUEST_ERR_BAD_LENGTH,
     QUEST_ERR_BAD_PAGE, QUEST_ERR_BAD_SELECTION, QUEST_ERR_CUDA, QUEST_ERR_INVALID_ARG,
     QUEST_ERR_TIMEOUT, QUEST_ERR_UNSUPPORTED, QUEST_ERR_WORKSPACE, QUEST_MAX_PAGES, QUEST_OK,
     QUEST_PATH_AUTO, QUEST_PATH_CHAIN, QUEST_PATH_FUSED, QUEST_PATH_STREAM,

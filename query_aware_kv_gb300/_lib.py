@@ -31,6 +31,7 @@ QUEST_ERR_BAD_LENGTH = 7
 QUEST_ERR_BAD_SELECTION = 8
 QUEST_MAX_PAGES = 16384
 QUEST_DEBUG_WITHHOLD_SELECTION = 1
+QUEST_DEBUG_WITHHOLD_VALUES = 2
 QUEST_PATH_AUTO, QUEST_PATH_FUSED, QUEST_PATH_CHAIN, QUEST_PATH_STREAM = 0, 1, 2, 3
 HEAD_DIM = 128
 

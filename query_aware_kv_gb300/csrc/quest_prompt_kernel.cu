@@ -194,7 +194,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 constexpr uint32_t kIdescQK = 1u << 4 | (kTileTokens >> 3) << 17 | (kTileRows >> 4) << 24;
 constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kTileRows >> 4) << 24;
 
-// ---- bounded waits: a wait that runs out sets the CTA's give-up flag, and everyone leaves
+// ---- bounded waits: a wait that runs out sets the CTA's give-up flag, everyone leaves the work,
+// and the CTA then waits for what it has in flight (settle)
 // (Everything this kernel calls is inlined: no call makes the compiler save registers.)
 __device__ __forceinline__ void record(const Params& p, int code, int b, int page) {
   if (atomicCAS(p.status, 0, code) == 0) {
@@ -227,6 +228,16 @@ __device__ __forceinline__ bool prompt_wait(const Params& p, uint64_t* bar, uint
   return mbar_try_wait(bar, parity) || prompt_wait_slow(p, bar, parity, give_up);
 }
 
+// Whether a phase that nothing holds up any more (copies and products that were issued) is over;
+// a second at most.
+__device__ __forceinline__ bool settle(uint64_t* bar, uint32_t parity) {
+  const long long t0 = global_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (global_ns() - t0 > kDefaultWaitNs) return false;
+  return true;
+}
+
 // One lane of the warp, the same one every time; the branch on it stays uniform for the
 // compiler, which keeps descriptors in uniform registers (behind `lane == 0` every product
 // took it about 90 cycles to issue, and a tile pair waited 4100 cycles for the issue warp).
@@ -250,6 +261,7 @@ struct Bars {
   uint64_t s_full[2][kScores], p_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int give_up;
+  int fetched[2];  // K and V tiles whose copies have been issued
 };
 static_assert(sizeof(Bars) <= 256, "barrier area");
 
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&bars.p_full[t], two ? 5 : 4);
       mbar_init(&bars.o_full[t], 1);
     }
-    bars.give_up = 0;
+    bars.give_up = bars.fetched[0] = bars.fetched[1] = 0;
     fence_mbar_init();
   }
   if (warp == 9) tmem_alloc(&bars.tmem);
@@ -425,9 +437,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         now = checked(now, j0 * PPT + lane);
         int st = kv, sc = 0;  // the stage; the barrier and phase of the scores of tile j - 2
         uint32_t ph = 0;
-        bool ok = true;
-        int fetched = 0;
-        for (int j = j0; j < j1; ++j) {
+        int j = j0;
+        for (; j < j1; ++j) {
+          // (a test of the waits: the last V tile of a work item never comes)
+          if (kv && j == j1 - 1 && (p.debug_flags & QUEST_DEBUG_WITHHOLD_VALUES)) break;
           const int at = (j - j0) * PPT & 31;
           if (at == 0 && j > j0) {
             now = checked(next, j * PPT + lane);
@@ -442,10 +455,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               sc = 0;
               ph ^= 1u;
             }
-            if (!__all_sync(0xffffffffu, free)) {
-              ok = false;
-              break;
-            }
+            if (!__all_sync(0xffffffffu, free)) break;
           }
           const bool leader = elect_lane();
           if (leader) mbar_arrive_expect_tx(&bars.kv_full[st], kTileBytes);
@@ -457,21 +467,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                        kv ? &map_v : &map_k, (phys * p.Hkv + g) * (P / 8), &bars.kv_full[st]);
           }
           __syncwarp();
-          ++fetched;
           if ((st += 2) >= kKvStages) st -= kKvStages;
         }
-        if (!ok) {  // leave only when every copy of this warp has landed
-          for (int f = max(0, fetched - kKvStages); f < fetched; ++f) {
-            const int u = 2 * f + kv;
-            for (int i = 0; i < 1 << 20; ++i)
-              if (mbar_try_wait(&bars.kv_full[u % kKvStages], (u / kKvStages) & 1)) break;
-          }
-        }
+        if (lane == 0) bars.fetched[kv] = j - j0;
       }
-      // (the queries too: no product waits for them where no token is visible)
-      if (kv == 0)
-        for (int i = 0; i < 1 << 20; ++i)
-          if (mbar_try_wait(&bars.q_full, 0)) break;
     } else if (warp - 9 < 2 * n_q - 1 && j1 > j0) {
       // ---- issue: warp 9 the products of query tile 0, warp 11 those of tile 1.  (One warp for
       // both spent 1000 cycles of every 3270 between its products, on waits and commits; the
@@ -561,12 +560,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           sk -= kKvStages;
           ++round_k;
         }
-      }
-      if (!ok) {  // products in flight finish before their memory goes
-        if (elect_lane()) commit(&bars.drain[t]);
-        __syncwarp();
-        for (int i = 0; i < 1 << 20; ++i)
-          if (mbar_try_wait(&bars.drain[t], 0)) break;
       }
     }
   } else {
@@ -776,8 +769,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   }
   fence_before();
-  const bool any_again = __syncthreads_or(again);
+  bool any_again = __syncthreads_or(again);
   fence_after();
+  if (*give_up) {  // (nobody sets it any more)
+    // A wait ran out: copies and products in flight end before their memory goes.  (Otherwise the
+    // results were waited for, and with them everything that went into them.)
+    any_again = false;
+    if (warp == 9 || warp == 11) {
+      if (elect_lane()) commit(&bars.drain[warp == 11]);  // the products that this thread issued
+      __syncwarp();
+      settle(&bars.drain[warp == 11], 0);
+    } else if (warp == 8 && lane < kKvStages) {
+      // copies into stage `lane`: K tile j is number 2 j of all, V tile j number 2 j + 1, number u
+      // goes to stage u % kKvStages, and as u and u + kKvStages are a K and a V tile, the later of
+      // them only once the earlier has been used: phase after phase
+      int phases = 0;
+      for (int kv = 0; kv < 2; ++kv)
+        for (int u = kv; u < 2 * bars.fetched[kv]; u += 2) phases += u % kKvStages == lane;
+      if (phases > 0) settle(&bars.kv_full[lane], (uint32_t)(phases - 1) & 1);
+    } else if (warp == 10 && lane == 0) {
+      settle(&bars.q_full, 0);
+    }
+    __syncthreads();
+  }
   if (warp == 9) tmem_free(tmem);
 
   // An infinity or NaN among the values of a tile reaches all of its rows, as 0 * NaN, those too

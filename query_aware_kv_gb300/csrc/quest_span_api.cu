@@ -364,6 +364,8 @@ static int window_rows(const quest_cache_t* cache, const void* q, int32_t n_toke
     sp.p.q = static_cast<const __half*>(q);
     sp.p.out = static_cast<__half*>(out);
     sp.p.lse = lse;
+    if (opts && opts->wait_limit_ns > 0) sp.p.wait_limit_ns = opts->wait_limit_ns;
+    sp.p.debug_flags = opts ? opts->debug_flags : 0;
     sp.p.n_splits =
         prompt_splits(sp.p, n_tokens, prompt_pages(*cache, n_tokens, sink_tokens, window),
                       user_split(opts));
