@@ -447,6 +447,8 @@ int quest_narrow_append(const quest_narrow_cache_t* cache, const void* k_new, co
 /* quest_sparse_decode over a narrow cache: attention over the pages idx[b][g][0 .. count-1]
  * (every one in [0, N_b), none twice).  fp32 sums over the exact products of q and the
  * codes; the softmax weights enter the second product as two fp16 numbers each (22 bits).
+ * A NaN in the query, or in a key among those pages, gives NaN in out and lse (every narrow
+ * decode).
  * opts: pages_per_split. */
 int quest_narrow_sparse_decode(const quest_narrow_cache_t* cache, const void* q,
                                const int32_t* idx, const int32_t* count, int32_t top_k, void* out,
@@ -479,7 +481,8 @@ int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, c
  * max_pages * page_size or more is plain causal attention.  Pages without a visible token
  * are never read, and neither are their block-table entries (pages that fell behind the
  * window may be unmapped).  What hidden tokens hold (infinities, NaN) does not reach a
- * result.  A row that sees no token gives out = 0, lse = -inf.
+ * result.  A row that sees no token gives out = 0, lse = -inf; a row whose query, or a key that
+ * it sees, holds a NaN gives NaN in out and lse.
  */
 
 /* Bytes of workspace of quest_window_decode (n_tokens = 1) and of quest_window_prefill with

@@ -873,8 +873,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
                         : make_float4(0.f, 0.f, 0.f, 0.f);
     if (s0 == 0) {
       M = warp_max(fmaxf(x.x, y.x));
-      fx = x.x == -CUDART_INF_F ? 0.f : ex2(x.x - M);  // an empty split has m = -inf, l and O 0
-      fy = y.x == -CUDART_INF_F ? 0.f : ex2(y.x - M);
+      // an empty split has m = -inf, l and O 0; with NaN scores alone m = -inf too, and l and O NaN
+      fx = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
+      fy = y.x == -CUDART_INF_F ? (y.y == 0.f ? 0.f : 1.f) : ex2(y.x - M);
       Z = warp_sum(fmaf(x.y, fx, y.y * fy));
     }
 #pragma unroll
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
       A.w = fmaf(a[e].w, f, A.w);
     }
   }
-  const bool none = M == -CUDART_INF_F;
+  const bool none = Z == 0.f;
   const float inv = none ? 0.f : 1.f / Z;
   reinterpret_cast<uint2*>(p.out + (size_t)at * kHeadDim)[lane] =
       none ? make_uint2(0u, 0u) : make_uint2(pack2(A.x * inv, A.y * inv), pack2(A.z * inv, A.w * inv));

@@ -116,6 +116,21 @@ struct State {
   float acc[8][4];
 };
 
+// What brings a part of a softmax (reference m, sum l) to the reference M of all parts.  A part
+// without a weight has m = -inf and l = 0.  Scores that are NaN move no maximum but make l one: with
+// m = -inf too such a part is not left out, its NaN goes on.  Whether a row has seen a token is read
+// from its sum alone.
+__device__ __forceinline__ float part_factor(float m, float l, float M) {
+  return m == -CUDART_INF_F ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M);
+}
+// Output and log-sum-exp of a row: A = sum of weights times values, Z = sum of weights.
+__device__ __forceinline__ __half row_out(float A, float Z) {
+  return __float2half_rn(Z == 0.f ? 0.f : A / Z);
+}
+__device__ __forceinline__ float row_lse(float M, float Z) {
+  return Z == 0.f ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+}
+
 // Scores of a block (16 tokens) to weights: updates m, l and rescales acc when the
 // reference moves; returns P^T as fp16 pairs, upper and lower parts.
 __device__ __forceinline__ void weigh(State& st, float (&s)[4], uint32_t& h0, uint32_t& h1,
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
       float M = -CUDART_INF_F;
 #pragma unroll
       for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
-      const float f = st.m[e] == -CUDART_INF_F ? 0.f : exp2f(st.m[e] - M);
+      const float f = part_factor(st.m[e], st.l[e], M);
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
         *reinterpret_cast<float2*>(&s_red[warp][h * kHeadDim + dv<N8>(m, r)]) =
@@ -576,14 +591,11 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
 #pragma unroll
     for (int w = 0; w < kSpanWarps; ++w) {
       A += s_red[w][o];
-      if (s_m[w][h] != -CUDART_INF_F) Z = fmaf(s_l[w][h], exp2f(s_m[w][h] - M), Z);
+      Z = fmaf(s_l[w][h], part_factor(s_m[w][h], s_l[w][h], M), Z);
     }
     if (p.n_splits == 1) {
-      p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
-      if (d == 0 && p.lse)
-        p.lse[head0 + h] = M == -CUDART_INF_F
-                               ? -CUDART_INF_F
-                               : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+      p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
+      if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
     } else if (sp.cluster) {
       s_red[0][o] = A;  // (this thread's alone to read and write)
       if (d == 0) {
@@ -618,14 +630,12 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
       for (int e = 0; e < kClusterSplits; ++e) M = fmaxf(M, m[e]);
 #pragma unroll
       for (int e = 0; e < kClusterSplits; ++e) {
-        const float f = e >= n || m[e] == -CUDART_INF_F ? 0.f : exp2f(m[e] - M);
+        const float f = e >= n ? 0.f : part_factor(m[e], z[e], M);
         Z = fmaf(z[e], f, Z);
         A = fmaf(a[e], f, A);
       }
-      p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
-      if (d == 0 && p.lse)
-        p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
-                                              : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+      p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
+      if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
     }
     cluster_barrier();  // no CTA leaves while another may still read its shared memory
   } else if (p.n_splits > 1) {
@@ -640,9 +650,10 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
         M = warp_max(M);
         for (int s = lane; s < n; s += 32) {
           const float ms = __ldcg(p.part_ml + 2 * slot(s, h));
-          const float f = ms == -CUDART_INF_F ? 0.f : exp2f(ms - M);
+          const float ls = __ldcg(p.part_ml + 2 * slot(s, h) + 1);
+          const float f = part_factor(ms, ls, M);
           msc[h * n + s] = f;
-          Z = fmaf(__ldcg(p.part_ml + 2 * slot(s, h) + 1), f, Z);
+          Z = fmaf(ls, f, Z);
         }
         Z = warp_sum(Z);
         if (lane == 0) {
@@ -687,10 +698,8 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
         float A = 0.f;
         for (int grp = 0; grp < groups; ++grp)
           A += reinterpret_cast<const float*>(shares)[grp * units * 4 + o];
-        p.out[(head0 + h) * kHeadDim + d] = __float2half_rn(M == -CUDART_INF_F ? 0.f : A / Z);
-        if (d == 0 && p.lse)
-          p.lse[head0 + h] = M == -CUDART_INF_F ? -CUDART_INF_F
-                                                : (M - kBias + log2f(Z)) * 0.6931471805599453f;
+        p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
+        if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
       }
       if (threadIdx.x == 0) p.decode_arrive[row] = 0u;
     }
