@@ -482,7 +482,8 @@ int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, c
  * are never read, and neither are their block-table entries (pages that fell behind the
  * window may be unmapped).  What hidden tokens hold (infinities, NaN) does not reach a
  * result.  A row that sees no token gives out = 0, lse = -inf; a row whose query, or a key that
- * it sees, holds a NaN gives NaN in out and lse.
+ * it sees, holds a NaN gives NaN in out and lse.  An infinity among the values that a row sees
+ * goes out as one (both signs of it as NaN).
  */
 
 /* Bytes of workspace of quest_window_decode (n_tokens = 1) and of quest_window_prefill with

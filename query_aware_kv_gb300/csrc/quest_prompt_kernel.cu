@@ -37,6 +37,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 #include "quest_device.cuh"
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       // (m and l of a row that has to be taken again, below; l < 0: it has not)
-      again = ok && mine && j1 > j0 && odd && !none && l <= 3.4e38f;
+      again = ok && mine && j1 > j0 && odd && !none && l <= FLT_MAX;
       __syncwarp();
       *stash(t, row) = again ? make_float2(m, l) : make_float2(0.f, -1.f);
     }
@@ -823,7 +824,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + from + k * kHeadDim);
           const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
           const float x = warp_sum(fmaf(qa.x, ka.x, qa.y * ka.y) + fmaf(qb.x, kb.x, qb.y * kb.y));
-          const float w = ex2(fmaf(x, p.qscale, kBias - m_r));
+          // (a visible infinity counts however small its weight: 0 * inf is not it)
+          const float w =
+              x == -CUDART_INF_F ? 0.f : fmaxf(ex2(fmaf(x, p.qscale, kBias - m_r)), FLT_MIN);
           acc[0] = fmaf(w, va.x, acc[0]);
           acc[1] = fmaf(w, va.y, acc[1]);
           acc[2] = fmaf(w, vb.x, acc[2]);
@@ -873,9 +876,10 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
                         : make_float4(0.f, 0.f, 0.f, 0.f);
     if (s0 == 0) {
       M = warp_max(fmaxf(x.x, y.x));
-      // an empty split has m = -inf, l and O 0; with NaN scores alone m = -inf too, and l and O NaN
-      fx = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
-      fy = y.x == -CUDART_INF_F ? (y.y == 0.f ? 0.f : 1.f) : ex2(y.x - M);
+      // an empty split has m = -inf, l and O 0; with NaN scores alone m = -inf too, and l and O NaN;
+      // an infinite O stays one under any factor
+      fx = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : fmaxf(ex2(x.x - M), FLT_MIN);
+      fy = y.x == -CUDART_INF_F ? (y.y == 0.f ? 0.f : 1.f) : fmaxf(ex2(y.x - M), FLT_MIN);
       Z = warp_sum(fmaf(x.y, fx, y.y * fy));
     }
 #pragma unroll

@@ -36,6 +36,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "quest_device.cuh"
 
@@ -119,9 +120,10 @@ struct State {
 // What brings a part of a softmax (reference m, sum l) to the reference M of all parts.  A part
 // without a weight has m = -inf and l = 0.  Scores that are NaN move no maximum but make l one: with
 // m = -inf too such a part is not left out, its NaN goes on.  Whether a row has seen a token is read
-// from its sum alone.
+// from its sum alone.  A part's share may be an infinity (of a visible value), which no factor may
+// turn into 0 * inf: the smallest normal number adds nothing to any other sum.
 __device__ __forceinline__ float part_factor(float m, float l, float M) {
-  return m == -CUDART_INF_F ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M);
+  return m == -CUDART_INF_F ? (l == 0.f ? 0.f : 1.f) : fmaxf(exp2f(m - M), FLT_MIN);
 }
 // Output and log-sum-exp of a row: A = sum of weights times values, Z = sum of weights.
 __device__ __forceinline__ __half row_out(float A, float Z) {
@@ -371,6 +373,74 @@ __device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b) {
   return x;
 }
 
+// A weight's two fp16 parts times an infinity are NaN (the lower part is 0 or of either sign), and
+// so is a weight below fp16's range.  Where a head's O is not finite although its scores are, the
+// warps of the CTA take the CTA's pages again, token by token, lane l the dims 4 l .. 4 l + 3 with
+// fp32 weights against the CTA's maximum: what leaves is then what the row sees, infinities as
+// infinities.  red: this warp's shares, [G][128].  list: the pages of kSpanList, `count` of them.
+template <bool N8, int kSpanWarps>
+__device__ __forceinline__ void take_again(const SpanParams& sp, int row, int split,
+                                           const int* list, int count,
+                                           const float (&s_m)[kSpanWarps][8], float* red) {
+  const Params& p = sp.p;
+  const int b = row / p.Hkv, g = row % p.Hkv, G = p.Hq / p.Hkv, P = p.P;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowShape x = row_shape(sp, b);
+  if (sp.mode == kSpanList) count = max(0, min(count, x.count));
+  else count = x.count;
+  const int i1 = count * (split + 1) / p.n_splits;
+  const int open_page = (N8 && x.L % P) ? x.L / P : -1;
+#pragma unroll 1
+  for (int h = 0; h < G; ++h) {
+    float M = -CUDART_INF_F;
+    for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
+    const uint2 qw = *reinterpret_cast<const uint2*>(
+        p.q + ((size_t)b * p.Hq + (size_t)g * G + h) * kHeadDim + 4 * lane);
+    const float2 qa = h2f(qw.x), qb = h2f(qw.y);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int i = count * split / p.n_splits + warp; i < i1; i += kSpanWarps) {
+      const int lp = sp.mode == kSpanDense ? i
+                     : sp.mode == kSpanList ? list[i]
+                     : i < x.n_sink ? i : x.first + i - x.n_sink;
+      if (lp < 0 || lp >= x.N) continue;
+      const bool open = lp == open_page;
+      const int phys = open ? 0 : p.block_table[(size_t)b * p.max_pages + lp];
+      if (phys < 0 || phys >= p.num_phys) continue;
+      const size_t at = (size_t)phys * p.Hkv + g;
+      const float ks = N8 && !open ? p.qscale * sp.nar.k_scale[at] : p.qscale;
+      const float vs = N8 && !open ? sp.nar.v_scale[at] : 1.f;
+#pragma unroll 1
+      for (int k = 0; k < P; ++k) {
+        if (!x.vis.token(lp * P + k)) continue;
+        uint2 kw, vw;
+        if (N8 && !open) {
+          const size_t from = (at * P + k) * kHeadDim + 4 * lane;
+          const uint32_t kc = *reinterpret_cast<const uint32_t*>(sp.nar.k_pool + from);
+          const uint32_t vc = *reinterpret_cast<const uint32_t*>(sp.nar.v_pool + from);
+          kw = make_uint2(widen(kc), widen(kc >> 16));
+          vw = make_uint2(widen(vc), widen(vc >> 16));
+        } else {
+          const size_t from = ((open ? (size_t)row : at) * P + k) * kHeadDim + 4 * lane;
+          kw = *reinterpret_cast<const uint2*>((open ? sp.nar.k_open : p.k_pool) + from);
+          vw = *reinterpret_cast<const uint2*>((open ? sp.nar.v_open : p.v_pool) + from);
+        }
+        const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
+        const float s =
+            ks * warp_sum(fmaf(qa.x, ka.x, qa.y * ka.y) + fmaf(qb.x, kb.x, qb.y * kb.y));
+        // (as for parts: no weight but that of a score of -inf is 0)
+        const float w = s == -CUDART_INF_F ? 0.f : vs * fmaxf(exp2f(s - M + kBias), FLT_MIN);
+        acc[0] = fmaf(w, va.x, acc[0]);
+        acc[1] = fmaf(w, va.y, acc[1]);
+        acc[2] = fmaf(w, vb.x, acc[2]);
+        acc[3] = fmaf(w, vb.y, acc[3]);
+      }
+    }
+    *reinterpret_cast<float4*>(red + h * kHeadDim + 4 * lane) =
+        make_float4(acc[0], acc[1], acc[2], acc[3]);
+  }
+}
+
 // grid rows * n_splits (split fastest): split s of a row takes the s-th share of its pages,
 // warp w of the CTA every kSpanWarps-th page of that.  A split row's parts are joined through
 // the shared memory of a cluster (the row's CTAs), or by the CTA that comes last to the row.
@@ -583,32 +653,48 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
   __syncthreads();
   const size_t slot0 = (size_t)row * p.n_splits * G;  // parts: [row][split][head]
   const size_t mine = slot0 + (size_t)split * G;
-  for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
-    const int h = o / kHeadDim, d = o % kHeadDim;
-    float M = -CUDART_INF_F, Z = 0.f, A = 0.f;
+  for (int pass = 0;; ++pass) {
+    bool odd = false;  // (found on the sums: a check of every warp's O cost the e4m3 rows 2 %)
+    for (int o = threadIdx.x; o < G * kHeadDim; o += kSpanThreads) {
+      const int h = o / kHeadDim, d = o % kHeadDim;
+      float M = -CUDART_INF_F, Z = 0.f, A = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
+      for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, s_m[w][h]);
 #pragma unroll
-    for (int w = 0; w < kSpanWarps; ++w) {
-      A += s_red[w][o];
-      Z = fmaf(s_l[w][h], part_factor(s_m[w][h], s_l[w][h], M), Z);
-    }
-    if (p.n_splits == 1) {
-      p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
-      if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
-    } else if (sp.cluster) {
-      s_red[0][o] = A;  // (this thread's alone to read and write)
-      if (d == 0) {
-        s_part[0][h] = M;
-        s_part[1][h] = Z;
+      for (int w = 0; w < kSpanWarps; ++w) {
+        A += s_red[w][o];
+        Z = fmaf(s_l[w][h], part_factor(s_m[w][h], s_l[w][h], M), Z);
       }
-    } else {
-      p.part_acc[(mine + h) * kHeadDim + d] = A;
-      if (d == 0) {
-        p.part_ml[2 * (mine + h)] = M;
-        p.part_ml[2 * (mine + h) + 1] = Z;
+      odd |= !(fabsf(A) <= FLT_MAX) && Z <= FLT_MAX;
+      if (p.n_splits == 1) {
+        p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
+        if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
+      } else if (sp.cluster) {
+        s_red[0][o] = A;  // (this thread's alone to read and write)
+        if (d == 0) {
+          s_part[0][h] = M;
+          s_part[1][h] = Z;
+        }
+      } else {
+        p.part_acc[(mine + h) * kHeadDim + d] = A;
+        if (d == 0) {
+          p.part_ml[2 * (mine + h)] = M;
+          p.part_ml[2 * (mine + h) + 1] = Z;
+        }
       }
     }
+    if (!__syncthreads_or(odd) || pass) break;
+    const int* list = p.sel_idx + (size_t)row * p.top_k;
+    int given = 0;
+    if constexpr (kSelect) {
+      extern __shared__ __align__(16) unsigned char s_sel[];
+      list = reinterpret_cast<const int*>(s_sel + topk_smem_bytes(p.max_pages)) + 256;
+      given = s_flag;
+    } else if (sp.mode == kSpanList) {
+      given = p.sel_count[row];
+    }
+    take_again<N8, kSpanWarps>(sp, row, split, list, given, s_m, s_red[warp]);
+    __syncthreads();
   }
   if (p.n_splits > 1 && sp.cluster) {
     // ---- every CTA of the row (rank = split) joins its share of the outputs
@@ -632,7 +718,7 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
       for (int e = 0; e < kClusterSplits; ++e) {
         const float f = e >= n ? 0.f : part_factor(m[e], z[e], M);
         Z = fmaf(z[e], f, Z);
-        A = fmaf(a[e], f, A);
+        A = e < n ? fmaf(a[e], f, A) : A;
       }
       p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
       if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);

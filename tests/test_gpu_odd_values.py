@@ -167,3 +167,99 @@ def test_a_nan_key_in_a_narrow_cache(geom, at, pps):
     sees = at >= 480
     assert torch.isnan(out).all() == sees and torch.isnan(lse).all() == sees
     assert torch.isfinite(out).all() != sees
+
+
+@pytest.mark.parametrize("pps", SPLITS)
+@pytest.mark.parametrize("geom", GEOMS, ids=str)
+@pytest.mark.parametrize("n", [1, 3, 150])
+def test_infinities_among_the_values(geom, n, pps):
+    """Rows that see one infinity get it in its dimension and nowhere else, rows that see both signs
+    of it NaN, and one with a weight far below the largest counts like any other."""
+    hq, hkv, P = geom
+    odd = [(0, 690, 5, INF), (0, 3, 6, -INF), (0, 128, 77, INF), (0, 699, 77, -INF), (0, 400, 127, INF),
+           (1, 1, 0, INF), (1, 1, 1, -INF)]
+    cache = make([700, 2], hq, hkv, P, seed=4)
+    qq = torch.randn((2, n, hq, 128), device="cuda").half()
+    # the key of one of them: a score of about -60, far under fp16's smallest weight
+    at = slot(cache, 0, 400)
+    cache.k_pool[at] = 0
+    cache.k_pool[at][:, 8] = -200
+    qq[..., 8] = 3.5
+    clean = cache.v_pool.clone()
+    for b, t, d, x in odd:
+        cache.v_pool[slot(cache, b, t)][:, d] = x
+    visible = [(0, BIG), (4, 55), (3, 1)]
+    got = [run(cache, qq, sink, window, pps) for sink, window in visible]
+    cache.v_pool.copy_(clean)
+    for (sink, window), (out, lse) in zip(visible, got):
+        assert_rows(cache, qq, out, lse, sink, window, odd_v=odd)
+
+
+@pytest.mark.parametrize("pps", SPLITS)
+@pytest.mark.parametrize("geom", GEOMS, ids=str)
+def test_an_infinity_of_little_weight(geom, pps):
+    """The work item that holds the infinity has a maximum far below that of another (a factor of
+    2^-170): its part is not multiplied away."""
+    hq, hkv, P = geom
+    cache = make([700], hq, hkv, P, seed=6)
+    for t in range(700):
+        cache.k_pool[slot(cache, 0, t)] = 0
+        cache.k_pool[slot(cache, 0, t)][:, 8] = 200 if t >= 600 else -200
+    cache.v_pool[slot(cache, 0, 100)][:, 9] = INF
+    for n in (1, 3):
+        qq = torch.randn((1, n, hq, 128), device="cuda").half()
+        qq[..., 8] = 3.35
+        out, lse = run(cache, qq, 0, BIG, pps)
+        assert (out[..., 9] == INF).all() and torch.isfinite(lse).all()
+        out[..., 9] = 0
+        assert torch.isfinite(out).all()
+
+
+def test_many_rows_with_an_infinity():
+    """More rows than are ever split, and rows of CTAs of four warps."""
+    for batch, hkv in [(20, 8), (70, 16)]:
+        lens = [(37 * b) % 211 for b in range(batch)]
+        cache = make(lens, hkv, hkv, 16, seed=15)
+        odd = [(b, lens[b] - 7, b % 128, INF if b % 2 else -INF) for b in range(batch) if lens[b] > 7]
+        clean = cache.v_pool.clone()
+        for b, t, d, x in odd:
+            cache.v_pool[slot(cache, b, t)][:, d] = x
+        qq = torch.randn((batch, 1, hkv, 128), device="cuda").half()
+        out, lse = run(cache, qq, 3, 50, 0)
+        cache.v_pool.copy_(clean)
+        assert_rows(cache, qq, out, lse, 3, 50, odd_v=odd)
+
+
+@pytest.mark.parametrize("name", ["dense", "window", "decode", "step"])
+@pytest.mark.parametrize("pps", [0, 1, 20])
+@pytest.mark.parametrize("geom", GEOMS, ids=str)
+def test_an_infinity_in_the_open_page(geom, pps, name):
+    """The fp16 rows of a narrow cache's open page hold what was written: its infinity goes out,
+    every other dimension is as if it were not there."""
+    hq, hkv, P = geom
+    L = 500  # 20 (P = 32) or 4 (P = 16) tokens in the open page
+    cache, ref, _ = narrow(geom, L, v_odd=[(498, 9, INF), (497, 70, -INF)])
+    K = L // P + 2
+    o = q.opts(pages_per_split=pps)
+    ws = q.narrow_workspace(cache, K, o)
+    qq = torch.randn((1, hq, 128), device="cuda").half()
+    new = torch.randn((2, 1, 1, hkv, 128)).half()
+    if name == "dense":
+        out, lse = q.narrow_dense_decode(cache, qq, ws, o)
+    elif name == "window":
+        out, lse = q.narrow_window_decode(cache, qq, 4, 300, ws, o)
+    elif name == "decode":
+        out, lse = q.narrow_decode(cache, qq, K, ws, o)
+    else:
+        out, lse = q.narrow_decode_step(cache, qq, new[0, 0].cuda(), new[1, 0].cuda(), K, ws, o)
+        ref.write(new[0], new[1])
+        L += 1
+    ok(ws)
+    assert (out[:, :, 9] == INF).all() and (out[:, :, 70] == -INF).all()
+    allowed = R.window_mask(L, 1, 4, 300 if name == "window" else BIG, "cpu")
+    for h in range(hq):
+        k, v = ref.values(0, "k")[h // (hq // hkv)], torch.nan_to_num(ref.values(0, "v")[h // (hq // hkv)], posinf=0, neginf=0)
+        r = R.attend(qq[0, h:h + 1].cpu(), k, v, allowed)
+        got = out[0, h:h + 1].cpu().clone()
+        got[:, [9, 70]] = r[0][:, [9, 70]].half()
+        R.assert_close(got, lse[0, h:h + 1].cpu(), r)
