@@ -185,6 +185,14 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _one_device(**tensors: torch.Tensor) -> None:
+    """A kernel follows every pointer of a cache: all of its tensors are on one device."""
+    (first, t), *rest = tensors.items()
+    for name, x in rest:
+        if x.get_device() != t.get_device():
+            raise ValueError(f"{name} is on another device than {first}")
+
+
 def opts(pages_per_split: int = 0, score_tile_pages: int = 0, max_ctas: int = 0,
          debug_flags: int = 0, wait_limit_ns: int = 0, trace: Optional[torch.Tensor] = None,
          cluster_size: int = 0, sink_pages: int = 0, local_pages: int = 0,
@@ -241,6 +249,8 @@ class PagedCache:
         _need(self.meta, "meta", torch.float16, (B, hkv, max_pages, 2, d))
         _need(self.block_table, "block_table", torch.int32)
         _need(self.seq_lens, "seq_lens", torch.int32, (B,))
+        _one_device(k_pool=self.k_pool, v_pool=self.v_pool, meta=self.meta,
+                    block_table=self.block_table, seq_lens=self.seq_lens)
         self.desc = QuestCacheDesc(B, int(self.num_q_heads), hkv, d, P, max_pages, num_phys,
                                    self.k_pool.data_ptr(), self.v_pool.data_ptr(),
                                    self.meta.data_ptr(), self.block_table.data_ptr(),
@@ -302,6 +312,9 @@ class NarrowCache:
         _need(self.meta, "meta", torch.float16, (B, hkv, max_pages, 2, d))
         _need(self.block_table, "block_table", torch.int32)
         _need(self.seq_lens, "seq_lens", torch.int32, (B,))
+        _one_device(k_pool=self.k_pool, v_pool=self.v_pool, k_scale=self.k_scale,
+                    v_scale=self.v_scale, k_open=self.k_open, v_open=self.v_open,
+                    meta=self.meta, block_table=self.block_table, seq_lens=self.seq_lens)
         self.desc = QuestNarrowCacheDesc(
             B, int(self.num_q_heads), hkv, d, P, max_pages, num_phys, self.k_pool.data_ptr(),
             self.v_pool.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
