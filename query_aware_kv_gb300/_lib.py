@@ -193,6 +193,13 @@ def _one_device(**tensors: torch.Tensor) -> None:
             raise ValueError(f"{name} is on another device than {first}")
 
 
+def _current(dev: int) -> None:
+    """A launch goes to the current device (its default stream, unless the plan has another): not
+    with pointers of `dev` while another one is current."""
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError("the cache is on another device than the current one")
+
+
 def opts(pages_per_split: int = 0, score_tile_pages: int = 0, max_ctas: int = 0,
          debug_flags: int = 0, wait_limit_ns: int = 0, trace: Optional[torch.Tensor] = None,
          cluster_size: int = 0, sink_pages: int = 0, local_pages: int = 0,
@@ -556,6 +563,7 @@ class DecodePlan:
 
     def decode(self, q: torch.Tensor):
         """quest_decode of this step's queries; returns (out, lse)."""
+        _current(self._dev)
         if not self._ok(q, self._qshape):
             _need(q, "q", torch.float16, self._qshape)
             raise ValueError("q is on another device than the cache")
@@ -566,6 +574,7 @@ class DecodePlan:
 
     def step(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor):
         """quest_decode_step: append (k_new, v_new), then decode q; returns (out, lse)."""
+        _current(self._dev)
         if not (self._ok(q, self._qshape) and self._ok(k_new, self._kvshape) and
                 self._ok(v_new, self._kvshape)):
             _need(q, "q", torch.float16, self._qshape)
@@ -669,9 +678,8 @@ def _here(cache, ws: torch.Tensor, *others: torch.Tensor) -> None:
     """The calls go to the current device's stream: the cache, the workspace and the other
     tensors have to be on it."""
     _need(ws, "ws", torch.uint8)
-    dev = torch._C._cuda_getDevice()
-    if cache.k_pool.get_device() != dev:
-        raise ValueError("the cache is on another device than the current one")
+    dev = cache.k_pool.get_device()
+    _current(dev)
     for t in (ws, *others):
         if t is not None and t.get_device() != dev:
             raise ValueError("a tensor is on another device than the cache")
@@ -689,6 +697,7 @@ class NarrowPlan(DecodePlan):
 
     def dense(self, q: torch.Tensor):
         """quest_narrow_dense_decode of this step's queries; returns (out, lse)."""
+        _current(self._dev)
         if not self._ok(q, self._qshape):
             _need(q, "q", torch.float16, self._qshape)
             raise ValueError("q is on another device than the cache")
@@ -732,6 +741,7 @@ class WindowPlan:
 
     def decode(self, q: torch.Tensor):
         """The windowed attention of this step's queries; returns (out, lse)."""
+        _current(self._dev)
         if not (type(q) is torch.Tensor and q.dtype is torch.float16 and
                 q.shape == self._qshape and q.get_device() == self._dev and q.is_contiguous()):
             _need(q, "q", torch.float16, self._qshape)
