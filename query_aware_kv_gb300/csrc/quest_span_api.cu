@@ -52,7 +52,7 @@ int check_narrow(const quest_narrow_cache_t* n) {
 }
 
 int user_split(const quest_opts_t* o) {
-  return o && o->pages_per_split > 0 ? o->pages_per_split : 0;
+  return o && o->pages_per_split > 0 ? std::min(o->pages_per_split, QUEST_MAX_PAGES) : 0;
 }
 
 // Workspace: the header and the counters (zero between calls, and at the same place for every

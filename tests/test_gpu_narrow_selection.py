@@ -8,6 +8,7 @@ import torch
 import query_aware_kv_gb300 as q
 import span_reference as R
 from test_gpu_narrow import assert_cache, check, empty, ok, tokens
+from test_gpu_window import check as check_window
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +146,23 @@ def test_outputs_are_near_the_fp16_caches(hq, hkv):
         assert ((a - z).abs() <= tol).all()
         lim = E + 2 * (132 * 2.0 ** -24 * U + 2.0 ** -20) + 2.0 ** -21 * abs(float(lse2[0, h]))
         assert abs(float(lse[0, h]) - float(lse2[0, h])) <= lim
+
+
+@pytest.mark.parametrize("pps", [16384, 16385, 2 ** 31 - 1])
+def test_splits_longer_than_any_row(pps):
+    """pages_per_split up to the largest number that it holds: one work item a row."""
+    g = torch.Generator().manual_seed(1)
+    cache, ref = filled(8, 2, 16, [900, 30], 60, g)
+    o = q.opts(pages_per_split=pps)
+    ws = q.narrow_workspace(cache, 1, o)
+    qq = torch.randn((2, 8, 128), device="cuda").half()
+    out, lse = q.narrow_dense_decode(cache, qq, ws, o)
+    ok(ws)
+    check(cache, ref, qq, out, lse, lambda b, h: torch.ones((1, ref.length(b)), dtype=torch.bool))
+    fp16 = [torch.randn(cache.k_pool.shape, device="cuda").half() for _ in range(2)]
+    wide = q.PagedCache.allocate_meta(*fp16, cache.block_table, cache.seq_lens, 8)
+    qn = torch.randn((2, 5, 8, 128), device="cuda").half()
+    wws = q.window_workspace(wide, 5, o)
+    out, lse = q.window_prefill(wide, qn, 4, 700, wws, o)
+    ok(wws)
+    check_window(wide, qn, out, lse, 4, 700, True)
