@@ -28,11 +28,12 @@
 // ones keep fp16's full precision down to 2^-22 of the reference.
 //
 // Measured (calls back to back): eight ragged 32K sequences of 32 heads, 4K window, fp16:
-// 80.9 us, 6.65 TB/s; full e4m3 attention over four 64K sequences of 32 / 8 heads: 94.6 us,
+// 81.0 us, 6.63 TB/s; full e4m3 attention over four 64K sequences of 32 / 8 heads: 94.4 us,
 // 5.7 TB/s; 16 ragged e4m3 sequences of 32 / 8 heads, 8K window: 56 us, 4.8 TB/s (256 CTAs on
 // 304 places, each waiting on its loads: DRAM at 58 %).  Tried and slower: equal runs of all
 // rows' pages (a run that crosses into a new row pays that row's latency again), and copies
-// through shared memory with cp.async (128 us for the 94.6).
+// through shared memory with cp.async (128 us for the 94.4).  A CTA that takes its pages again (a NaN or
+// an infinity among the values that it sees) is slow: the 94.4 us become 1.8 ms.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -808,8 +809,9 @@ __global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams
 }  // namespace
 
 // Launch shapes: warps of a CTA, CTAs that an SM holds, blocks in flight a warp.  A narrow
-// block is 32 registers a lane and leaves room for 16 warps of one block; an fp16 block is 64,
-// for 8 warps of two.  With more rows than SMs the fp16 rows get CTAs of four warps, two of
+// block is 32 registers a lane and leaves room for 16 warps of one block (at 128 registers a lane,
+// of which the compiler spills 56 bytes, 64 where the CTAs select; no shape without a spill has
+// been measured); an fp16 block is 64, for 8 warps of two.  With more rows than SMs the fp16 rows get CTAs of four warps, two of
 // which share an SM: eight sequences of 32 heads with a 4K window took 85.6 us at 8 warps and
 // 81.4 at 4, one sequence of 8 heads over 64K tokens 48.4 at 8 and 55.2 at 4.
 struct SpanShape {
