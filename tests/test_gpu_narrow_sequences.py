@@ -49,3 +49,47 @@ def test_a_table_that_changes_between_chunks():
     ref = R.NarrowReference(1, hkv, P)
     ref.write(k, v)
     assert_cache(cache, ref)
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompt chunks, decode over split rows and narrow steps on two streams, each stream with its
+    own caches and workspaces: the same bits as one after the other."""
+    def state(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        mp = 130
+        pools = [torch.randn((2 * mp, 4, 16, 128), device="cuda", generator=g).half() for _ in range(2)]
+        bt = torch.randperm(2 * mp, device="cuda", generator=g).view(2, mp).int()
+        lens = torch.tensor([2050, 1234], dtype=torch.int32, device="cuda")
+        paged = q.PagedCache.allocate_meta(*pools, bt, lens, 8)
+        narrow = q.NarrowCache.allocate(2 * mp, 4, 16, bt, torch.zeros(2, dtype=torch.int32, device="cuda"), 8)
+        kv = torch.randn((2, 2, 700, 4, 128), device="cuda", generator=g).half()
+        return dict(paged=paged, narrow=narrow, wws=q.window_workspace(paged, 400), nws=q.narrow_workspace(narrow, 12),
+                    kv=kv, qn=torch.randn((2, 400, 8, 128), device="cuda", generator=g).half(),
+                    q1=torch.randn((8, 2, 8, 128), device="cuda", generator=g).half(),
+                    new=torch.randn((8, 2, 2, 4, 128), device="cuda", generator=g).half())
+
+    def work(s):
+        got = []
+        q.narrow_prefill(s["narrow"], s["kv"][0], s["kv"][1], s["nws"])
+        for i in range(8):
+            n = (400, 7, 33, 250)[i % 4]
+            got += q.window_prefill(s["paged"], s["qn"][:, :n].contiguous(), 4, 1500, s["wws"])
+            got += q.window_decode(s["paged"], s["q1"][i], 4, 1900, s["wws"])
+            got += q.narrow_decode_step(s["narrow"], s["q1"][i], s["new"][i, 0], s["new"][i, 1], 12, s["nws"])
+        return got
+
+    want = [work(state(seed)) for seed in (1, 2)]
+    torch.cuda.synchronize()
+    states = [state(seed) for seed in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in states]
+    torch.cuda.synchronize()
+    got = []
+    for s, stream in zip(states, streams):
+        with torch.cuda.stream(stream):
+            got.append(work(s))
+    torch.cuda.synchronize()
+    for s, a, b in zip(states, got, want):
+        ok(s["nws"])
+        ok(s["wws"])
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
