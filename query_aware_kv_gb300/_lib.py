@@ -161,7 +161,7 @@ def _check(rc: int) -> None:
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is None:  # torch.cuda.current_stream().cuda_stream, without the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     return stream.cuda_stream
 
 
@@ -193,11 +193,14 @@ def _one_device(**tensors: torch.Tensor) -> None:
             raise ValueError(f"{name} is on another device than {first}")
 
 
-def _current(dev: int) -> None:
-    """A launch goes to the current device (its default stream, unless the plan has another): not
-    with pointers of `dev` while another one is current."""
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError("the cache is on another device than the current one")
+# A launch goes to the current device (its default stream, unless a plan has another): not with
+# pointers of a cache while another device than the cache's is current.  (Plans ask only where there
+# are several devices: the question takes 0.1 us of every call.)
+_current_device = torch._C._cuda_getDevice
+
+
+def _not_current():
+    raise ValueError("the cache is on another device than the current one")
 
 
 def opts(pages_per_split: int = 0, score_tile_pages: int = 0, max_ctas: int = 0,
@@ -540,7 +543,7 @@ class DecodePlan:
         B, Hq, Hkv = cache.batch, cache.desc.num_q_heads, cache.num_kv_heads
         self._qshape = torch.Size((B, Hq, HEAD_DIM))
         self._kvshape = torch.Size((B, Hkv, HEAD_DIM))
-        self._dev = cache.k_pool.get_device()
+        self._dev, self._many = cache.k_pool.get_device(), torch.cuda.device_count() > 1
         self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
         if idx_out is not None:
             _need(idx_out, "idx_out", torch.int32, (B, Hkv, _sel_row(cache, top_k, o)))
@@ -563,7 +566,8 @@ class DecodePlan:
 
     def decode(self, q: torch.Tensor):
         """quest_decode of this step's queries; returns (out, lse)."""
-        _current(self._dev)
+        if self._many and _current_device() != self._dev:
+            _not_current()
         if not self._ok(q, self._qshape):
             _need(q, "q", torch.float16, self._qshape)
             raise ValueError("q is on another device than the cache")
@@ -574,7 +578,8 @@ class DecodePlan:
 
     def step(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor):
         """quest_decode_step: append (k_new, v_new), then decode q; returns (out, lse)."""
-        _current(self._dev)
+        if self._many and _current_device() != self._dev:
+            _not_current()
         if not (self._ok(q, self._qshape) and self._ok(k_new, self._kvshape) and
                 self._ok(v_new, self._kvshape)):
             _need(q, "q", torch.float16, self._qshape)
@@ -679,7 +684,8 @@ def _here(cache, ws: torch.Tensor, *others: torch.Tensor) -> None:
     tensors have to be on it."""
     _need(ws, "ws", torch.uint8)
     dev = cache.k_pool.get_device()
-    _current(dev)
+    if _current_device() != dev:
+        _not_current()
     for t in (ws, *others):
         if t is not None and t.get_device() != dev:
             raise ValueError("a tensor is on another device than the cache")
@@ -697,7 +703,8 @@ class NarrowPlan(DecodePlan):
 
     def dense(self, q: torch.Tensor):
         """quest_narrow_dense_decode of this step's queries; returns (out, lse)."""
-        _current(self._dev)
+        if self._many and _current_device() != self._dev:
+            _not_current()
         if not self._ok(q, self._qshape):
             _need(q, "q", torch.float16, self._qshape)
             raise ValueError("q is on another device than the cache")
@@ -728,7 +735,7 @@ class WindowPlan:
                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
                  stream=None):
         self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
-        self._dev = cache.k_pool.get_device()
+        self._dev, self._many = cache.k_pool.get_device(), torch.cuda.device_count() > 1
         self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
         _here(cache, ws, self.out, self.lse)
         self._keep = (cache, ws, o)  # alive as long as the plan
@@ -741,7 +748,8 @@ class WindowPlan:
 
     def decode(self, q: torch.Tensor):
         """The windowed attention of this step's queries; returns (out, lse)."""
-        _current(self._dev)
+        if self._many and _current_device() != self._dev:
+            _not_current()
         if not (type(q) is torch.Tensor and q.dtype is torch.float16 and
                 q.shape == self._qshape and q.get_device() == self._dev and q.is_contiguous()):
             _need(q, "q", torch.float16, self._qshape)

@@ -42,9 +42,9 @@ def test_every_tensor_of_a_cache_is_on_its_device(monkeypatch, make, shapes):
                                         (q.DecodePlan, ("decode", "step"))])
 def test_a_plan_is_not_launched_on_another_device(monkeypatch, plan, calls):
     """A plan made on device 0, called while device 1 is the current one."""
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(_lib, "_current_device", lambda: 1)
     p = object.__new__(plan)
-    p._dev = 0
+    p._dev, p._many = 0, True
     for name in calls:
         with pytest.raises(ValueError, match="current"):
             getattr(p, name)(*[None] * (3 if name == "step" else 1))
