@@ -516,6 +516,97 @@ int quest_window_prefill(const quest_cache_t* cache, const void* q, int32_t n_to
                          size_t ws_bytes, const quest_opts_t* opts, quest_stream_t stream);
 
 /*
+ * ---- Rotary positions ----------------------------------------------------------------
+ *
+ * The first rotary_dim dims of a head are pairs (x_a, x_b); pair i of the token at position t
+ * is turned by the angle t * f_i:
+ *   y_a = m (x_a cos(t f_i) - x_b sin(t f_i)),   y_b = m (x_b cos(t f_i) + x_a sin(t f_i))
+ * and the other dims pass through unchanged.  The pairs are (i, i + rotary_dim / 2), or
+ * (2i, 2i + 1) with `interleaved`.  Frequencies are held as 2^-64ths of a turn, so that an
+ * angle is exact to 2^-32 of a turn at every 32-bit position (a negative one too); cosines,
+ * sines and products are fp32, rounded once to the output's type.
+ */
+#define QUEST_FP16 0
+#define QUEST_BF16 1
+#define QUEST_FP32 2
+
+/* A rotation: filled by quest_rope_init, host memory, copied by every call. */
+typedef struct quest_rope {
+    int32_t rotary_dim;  /* 8, 16, ..., 128 */
+    int32_t interleaved; /* 0 or 1 */
+    float magnitude;     /* m */
+    int32_t reserved;
+    uint64_t turns[64];  /* f_i / (2 pi) mod 1, in 2^-64ths */
+} quest_rope_t;
+
+/* inv_freq: rotary_dim / 2 frequencies f_i in radians per position (finite, at most 1e6 in
+ * magnitude).  A host function: no stream, no device. */
+int quest_rope_init(quest_rope_t* rope, int32_t rotary_dim, int32_t interleaved,
+                    const double* inv_freq, double magnitude);
+
+/* Heads [n_tokens][num_heads][128] turned by positions[t] (int32 [n_tokens]).  x, out: dtype
+ * QUEST_FP16 / _BF16 / _FP32, a token's heads side by side, tokens x_stride / out_stride
+ * elements apart (multiples of 8).  transposed = 1 turns the other way, by the same factor m:
+ * the gradient with respect to x of a gradient x.  out may be x (the same stride); otherwise
+ * they do not overlap.  n_tokens = 0 does nothing. */
+int quest_rotate(const quest_rope_t* rope, const void* x, int64_t x_stride,
+                 const int32_t* positions, int32_t n_tokens, int32_t num_heads, int32_t dtype,
+                 int32_t transposed, void* out, int64_t out_stride, quest_stream_t stream);
+
+/* A chunk of n_tokens tokens per sequence on its way into a cache: q [batch][n_tokens]
+ * [num_q_heads][128], k and v [batch][n_tokens][num_kv_heads][128], QUEST_FP16 or QUEST_BF16.
+ * A token's heads are side by side; sequences and tokens are stride[0] and stride[1] elements
+ * apart (multiples of 8; stride[0] is not used with one sequence, stride[1] not with one
+ * token), so that q, k and v may be parts of one projection's rows. */
+typedef struct quest_rotary_io {
+    const void* q;       /* or NULL: no queries */
+    const void* k;
+    const void* v;
+    int64_t q_stride[2];
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int32_t dtype;
+    int32_t n_tokens;
+    void* q_out;         /* fp16 [batch][n_tokens][num_q_heads][128], dense; may be q itself where
+                            q is dense fp16; NULL where q is */
+    const int32_t* position_offsets; /* int32 [batch] or NULL */
+} quest_rotary_io_t;
+
+/* quest_prefill (n_tokens = 1: quest_append) of keys that are turned on the way: token i of
+ * sequence b goes to seq_lens[b] + i, its position is that plus position_offsets[b].  Keys,
+ * values and turned queries are rounded once to fp16 (of a bf16 number beyond fp16's range an
+ * infinity is left); the boxes are those of the keys as stored.  Of fp16 inputs the same cache
+ * and queries, bit for bit, as quest_rotate followed by quest_prefill.  A sequence with no room,
+ * or with a touched page outside [0, num_phys), is reported and its length left unchanged.  One
+ * launch with n_tokens = 1, otherwise two. */
+int quest_prefill_rotary(const quest_cache_t* cache, const quest_rope_t* rope,
+                         const quest_rotary_io_t* io, void* ws, size_t ws_bytes,
+                         quest_stream_t stream);
+
+/* The same into a narrow cache: quest_narrow_prefill (or quest_narrow_append) of the turned
+ * fp16 keys. */
+int quest_narrow_prefill_rotary(const quest_narrow_cache_t* cache, const quest_rope_t* rope,
+                                const quest_rotary_io_t* io, void* ws, size_t ws_bytes,
+                                quest_stream_t stream);
+
+/*
+ * ---- Prefixes that sequences share ---------------------------------------------------
+ *
+ * Attention of one query token per sequence over every token of its sequence, where groups of
+ * sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
+ * batch (the counts sum to `batch`), whose first prefix_tokens tokens are the same; of these
+ * the whole pages, prefix_tokens / page_size of them, are read once for the group, through the
+ * block-table row of the group's first sequence.  (The other sequences' entries for them may
+ * hold anything, where prefix_tokens is at most every length of the group.)  A sequence shorter
+ * than its prefix sees its own seq_len tokens.  prefix_tokens = 0: nothing is shared.
+ */
+typedef struct quest_prefix_group {
+    int32_t count;         /* >= 1 */
+    int32_t prefix_tokens; /* >= 0, at most max_pages * page_size */
+} quest_prefix_group_t;
+#define QUEST_MAX_PREFIX_GROUPS 128
+
+/*
  * Synchronise `stream`, return the device status recorded in the workspace (QUEST_OK
  * or a QUEST_ERR_* code) and clear it.  detail (nullable, 3 ints) receives the first
  * fault's sequence, logical page and a kernel-specific code.

@@ -17,4 +17,7 @@ from ._lib import (  # noqa: F401
     NarrowCache, NarrowPlan, QuestNarrowCacheDesc, WindowPlan, narrow_append, narrow_decode,
     narrow_decode_step, narrow_dense_decode, narrow_prefill, narrow_sparse_decode,
     narrow_window_decode, narrow_workspace, window_decode, window_prefill, window_workspace,
+    QuestRope, QuestRotaryIo, RotaryPlan, append_rotary, narrow_append_rotary,
+    narrow_prefill_rotary, prefill_rotary, rotate,
 )
+from .rope import Rope, rope_frequencies  # noqa: F401

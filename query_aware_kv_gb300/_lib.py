@@ -47,6 +47,7 @@ EXPORTS = (
     "quest_narrow_sparse_decode", "quest_narrow_dense_decode", "quest_narrow_decode",
     "quest_narrow_decode_step", "quest_narrow_window_decode",
     "quest_window_workspace_size", "quest_window_decode", "quest_window_prefill",
+    "quest_rope_init", "quest_rotate", "quest_prefill_rotary", "quest_narrow_prefill_rotary",
 )
 
 
@@ -76,6 +77,20 @@ class QuestNarrowCacheDesc(ctypes.Structure):
 class QuestLayer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("k_pool", "v_pool", "meta", "q", "k_new", "v_new", "out", "lse")]
+
+
+class QuestRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+class QuestRotaryIo(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("dtype", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("q_out", ctypes.c_void_p),
+                ("position_offsets", ctypes.c_void_p)]
 
 
 class QuestOpts(ctypes.Structure):
@@ -111,6 +126,9 @@ def load() -> ctypes.CDLL:
         C = ctypes.POINTER(QuestCacheDesc)
         O = ctypes.POINTER(QuestOpts)
         N = ctypes.POINTER(QuestNarrowCacheDesc)
+        R = ctypes.POINTER(QuestRope)
+        IO = ctypes.POINTER(QuestRotaryIo)
+        I64 = ctypes.c_int64
         sig = {
             "quest_workspace_size": (SZ, [C, I32, O]),
             "quest_workspace_init": (ctypes.c_int, [V, SZ, V]),
@@ -144,6 +162,11 @@ def load() -> ctypes.CDLL:
             "quest_window_workspace_size": (SZ, [C, I32, O]),
             "quest_window_decode": (ctypes.c_int, [C, V, I32, I32, V, V, V, SZ, O, V]),
             "quest_window_prefill": (ctypes.c_int, [C, V, I32, I32, I32, V, V, V, SZ, O, V]),
+            "quest_rope_init": (ctypes.c_int, [R, I32, I32, ctypes.POINTER(ctypes.c_double),
+                                               ctypes.c_double]),
+            "quest_rotate": (ctypes.c_int, [R, V, I64, V, I32, I32, I32, I32, V, I64, V]),
+            "quest_prefill_rotary": (ctypes.c_int, [C, R, IO, V, SZ, V]),
+            "quest_narrow_prefill_rotary": (ctypes.c_int, [N, R, IO, V, SZ, V]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -790,6 +813,202 @@ def window_prefill(cache: PagedCache, q: torch.Tensor, sink_tokens: int, window:
         ctypes.byref(cache.desc), q.data_ptr(), int(shape[1]), int(sink_tokens), int(window),
         out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream)))
     return out, lse
+
+
+# ---- rotary positions (the rotation itself is a ``Rope``, in rope.py)
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _heads(t: torch.Tensor, name: str, shape) -> None:
+    """Heads of 128 dims, a token's side by side; tokens may be any multiple of 8 elements apart
+    (a part of a projection's rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if shape is not None and t.shape != torch.Size(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != HEAD_DIM):
+        raise ValueError(f"{name}: the heads of a token must be side by side")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """The distance of the tokens of t [..., heads, 128], whose leading dims are one axis."""
+    step = reach = None
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step, reach = stride, stride * size
+        elif stride != reach:
+            raise ValueError(f"{name}: its tokens must be evenly spaced")
+        else:
+            reach *= size
+    return step or 0
+
+
+def rotate(rope, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None,
+           transposed: bool = False, stream=None) -> torch.Tensor:
+    """Heads x [..., heads, 128] (fp16, bf16 or fp32) turned by their tokens' positions (int32, of
+    x's leading dims).  ``transposed``: turned the other way, by the same magnitude: with a gradient
+    of the output as x, the gradient of the input.  ``out`` may be x."""
+    if x.dim() < 3 or x.shape[-1] != HEAD_DIM:
+        raise ValueError("x must be [..., heads, 128]")
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be float16, bfloat16 or float32")
+    _heads(x, "x", None)
+    _need(positions, "positions", torch.int32, x.shape[:-2])
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype:
+        raise TypeError("out must have x's type")
+    _heads(out, "out", x.shape)
+    dev = x.get_device()
+    if positions.get_device() != dev or out.get_device() != dev:
+        raise ValueError("x, positions and out must be on one device")
+    if _current_device() != dev:
+        raise ValueError("x is on another device than the current one")
+    if x.numel() == 0:
+        return out
+    _check(load().quest_rotate(rope.ref, x.data_ptr(), _token_stride(x, "x"), positions.data_ptr(),
+                               positions.numel(), x.shape[-2], _DTYPES[x.dtype], int(transposed),
+                               out.data_ptr(), _token_stride(out, "out"), _stream(stream)))
+    return out
+
+
+def _rotary_fn(cache):
+    lib = load()
+    return lib.quest_narrow_prefill_rotary if isinstance(cache, NarrowCache) else lib.quest_prefill_rotary
+
+
+def _rotary_write(cache, rope, q, k, v, ws, q_out, offsets, stream):
+    """k, v [B][n][Hkv][128], q [B][n][Hq][128] or None."""
+    B, n, Hq, Hkv = cache.batch, k.shape[1], cache.desc.num_q_heads, cache.num_kv_heads
+    if k.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("q, k and v must be float16 or bfloat16")
+    io = QuestRotaryIo(dtype=_DTYPES[k.dtype], n_tokens=n)
+    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        if t is None and name == "q":
+            continue
+        _heads(t, name, (B, n, H, HEAD_DIM))
+        if t.dtype != k.dtype:
+            raise TypeError("q, k and v must be of one type")
+        setattr(io, name, t.data_ptr())
+        s = getattr(io, name + "_stride")
+        s[0], s[1] = t.stride(0) if B > 1 else 0, t.stride(1) if n > 1 else 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if q_out is None:
+            q_out = torch.empty((B, n, Hq, HEAD_DIM), dtype=torch.float16, device=q.device)
+        _need(q_out, "q_out", torch.float16, (B, n, Hq, HEAD_DIM))
+        io.q_out = q_out.data_ptr()
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, (B,))
+        io.position_offsets = offsets.data_ptr()
+    _here(cache, ws, q, k, v, q_out, offsets)
+    _check(_rotary_fn(cache)(ctypes.byref(cache.desc), rope.ref, ctypes.byref(io), ws.data_ptr(),
+                             ws.numel(), _stream(stream)))
+    return q_out
+
+
+def prefill_rotary(cache: PagedCache, rope, q: Optional[torch.Tensor], k: torch.Tensor,
+                   v: torch.Tensor, ws: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                   offsets: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """``prefill`` of a chunk as the projection leaves it: keys are turned by their positions
+    (seq_lens[b] + i, plus offsets[b]) on the way into the pages, the turned queries are returned
+    (fp16 [B][n][Hq][128]).  q [B][n][Hq][128] (or None), k, v [B][n][Hkv][128]: fp16 or bf16, their
+    tokens any multiple of 8 elements apart."""
+    if k.dim() != 4:
+        raise ValueError("k must be [batch][n_tokens][num_kv_heads][128]")
+    return _rotary_write(cache, rope, q, k, v, ws, q_out, offsets, stream)
+
+
+def narrow_prefill_rotary(cache: NarrowCache, rope, q: Optional[torch.Tensor], k: torch.Tensor,
+                          v: torch.Tensor, ws: torch.Tensor,
+                          q_out: Optional[torch.Tensor] = None,
+                          offsets: Optional[torch.Tensor] = None,
+                          stream=None) -> Optional[torch.Tensor]:
+    """``prefill_rotary`` into a narrow cache (``narrow_prefill`` of the turned keys)."""
+    return prefill_rotary(cache, rope, q, k, v, ws, q_out, offsets, stream)
+
+
+def append_rotary(cache: PagedCache, rope, q: Optional[torch.Tensor], k_new: torch.Tensor,
+                  v_new: torch.Tensor, ws: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                  offsets: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """``append`` of one token per sequence, its key turned by its position; the turned queries are
+    returned.  q [B][Hq][128] (or None), k_new, v_new [B][Hkv][128], as for ``prefill_rotary``."""
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [batch][num_kv_heads][128]")
+    if q_out is not None:
+        q_out = q_out.unsqueeze(1)
+    r = _rotary_write(cache, rope, None if q is None else q.unsqueeze(1), k_new.unsqueeze(1),
+                      v_new.unsqueeze(1), ws, q_out, offsets, stream)
+    return None if r is None else r.squeeze(1)
+
+
+def narrow_append_rotary(cache: NarrowCache, rope, q: Optional[torch.Tensor], k_new: torch.Tensor,
+                         v_new: torch.Tensor, ws: torch.Tensor,
+                         q_out: Optional[torch.Tensor] = None,
+                         offsets: Optional[torch.Tensor] = None,
+                         stream=None) -> Optional[torch.Tensor]:
+    """``append_rotary`` into a narrow cache."""
+    return append_rotary(cache, rope, q, k_new, v_new, ws, q_out, offsets, stream)
+
+
+class RotaryPlan:
+    """``append_rotary`` (of a ``PagedCache`` or a ``NarrowCache``) bound to its cache, rotation,
+    workspace, output, offsets and stream, for a decode loop: each call only checks q, k_new and
+    v_new.  The turned queries (``q_out``) are overwritten by every call and returned by it.  A
+    plan is used by one thread at a time."""
+
+    def __init__(self, cache, rope, ws: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                 offsets: Optional[torch.Tensor] = None, stream=None):
+        B, Hq, Hkv = cache.batch, cache.desc.num_q_heads, cache.num_kv_heads
+        self._qshape, self._kvshape = torch.Size((B, Hq, HEAD_DIM)), torch.Size((B, Hkv, HEAD_DIM))
+        self._dev, self._many = cache.k_pool.get_device(), torch.cuda.device_count() > 1
+        if q_out is None:
+            q_out = torch.empty(self._qshape, dtype=torch.float16, device=cache.k_pool.device)
+        _need(q_out, "q_out", torch.float16, self._qshape)
+        if offsets is not None:
+            _need(offsets, "offsets", torch.int32, (B,))
+        _here(cache, ws, q_out, offsets)
+        self.q_out = q_out
+        self._keep = (cache, rope, ws, offsets)  # alive as long as the plan
+        self._fn = _rotary_fn(cache)
+        self._io = QuestRotaryIo(n_tokens=1, q_out=q_out.data_ptr(),
+                                 position_offsets=_ptr(offsets))
+        self._args = (ctypes.byref(cache.desc), rope.ref, ctypes.byref(self._io), ws.data_ptr(),
+                      ws.numel(), _stream(stream))
+
+    def append(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor) -> torch.Tensor:
+        """Write (k_new, v_new) with the key turned; returns the turned queries."""
+        if self._many and _current_device() != self._dev:
+            _not_current()
+        io, dtype = self._io, q.dtype
+        for name, t, shape in (("q", q, self._qshape), ("k", k_new, self._kvshape),
+                               ("v", v_new, self._kvshape)):
+            s = t.stride()
+            if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and
+                    t.get_device() == self._dev and s[2] == 1 and (s[1] == HEAD_DIM or shape[1] == 1)):
+                _heads(t, name, shape)
+                if t.dtype != dtype:
+                    raise TypeError("q, k_new and v_new must be of one type")
+                if t.get_device() != self._dev:
+                    raise ValueError("q / k_new / v_new are on another device than the cache")
+            setattr(io, name, t.data_ptr())
+            getattr(io, name + "_stride")[0] = s[0] if shape[0] > 1 else 0
+        if dtype is torch.float16:
+            io.dtype = 0
+        elif dtype is torch.bfloat16:
+            io.dtype = 1
+        else:
+            raise TypeError("q, k_new and v_new must be float16 or bfloat16")
+        rc = self._fn(*self._args)
+        if rc:
+            _check(rc)
+        return self.q_out
 
 
 def decode_layers(cache: PagedCache, layers: Sequence[PagedCache], q: Sequence[torch.Tensor],

@@ -241,6 +241,25 @@ cudaError_t launch_narrow_prefill(const Params& p, const NarrowPtrs& nar, const 
 cudaError_t launch_narrow_estimate(const Params& p, const NarrowPtrs& nar, int G, cudaStream_t s);
 cudaError_t launch_narrow_append(const Params& p, const NarrowPtrs& nar, const __half* k_new,
                                  const __half* v_new, cudaStream_t s);
+// ---- rotary positions (quest_rotary_kernels.cu)
+struct RotateCall {
+  const quest_rope_t* rope;
+  const void* x;
+  void* out;
+  const int* positions;
+  long long x_stride, out_stride;
+  int tokens, heads, dtype, transposed;
+};
+cudaError_t launch_rotate(const RotateCall& r, cudaStream_t s);
+// A chunk into an fp16 cache (nar null) or a narrow one.
+cudaError_t launch_rotary_write(const Params& p, const NarrowPtrs* nar, const quest_rope_t& rope,
+                                const quest_rotary_io_t& io, cudaStream_t s);
+
+int check_narrow_desc(const quest_narrow_cache_t* cache);
+// The cache's part of a narrow write's parameters, after its checks (quest_span_api.cu).
+int narrow_write_params(const quest_narrow_cache_t* cache, void* ws, size_t ws_bytes, Params* p,
+                        NarrowPtrs* nar);
+
 // Host checks shared with quest_api.cu (status code, error text set).
 int check_cache_desc(const quest_cache_t* cache);
 int check_top_k(int top_k);

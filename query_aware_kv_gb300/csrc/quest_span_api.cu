@@ -209,6 +209,22 @@ int narrow_decode(const quest_narrow_cache_t* cache, const void* q, const void* 
 
 }  // namespace
 
+namespace quest {
+
+int narrow_write_params(const quest_narrow_cache_t* cache, void* ws, size_t ws_bytes, Params* p,
+                        NarrowPtrs* nar) {
+  const quest_cache_t c = shared_part(*cache);
+  const SpanLayout L = span_layout(c, 1, nullptr);
+  const int rc = check_workspace(ws, ws_bytes, L.arrive);
+  if (rc) return rc;
+  *p = make_params(c, ws, L, nullptr);
+  *nar = narrow_ptrs(*cache);
+  return QUEST_OK;
+}
+int check_narrow_desc(const quest_narrow_cache_t* cache) { return check_narrow(cache); }
+
+}  // namespace quest
+
 extern "C" {
 
 size_t quest_narrow_workspace_size(const quest_narrow_cache_t* cache, int32_t top_k,
