@@ -596,15 +596,31 @@ int quest_narrow_prefill_rotary(const quest_narrow_cache_t* cache, const quest_r
  * sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
  * batch (the counts sum to `batch`), whose first prefix_tokens tokens are the same; of these
  * the whole pages, prefix_tokens / page_size of them, are read once for the group, through the
- * block-table row of the group's first sequence.  (The other sequences' entries for them may
- * hold anything, where prefix_tokens is at most every length of the group.)  A sequence shorter
- * than its prefix sees its own seq_len tokens.  prefix_tokens = 0: nothing is shared.
+ * block-table row of the group's first sequence.  (The other sequences' rows hold the same
+ * entries: which row is read is the call's choice.)  A sequence shorter than its prefix sees its
+ * own seq_len tokens.  prefix_tokens = 0: nothing is shared.
  */
 typedef struct quest_prefix_group {
     int32_t count;         /* >= 1 */
     int32_t prefix_tokens; /* >= 0, at most max_pages * page_size */
 } quest_prefix_group_t;
 #define QUEST_MAX_PREFIX_GROUPS 128
+
+/* Bytes of workspace of quest_prefix_decode with these groups and opts; 0 if the arguments are
+ * invalid.  One workspace serves calls with the same groups, and no calls but
+ * quest_prefix_decode. */
+size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefix_group_t* groups,
+                                   int32_t n_groups, const quest_opts_t* opts);
+
+/* q fp16 [batch][num_q_heads][128]; groups: HOST array, copied by the call; out, lse as in
+ * quest_dense_decode.  A row whose sequence is empty gives out = 0, lse = -inf; NaN and
+ * infinities as in windowed attention.  Where sharing would not pay every sequence reads all of
+ * its tokens itself.
+ * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns, debug_flags. */
+int quest_prefix_decode(const quest_cache_t* cache, const void* q,
+                        const quest_prefix_group_t* groups, int32_t n_groups, void* out,
+                        float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,
+                        quest_stream_t stream);
 
 /*
  * Synchronise `stream`, return the device status recorded in the workspace (QUEST_OK

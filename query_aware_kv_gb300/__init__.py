@@ -19,5 +19,6 @@ from ._lib import (  # noqa: F401
     narrow_window_decode, narrow_workspace, window_decode, window_prefill, window_workspace,
     QuestRope, QuestRotaryIo, RotaryPlan, append_rotary, narrow_append_rotary,
     narrow_prefill_rotary, prefill_rotary, rotate,
+    QUEST_MAX_PREFIX_GROUPS, PrefixPlan, QuestPrefixGroup, prefix_decode, prefix_workspace,
 )
 from .rope import Rope, rope_frequencies  # noqa: F401

@@ -30,6 +30,7 @@ QUEST_ERR_BAD_PAGE = 6
 QUEST_ERR_BAD_LENGTH = 7
 QUEST_ERR_BAD_SELECTION = 8
 QUEST_MAX_PAGES = 16384
+QUEST_MAX_PREFIX_GROUPS = 128
 QUEST_DEBUG_WITHHOLD_SELECTION = 1
 QUEST_DEBUG_WITHHOLD_VALUES = 2
 QUEST_PATH_AUTO, QUEST_PATH_FUSED, QUEST_PATH_CHAIN, QUEST_PATH_STREAM = 0, 1, 2, 3
@@ -48,6 +49,7 @@ EXPORTS = (
     "quest_narrow_decode_step", "quest_narrow_window_decode",
     "quest_window_workspace_size", "quest_window_decode", "quest_window_prefill",
     "quest_rope_init", "quest_rotate", "quest_prefill_rotary", "quest_narrow_prefill_rotary",
+    "quest_prefix_workspace_size", "quest_prefix_decode",
 )
 
 
@@ -77,6 +79,10 @@ class QuestNarrowCacheDesc(ctypes.Structure):
 class QuestLayer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("k_pool", "v_pool", "meta", "q", "k_new", "v_new", "out", "lse")]
+
+
+class QuestPrefixGroup(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("prefix_tokens", ctypes.c_int32)]
 
 
 class QuestRope(ctypes.Structure):
@@ -128,6 +134,7 @@ def load() -> ctypes.CDLL:
         N = ctypes.POINTER(QuestNarrowCacheDesc)
         R = ctypes.POINTER(QuestRope)
         IO = ctypes.POINTER(QuestRotaryIo)
+        G = ctypes.POINTER(QuestPrefixGroup)
         I64 = ctypes.c_int64
         sig = {
             "quest_workspace_size": (SZ, [C, I32, O]),
@@ -162,6 +169,8 @@ def load() -> ctypes.CDLL:
             "quest_window_workspace_size": (SZ, [C, I32, O]),
             "quest_window_decode": (ctypes.c_int, [C, V, I32, I32, V, V, V, SZ, O, V]),
             "quest_window_prefill": (ctypes.c_int, [C, V, I32, I32, I32, V, V, V, SZ, O, V]),
+            "quest_prefix_workspace_size": (SZ, [C, G, I32, O]),
+            "quest_prefix_decode": (ctypes.c_int, [C, V, G, I32, V, V, V, SZ, O, V]),
             "quest_rope_init": (ctypes.c_int, [R, I32, I32, ctypes.POINTER(ctypes.c_double),
                                                ctypes.c_double]),
             "quest_rotate": (ctypes.c_int, [R, V, I64, V, I32, I32, I32, I32, V, I64, V]),
@@ -1009,6 +1018,68 @@ class RotaryPlan:
         if rc:
             _check(rc)
         return self.q_out
+
+
+# ---- prefixes that sequences share
+def _groups(groups: Sequence[Tuple[int, int]]):
+    rows = [(int(count), int(tokens)) for count, tokens in groups]
+    return (QuestPrefixGroup * max(1, len(rows)))(*rows), len(rows)
+
+
+def prefix_workspace(cache: PagedCache, groups: Sequence[Tuple[int, int]],
+                     o: Optional[QuestOpts] = None) -> torch.Tensor:
+    """A zeroed workspace for prefix_decode with these groups and opts."""
+    lib = load()
+    arr, n_groups = _groups(groups)
+    n = lib.quest_prefix_workspace_size(ctypes.byref(cache.desc), arr, n_groups, _opts_ref(o))
+    if n == 0:
+        raise QuestError(QUEST_ERR_INVALID_ARG, lib.quest_last_error().decode())
+    return torch.zeros(int(n), dtype=torch.uint8, device=cache.k_pool.device)
+
+
+class PrefixPlan:
+    """prefix_decode bound to its cache, groups, workspace, stream and outputs, for a decode loop
+    (the sequences may grow; a batch of other groups needs another plan): each call only checks q.
+    The outputs are overwritten by every call and returned by it."""
+
+    def __init__(self, cache: PagedCache, groups: Sequence[Tuple[int, int]], ws: torch.Tensor,
+                 o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
+                 stream=None):
+        if not isinstance(cache, PagedCache):
+            raise TypeError("cache must be a PagedCache")
+        self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
+        self._dev, self._many = cache.k_pool.get_device(), torch.cuda.device_count() > 1
+        self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
+        _here(cache, ws, self.out, self.lse)
+        arr, n_groups = _groups(groups)
+        self._keep = (cache, ws, o, arr)  # alive as long as the plan
+        self._fn = load().quest_prefix_decode
+        self._desc = ctypes.byref(cache.desc)
+        self._tail = (arr, n_groups, self.out.data_ptr(), _ptr(self.lse), ws.data_ptr(),
+                      ws.numel(), _opts_ref(o), _stream(stream))
+
+    def decode(self, q: torch.Tensor):
+        """The attention of this step's queries over their sequences; returns (out, lse)."""
+        if self._many and _current_device() != self._dev:
+            _not_current()
+        if not (type(q) is torch.Tensor and q.dtype is torch.float16 and
+                q.shape == self._qshape and q.get_device() == self._dev and q.is_contiguous()):
+            _need(q, "q", torch.float16, self._qshape)
+            raise ValueError("q is on another device than the cache")
+        rc = self._fn(self._desc, q.data_ptr(), *self._tail)
+        if rc:
+            _check(rc)
+        return self.out, self.lse
+
+
+def prefix_decode(cache: PagedCache, q: torch.Tensor, groups: Sequence[Tuple[int, int]],
+                  ws: torch.Tensor, o: Optional[QuestOpts] = None, out=None, lse=None,
+                  want_lse: bool = True, stream=None):
+    """Attention of the last token of every sequence over its whole cache, where groups of
+    sequences begin with the same tokens: ``groups`` holds (sequences, tokens of their common
+    prefix) of the batch's sequences in order.  A prefix's whole pages are read once for its
+    group."""
+    return PrefixPlan(cache, groups, ws, o, out, lse, want_lse, stream).decode(q)
 
 
 def decode_layers(cache: PagedCache, layers: Sequence[PagedCache], q: Sequence[torch.Tensor],

@@ -227,11 +227,56 @@ size_t span_max_parts(int batch, int hkv, bool user);
 bool span_selects(const SpanParams& sp, int pages);
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s);
 
+// ---- prefixes that sequences share (quest_prefix.cu: the cut; the launches below)
+// The groups of a batch, in order; passed by value.  A group without pages shares nothing.
+struct PrefixTable {
+  struct Group {
+    int first, count;  // sequences
+    int pages;         // of the prefix that is read once
+    int splits;        // of its K / V tiles
+    int cta0;          // the group's first CTA of the launch over prefixes
+    int part0;         // its first row of part_ml / part_acc
+  };
+  int n, ctas;    // groups; CTAs of the launch over prefixes (0: nothing is shared)
+  int parts;      // rows of part_ml / part_acc of the prefixes' shares
+  int most_pages; // of a sequence behind its prefix
+  Group group[QUEST_MAX_PREFIX_GROUPS];
+
+  // The last group with value(group) <= x.
+  template <class F>
+  __host__ __device__ int last(int x, F value) const {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (value(group[mid]) <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+  // (a group without CTAs starts where the next one does)
+  __host__ __device__ int group_of_cta(int c) const {
+    return last(c, [](const Group& g) { return g.cta0; });
+  }
+  __host__ __device__ int group_of_seq(int b) const {
+    return last(b, [](const Group& g) { return g.first; });
+  }
+};
+
+// Attention over prefixes: the prefixes' shares (prefix_kernel, quest_prompt_kernel.cu), the tails'
+// (tail_kernel, quest_span_kernel.cu), and both into out and lse (prefix_join_kernel).
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s);
+// Splits of a tail; part_ml / part_acc rows of the tails start at t.parts.
+int tail_splits(const Params& p, const PrefixTable& t, int user_pps);
+cudaError_t launch_tail(const Params& p, const PrefixTable& t, int splits, cudaStream_t s);
+cudaError_t launch_prefix_join(const Params& p, const PrefixTable& t, int splits, cudaStream_t s);
+
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
 // p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of
 // part_ml / part_acc each; splits only while items * splits is at most kPromptParts.  Two
 // launches where rows are split (the second joins their shares), one otherwise.
 constexpr int kPromptParts = 304;
+constexpr int kPromptRows = 256;   // query rows of a work item
+constexpr int kPromptTokens = 128; // tokens of its K / V tiles
 int prompt_part_rows(int G, int n_tokens);
 int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps);
 cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s);

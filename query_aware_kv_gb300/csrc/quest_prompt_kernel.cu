@@ -56,6 +56,7 @@ namespace {
 constexpr int kPromptThreads = 384;
 constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
+static_assert(kPromptRows == 2 * kTileRows && kPromptTokens == kTileTokens, "the cut's sizes");
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
 constexpr int kKvStages = 5;         // K and V tiles in flight, alternating
 constexpr int kScores = 3;           // barriers of a query tile's scores, in turn
@@ -283,6 +284,32 @@ __device__ __forceinline__ size_t part_slot(const PromptParams& pp, int s) {
   return (item * pp.p.n_splits + s) * pp.part_rows;
 }
 
+// A CTA's work: row block `blk` of kv head g, its split's K / V tiles.
+struct Item {
+  int blk, split, n_splits, g, b, n;
+  int pages;      // of a shared prefix
+  size_t share0;  // of a group: where the item's shares start
+};
+
+// CTA c of a launch over prefixes: of its group's CTAs the row blocks vary fastest (the CTAs that
+// read the same tiles run side by side), then the splits, then the kv heads.
+__device__ __forceinline__ Item shared_item(const PrefixTable& t, int hkv, int lg) {
+  const int c = (int)blockIdx.x, i = t.group_of_cta(c);
+  const PrefixTable::Group& q = t.group[i];
+  const int rows = q.count << lg;
+  const int blocks = (rows + 2 * kTileRows - 1) / (2 * kTileRows), at = c - q.cta0;
+  Item it;
+  it.blk = at % blocks;
+  it.split = at / blocks % q.splits;
+  it.n_splits = q.splits;
+  it.g = at / blocks / q.splits;
+  it.b = q.first;
+  it.n = q.count;
+  it.pages = q.pages;
+  it.share0 = (size_t)q.part0 + (size_t)at * min(rows, 2 * kTileRows);
+  return it;
+}
+
 // The lowest x bits (0 <= x <= 32).
 __device__ __forceinline__ uint32_t low_bits(int x) { return (uint32_t)((1ull << x) - 1ull); }
 // A weight row's threads: 128 scores to weights.
@@ -336,11 +363,13 @@ __device__ __forceinline__ bool not_finite(const uint32_t* o) {
   return x;
 }
 
-template <int P>
-__global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
-                  const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v) {
+// The attention of one work item.  kShared: its rows are the query tokens of a group's sequences
+// (one each, so that token i of the group is sequence first + i), its tokens the prefix that they
+// share, without a causal mask; what a row sees ends with the prefix or with its own sequence.
+template <int P, bool kShared>
+__device__ __forceinline__ void prompt_body(const PromptParams& pp, const PrefixTable* table,
+                                            const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                            const CUtensorMap& map_v) {
   extern __shared__ unsigned char smem_raw[];
   constexpr int PPT = kTileTokens / P;  // pages of a K / V tile
   const Params& p = pp.p;
@@ -350,8 +379,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = pp.log_g, G = 1 << lg, TT = kTileRows >> lg;  // tokens of a query tile
 
-  const int blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
-  const int n = pp.n_tokens, tok0 = blk * 2 * TT;
+  Item it;
+  if constexpr (kShared) {
+    it = shared_item(*table, p.Hkv, lg);
+  } else {
+    it.blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
+    it.split = (int)blockIdx.x % p.n_splits;
+    it.n_splits = p.n_splits;
+    it.g = (int)blockIdx.y;
+    it.b = (int)blockIdx.z;
+    it.n = pp.n_tokens;
+  }
+  const int n = kShared ? it.n : pp.n_tokens, tok0 = it.blk * 2 * TT;
   const int tok1 = min(n, tok0 + 2 * TT);
   const bool two = tok1 - tok0 > TT;
   const int n_q = two ? 2 : 1;  // query tiles with rows
@@ -379,24 +418,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   // ---- the CTA's work (its length and first pages are looked up while the barriers and TMEM
   // are set up)
-  const int split = (int)blockIdx.x % p.n_splits;
-  const int g = (int)blockIdx.y, b = (int)blockIdx.z;
-  int L = p.seq_lens[b];
-  if (L < 0 || (long long)L > (long long)p.max_pages * P) {
-    if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
-    L = 0;
-  }
-  const int pos0 = L - n;  // position of query token 0 (may be negative)
-  const int end = pos0 + tok1;
+  const int g = it.g, b = it.b;  // (of a group, b is its first sequence)
   PageList list{0, 0, 0, 0};
-  if (end > 0) {
-    list.lo = max(0, max(0, pos0 + tok0) - pp.window + 1);
-    list.first = list.lo / P;
-    list.n_sink = min((min(pp.sink, list.lo) + P - 1) / P, list.first);
-    list.count = list.n_sink + (end + P - 1) / P - list.first;
+  int pos0 = 0, end;  // position of query token 0 (may be negative); the end of what rows see
+  auto length = [&](int seq) {
+    const int L = p.seq_lens[seq];
+    if (L >= 0 && (long long)L <= (long long)p.max_pages * P) return L;
+    record(p, QUEST_ERR_BAD_LENGTH, seq, -1);
+    return 0;
+  };
+  if constexpr (kShared) {
+    int most = 0;
+    for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(b + i));
+    end = min(__reduce_max_sync(0xffffffffu, most), it.pages * P);
+    list.count = (end + P - 1) / P;
+  } else {
+    int L = p.seq_lens[b];
+    if (L < 0 || (long long)L > (long long)p.max_pages * P) {
+      if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
+      L = 0;
+    }
+    pos0 = L - n;
+    end = pos0 + tok1;
+    if (end > 0) {
+      list.lo = max(0, max(0, pos0 + tok0) - pp.window + 1);
+      list.first = list.lo / P;
+      list.n_sink = min((min(pp.sink, list.lo) + P - 1) / P, list.first);
+      list.count = list.n_sink + (end + P - 1) / P - list.first;
+    }
   }
   const int tiles = (list.count + PPT - 1) / PPT;
-  const int j0 = tiles * split / p.n_splits, j1 = tiles * (split + 1) / p.n_splits;
+  const int j0 = tiles * it.split / it.n_splits, j1 = tiles * (it.split + 1) / it.n_splits;
+  // the first of the item's rows of q, out and lse, in tokens
+  // (taken where it is used: a value kept over the loops makes the compiler spill)
+  auto q_tok0 = [&]() { return kShared ? (size_t)b + tok0 : (size_t)b * n + tok0; };
+  // where the item's row r keeps its share
+  auto share0 = [&]() {
+    return kShared ? shared_item(*table, p.Hkv, lg).share0
+                   : part_slot(pp, (int)blockIdx.x % p.n_splits);
+  };
 
   // Pages of the list, for the fetch warps: 32 at a time, a page per lane, the next 32 on their
   // way; entries behind the list's end repeat its last page (their tokens are hidden).
@@ -417,7 +477,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
     for (int i = 0; i < 2 * n_q; ++i)
       tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
-             64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
+             64 * (i & 1), g * G, (int)q_tok0() + (i >> 1) * TT, &bars.q_full);
   }
   __syncwarp();
 
@@ -569,14 +629,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // ---- softmax: a thread a row
     const int t = warp >> 2, row = threadIdx.x & 127;
     const int tok = tok0 + t * TT + (row >> lg);
-    const int pr = pos0 + tok;  // the row's position
+    int pr = pos0 + tok;  // the row's position
+    int least = 0;  // of a group: of the warp's rows (they go together)
+    if constexpr (kShared) {
+      pr = tok < tok1 ? length(b + tok) - 1 : end - 1;
+      least = __reduce_min_sync(0xffffffffu, pr);
+    }
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + 256 + t * 128;
     float m = -CUDART_INF_F, l = 0.f;
     bool ok = true;
     if (t < n_q) {
-      const int r0 = pos0 + tok0 + t * TT;
-      const int r1 = min(r0 + TT, end) - 1;
+      const int r0 = kShared ? least : pos0 + tok0 + t * TT;
+      const int r1 = kShared ? end - 1 : min(r0 + TT, end) - 1;
       for (int j = j0; j < j1; ++j) {
         const uint32_t turn = (uint32_t)(j - j0) / kScores;  // (counters would spill here)
         ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(uint32_t)(j - j0) - turn * kScores],
@@ -700,10 +765,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
       const bool mine = tok < tok1;
       bool odd = false;  // some of the row's O is not finite
-      if (ok && p.n_splits == 1) {
+      if (!kShared && ok && p.n_splits == 1) {
         // ---- out = O / l, through the tile's own query space (its products are done): a row
         // of 256 B per thread goes to shared memory, two rows at a time leave as whole lines
-        const size_t row0 = ((size_t)b * n + tok0 + t * TT) * p.Hq + ((size_t)g << lg);
+        const size_t row0 = (q_tok0() + t * TT) * p.Hq + ((size_t)g << lg);
         unsigned char* stage = smem + PromptSmem::q + t * kTileBytes;
         const float inv = none ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -741,7 +806,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       } else if (ok) {
         // ---- a split's share: O, m and l as they are (the loads are the whole warp's)
-        const size_t slot = part_slot(pp, split) + t * kTileRows + row;
+        const size_t slot = share0() + t * kTileRows + row;
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           uint32_t o[32];
@@ -805,8 +870,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const float2 ml = *stash(r / kTileRows, r % kTileRows);
       const float m_r = ml.x, l_r = ml.y;
       if (l_r < 0.f) continue;  // warp-uniform
-      const int pos_r = pos0 + tok0 + (r >> lg);
-      const size_t at = (((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) +
+      const int pos_r = kShared ? length(b + tok0 + (r >> lg)) - 1 : pos0 + tok0 + (r >> lg);
+      const size_t at = ((q_tok0() + (r >> lg)) * p.Hq + ((size_t)g << lg) +
                          (r & (G - 1))) * kHeadDim + 4 * lane;
       const uint2 qw = *reinterpret_cast<const uint2*>(p.q + at);
       const float2 qa = h2f(qw.x), qb = h2f(qw.y);
@@ -821,7 +886,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 4
         for (int k = 0; k < P; ++k) {
           const int pos = lp * P + k;
-          if (pos > pos_r || (pos >= pp.sink && pos <= pos_r - pp.window)) continue;
+          if (pos > pos_r || pos >= end || (pos >= pp.sink && pos <= pos_r - pp.window)) continue;
           const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + from + k * kHeadDim);
           const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + from + k * kHeadDim);
           const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
@@ -835,14 +900,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           acc[3] = fmaf(w, vb.y, acc[3]);
         }
       }
-      if (p.n_splits == 1)
+      if (!kShared && p.n_splits == 1)
         *reinterpret_cast<uint2*>(p.out + at) =
             make_uint2(pack2(acc[0] / l_r, acc[1] / l_r), pack2(acc[2] / l_r, acc[3] / l_r));
       else
-        *reinterpret_cast<float4*>(p.part_acc + (part_slot(pp, split) + r) * kHeadDim + 4 * lane) =
+        *reinterpret_cast<float4*>(p.part_acc + (share0() + r) * kHeadDim + 4 * lane) =
             make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
   }
+}
+
+template <int P>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  prompt_body<P, false>(pp, nullptr, map_q, map_k, map_v);
+}
+
+// grid: PrefixTable::ctas
+template <int P>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prefix_kernel(const __grid_constant__ PromptParams pp, const __grid_constant__ PrefixTable table,
+                  const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  prompt_body<P, true>(pp, &table, map_q, map_k, map_v);
 }
 
 // The shares of the rows' splits into out and lse: a warp a row, lane l the dims 4 l .. 4 l + 3
@@ -950,6 +1033,40 @@ int prompt_part_rows(int G, int n_tokens) {
   return (int)std::min<long long>(2 * kTileRows, (long long)n_tokens * G);
 }
 
+// Descriptors of the queries ([tokens][Hq][128], boxes of a tile's tokens and a group's heads) and
+// of a pool.
+static cudaError_t prompt_maps(const Params& p, long long tokens, CUtensorMap* mq, CUtensorMap* mk,
+                               CUtensorMap* mv) {
+  const int G = p.Hq / p.Hkv;
+  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)tokens};
+  const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
+  cudaError_t e = make_map(mq, p.q, 3, qd, qs, qb);
+  if (e != cudaSuccess) return e;
+  // a pool as [8-row group][half of the dims][row][64 dims]
+  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
+  const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
+  const cuuint32_t kb[4] = {64, 8, 2, (cuuint32_t)(p.P / 8)};
+  if ((e = make_map(mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
+  return make_map(mv, p.v_pool, 4, kd, ks, kb);
+}
+
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s) {
+  PromptParams pp{};
+  pp.p = p;
+  pp.window = 1 << 30;
+  const int G = p.Hq / p.Hkv;
+  pp.log_g = G == 8 ? 3 : G / 2;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = prompt_maps(p, p.B, &mq, &mk, &mv);
+  if (e != cudaSuccess) return e;
+  const void* fn = p.P == 16 ? (const void*)prefix_kernel<16> : (const void*)prefix_kernel<32>;
+  const size_t smem = PromptSmem::total + 1024;
+  if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
+  void* args[] = {&pp, const_cast<PrefixTable*>(&t), &mq, &mk, &mv};
+  return launch_pdl(fn, dim3((unsigned)t.ctas), dim3(kPromptThreads), smem, s, args);
+}
+
 // Few work items share their K / V tiles with as many CTAs as fill the GPU once, at least two
 // tiles each.
 int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps) {
@@ -970,17 +1087,8 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   pp.log_g = G == 8 ? 3 : G / 2;
   pp.part_rows = prompt_part_rows(G, n_tokens);
   CUtensorMap mq, mk, mv;
-  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * n_tokens};
-  const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
-  const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
-  cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
+  cudaError_t e = prompt_maps(p, (long long)p.B * n_tokens, &mq, &mk, &mv);
   if (e != cudaSuccess) return e;
-  // a pool as [8-row group][half of the dims][row][64 dims]
-  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
-  const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
-  const cuuint32_t kb[4] = {64, 8, 2, (cuuint32_t)(p.P / 8)};
-  if ((e = make_map(&mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
-  if ((e = make_map(&mv, p.v_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
   const void* fn = p.P == 16 ? (const void*)prompt_kernel<16> : (const void*)prompt_kernel<32>;
   const size_t smem = PromptSmem::total + 1024;
   if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;

@@ -63,13 +63,14 @@ struct SpanLayout {
 };
 
 SpanLayout span_layout(const quest_cache_t& c, int top_k, const quest_opts_t* o,
-                       int n_tokens = 1) {
+                       int n_tokens = 1, size_t prefix_parts = 0) {
   SpanLayout L{};
   const size_t nbg = (size_t)c.batch * c.num_kv_heads;
   size_t parts = span_max_parts(c.batch, c.num_kv_heads, user_split(o) > 0) * group_of(c);
   if (n_tokens > 1)
     parts = std::max(parts, (size_t)(user_split(o) ? kPromptParts : kPromptParts / 2) *
                                 prompt_part_rows(group_of(c), n_tokens));
+  parts = std::max(parts, prefix_parts);
   size_t off = sizeof(WsHeader);
   L.seq_done = off;  off = up256(off + (size_t)c.batch * 4);
   L.arrive = off;    off = up256(off + (size_t)kSplitRows * 4);
@@ -143,6 +144,94 @@ int window_pages(const quest_cache_t& c, int sink, int window) {
 int prompt_pages(const quest_cache_t& c, int n_tokens, int sink, int window) {
   return window_pages(c, sink, (int)std::min<long long>((long long)window + std::min(n_tokens, 256),
                                                         0x7fffffff));
+}
+
+// ---- prefixes that sequences share
+int check_groups(const quest_cache_t& c, const quest_prefix_group_t* groups, int n) {
+  if (!groups || n < 1) return bad("groups must be non-NULL, n_groups >= 1");
+  if (n > QUEST_MAX_PREFIX_GROUPS)
+    return set_last_error(QUEST_ERR_UNSUPPORTED, "n_groups exceeds QUEST_MAX_PREFIX_GROUPS");
+  long long total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (groups[i].count < 1 || groups[i].prefix_tokens < 0 ||
+        groups[i].prefix_tokens > (long long)c.max_pages * c.page_size)
+      return bad("a group needs count >= 1 and prefix_tokens in [0, max_pages * page_size]");
+    total += groups[i].count;
+  }
+  return total == c.batch ? QUEST_OK : bad("the groups' counts must sum to the batch");
+}
+
+// Whether sharing pays: below this many bytes of keys and values that sequences would read again.
+constexpr long long kShareBytes = 0;
+constexpr int kPrefixCtas = 152;      // CTAs of the prefixes' launch that run at once
+constexpr int kPrefixSplits = 64;     // of a prefix
+constexpr int kPrefixStart = 3;       // what a CTA's start and end cost, in tiles
+
+// How the launch over prefixes is cut.  Its CTAs take `per` K / V tiles each, so that they fill
+// their places once, or twice, ..., whichever takes the fewest tiles one after another.
+PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* groups, int n,
+                       const quest_opts_t* o) {
+  PrefixTable t{};
+  t.n = n;
+  const int G = group_of(c), user = user_split(o);
+  long long saved = 0;
+  int first = 0;
+  for (int i = 0; i < n; ++i) {
+    const int pages = groups[i].count > 1 ? groups[i].prefix_tokens / c.page_size : 0;
+    t.group[i] = PrefixTable::Group{first, groups[i].count, pages, 1, 0, 0};
+    first += groups[i].count;
+    saved += (groups[i].count - 1LL) * pages * c.page_size * c.num_kv_heads * (4 * kHeadDim);
+  }
+  if (saved == 0 || (!user && saved < kShareBytes))
+    for (int i = 0; i < n; ++i) t.group[i].pages = 0;
+  auto tiles = [&](int i) {
+    return (t.group[i].pages * c.page_size + kPromptTokens - 1) / kPromptTokens;
+  };
+  auto items = [&](int i) {
+    return (long long)c.num_kv_heads *
+           (((long long)t.group[i].count * G + kPromptRows - 1) / kPromptRows);
+  };
+  int most = 0;
+  for (int i = 0; i < n; ++i) most = std::max(most, tiles(i));
+  auto ctas = [&](int per) {
+    long long sum = 0;
+    for (int i = 0; i < n; ++i) sum += items(i) * ((tiles(i) + per - 1) / per);
+    return sum;
+  };
+  const int least = std::max(2, (most + kPrefixSplits - 1) / kPrefixSplits);
+  int per = std::max(1, most);
+  if (user) {
+    per = std::max(1, user * c.page_size / kPromptTokens);
+    per = std::max(per, (most + kPrefixSplits - 1) / kPrefixSplits);
+  } else if (most > least) {
+    long long best = 0;
+    for (int waves = 1; waves <= 4; ++waves) {
+      int lo = least, hi = most;  // the fewest tiles a CTA with that many waves (hi: all of them)
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ctas(mid) <= (long long)waves * kPrefixCtas) hi = mid;
+        else lo = mid + 1;
+      }
+      const long long cost = (ctas(lo) + kPrefixCtas - 1) / kPrefixCtas * (lo + kPrefixStart);
+      if (best == 0 || cost < best) {
+        best = cost;
+        per = lo;
+      }
+    }
+  }
+  for (int i = 0; i < n; ++i) {
+    PrefixTable::Group& g = t.group[i];
+    g.splits = std::max(1, (tiles(i) + per - 1) / per);
+    g.cta0 = t.ctas;
+    g.part0 = t.parts;
+    if (g.pages > 0) {
+      const int mine = (int)items(i) * g.splits;
+      t.ctas += mine;
+      t.parts += mine * (int)std::min<long long>(kPromptRows, (long long)g.count * G);
+    }
+    t.most_pages = std::max(t.most_pages, c.max_pages - g.pages);
+  }
+  return t;
 }
 
 // One span-decode launch over rows of at most `pages` pages.
@@ -327,6 +416,54 @@ int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, c
   if (!k_new || !v_new) return bad("quest_narrow_decode_step needs k_new and v_new");
   return narrow_decode(cache, q, k_new, v_new, top_k, out, lse, idx_out, count_out, ws, ws_bytes,
                        opts, stream, "quest_narrow_decode_step");
+}
+
+size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefix_group_t* groups,
+                                   int32_t n_groups, const quest_opts_t* opts) {
+  if (check_cache_desc(cache)) return 0;
+  if (cache->batch == 0) return span_layout(*cache, 0, opts).total;
+  if (check_groups(*cache, groups, n_groups)) return 0;
+  const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
+  Params p{};
+  p.B = cache->batch;
+  p.Hkv = cache->num_kv_heads;
+  p.P = cache->page_size;
+  const size_t tails = (size_t)cache->batch * cache->num_q_heads * tail_splits(p, t, user_split(opts));
+  return span_layout(*cache, 0, opts, 1, t.parts + tails).total;
+}
+
+int quest_prefix_decode(const quest_cache_t* cache, const void* q,
+                        const quest_prefix_group_t* groups, int32_t n_groups, void* out, float* lse,
+                        void* ws, size_t ws_bytes, const quest_opts_t* opts,
+                        quest_stream_t stream) {
+  int rc = check_cache_desc(cache);
+  if (rc || cache->batch == 0) return rc;
+  if ((rc = check_groups(*cache, groups, n_groups))) return rc;
+  if ((rc = check_io(q, out, lse))) return rc;
+  const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
+  SpanParams sp{};
+  sp.p.B = cache->batch;
+  sp.p.Hkv = cache->num_kv_heads;
+  sp.p.P = cache->page_size;
+  const int splits = tail_splits(sp.p, t, user_split(opts));
+  const size_t tails = (size_t)cache->batch * cache->num_q_heads * splits;
+  const SpanLayout L = span_layout(*cache, 0, opts, 1, t.parts + tails);
+  if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
+  sp.p = make_params(*cache, ws, L, opts);
+  if (t.ctas == 0) {  // nothing is shared: every sequence on its own
+    sp.mode = kSpanDense;
+    return run_span(sp, false, cache->max_pages, opts, q, out, lse, stream, "quest_prefix_decode");
+  }
+  sp.p.q = static_cast<const __half*>(q);
+  sp.p.out = static_cast<__half*>(out);
+  sp.p.lse = lse;
+  if (opts && opts->wait_limit_ns > 0) sp.p.wait_limit_ns = opts->wait_limit_ns;
+  if (opts) sp.p.debug_flags = opts->debug_flags;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_prefix(sp.p, t, s);
+  if (e == cudaSuccess) e = launch_tail(sp.p, t, splits, s);
+  if (e == cudaSuccess) e = launch_prefix_join(sp.p, t, splits, s);
+  return launched(e, "quest_prefix_decode");
 }
 
 int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,
