@@ -26,7 +26,7 @@ constexpr long long kDefaultWaitNs = 1000000000LL;
 enum FaultSite : int {
   kSiteMeta = 1, kSiteAppend = 2, kSiteScore = 3, kSiteTopk = 4, kSiteDecode = 5,
   kSiteWaitSelection = 6, kSiteWaitStage = 7, kSiteWaitSlot = 8, kSiteSelection = 9,
-  kSiteSpan = 10, kSitePrompt = 11,
+  kSiteSpan = 10, kSitePrompt = 11, kSitePrefix = 12,
 };
 
 // First 256 bytes of the workspace.
@@ -227,7 +227,9 @@ size_t span_max_parts(int batch, int hkv, bool user);
 bool span_selects(const SpanParams& sp, int pages);
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s);
 
-// ---- prefixes that sequences share (quest_prefix.cu: the cut; the launches below)
+// ---- prefixes that sequences share
+constexpr int kPrefixRows = 128;    // query rows (sequence, head) of a work item of the prefixes
+constexpr int kPrefixTokens = 128;  // tokens of its K / V tiles
 // The groups of a batch, in order; passed by value.  A group without pages shares nothing.
 struct PrefixTable {
   struct Group {
@@ -262,7 +264,7 @@ struct PrefixTable {
   }
 };
 
-// Attention over prefixes: the prefixes' shares (prefix_kernel, quest_prompt_kernel.cu), the tails'
+// Attention over prefixes: the prefixes' shares (prefix_kernel, quest_prefix_kernel.cu), the tails'
 // (tail_kernel, quest_span_kernel.cu), and both into out and lse (prefix_join_kernel).
 cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s);
 // Splits of a tail; part_ml / part_acc rows of the tails start at t.parts.
@@ -275,8 +277,6 @@ cudaError_t launch_prefix_join(const Params& p, const PrefixTable& t, int splits
 // part_ml / part_acc each; splits only while items * splits is at most kPromptParts.  Two
 // launches where rows are split (the second joins their shares), one otherwise.
 constexpr int kPromptParts = 304;
-constexpr int kPromptRows = 256;   // query rows of a work item
-constexpr int kPromptTokens = 128; // tokens of its K / V tiles
 int prompt_part_rows(int G, int n_tokens);
 int prompt_splits(const Params& p, int n_tokens, int pages, int user_pps);
 cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, cudaStream_t s);

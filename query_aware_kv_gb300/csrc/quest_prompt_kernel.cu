@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "quest_device.cuh"
+#include "quest_tc.cuh"
 
 namespace quest {
 
@@ -56,7 +57,6 @@ namespace {
 constexpr int kPromptThreads = 384;
 constexpr int kTileRows = 128;       // query rows of a tile; two tiles a CTA
 constexpr int kTileTokens = 128;     // tokens of a K / V tile
-static_assert(kPromptRows == 2 * kTileRows && kPromptTokens == kTileTokens, "the cut's sizes");
 constexpr int kTileBytes = kTileTokens * kHeadDim * 2;  // 32 KiB
 constexpr int kKvStages = 5;         // K and V tiles in flight, alternating
 constexpr int kScores = 3;           // barriers of a query tile's scores, in turn
@@ -79,178 +79,22 @@ struct PromptParams {
   int part_rows; // rows of a work item that partials have room for
 };
 
-// ---- tcgen05 / TMA
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                   smem_u32(slot))
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base));
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-// D (+)= A B with A and B in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// The same with A in TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add)
-      : "memory");
-}
-#define QUEST_R8(a, i) a[i], a[i + 1], a[i + 2], a[i + 3], a[i + 4], a[i + 5], a[i + 6], a[i + 7]
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// One page of one kv head: 8-row groups `group` .. of the pool.
-__device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int group,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(0), "r"(group), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                       uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Shared-memory operand descriptors, 128-byte swizzle: atoms of 8 rows x 64 dims (1 KiB).
 // Q tile: the atoms of dims 0-63 of all rows, then those of dims 64-127, kHalfBytes apart.
 // K and V tiles: per 8 tokens the atoms of both halves of the dims side by side, so that a
 // whole page is one TMA box (two boxes a page took the fetch warp 3200 cycles per tile pair,
 // more than the products); 8-token groups are kGroupBytes apart.
 constexpr int kAtomBytes = 1024, kGroupBytes = 2 * kAtomBytes;
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 |
-         (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
 // fp16 x fp16 -> fp32, 128 x 128 x 16; bit 16: B is MN-major.
 constexpr uint32_t kIdescQK = 1u << 4 | (kTileTokens >> 3) << 17 | (kTileRows >> 4) << 24;
 constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kTileRows >> 4) << 24;
 
-// ---- bounded waits: a wait that runs out sets the CTA's give-up flag, everyone leaves the work,
-// and the CTA then waits for what it has in flight (settle)
-// (Everything this kernel calls is inlined: no call makes the compiler save registers.)
 __device__ __forceinline__ void record(const Params& p, int code, int b, int page) {
-  if (atomicCAS(p.status, 0, code) == 0) {
-    p.status[1] = b;
-    p.status[2] = page;
-    p.status[3] = kSitePrompt;
-  }
-}
-__device__ __forceinline__ bool prompt_wait_slow(const Params& p, uint64_t* bar, uint32_t parity,
-                                              volatile int* give_up) {
-  // the clock is read only after many polls: reading it first made every wait that was not
-  // over yet several hundred cycles longer
-  long long t0 = 0;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 1024; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*give_up) return false;
-    const long long now = global_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > p.wait_limit_ns) {
-      *give_up = 1;
-      record(p, QUEST_ERR_TIMEOUT, -1, -1);
-      return false;
-    }
-  }
+  record_at<kSitePrompt>(p, code, b, page);
 }
 __device__ __forceinline__ bool prompt_wait(const Params& p, uint64_t* bar, uint32_t parity,
                                             volatile int* give_up) {
-  return mbar_try_wait(bar, parity) || prompt_wait_slow(p, bar, parity, give_up);
-}
-
-// Whether a phase that nothing holds up any more (copies and products that were issued) is over;
-// a second at most.
-__device__ __forceinline__ bool settle(uint64_t* bar, uint32_t parity) {
-  const long long t0 = global_ns();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity))
-    if (global_ns() - t0 > kDefaultWaitNs) return false;
-  return true;
-}
-
-// One lane of the warp, the same one every time; the branch on it stays uniform for the
-// compiler, which keeps descriptors in uniform registers (behind `lane == 0` every product
-// took it about 90 cycles to issue, and a tile pair waited 4100 cycles for the issue warp).
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
+  return wait_at<kSitePrompt>(p, bar, parity, give_up);
 }
 
 struct Bars {
@@ -284,92 +128,11 @@ __device__ __forceinline__ size_t part_slot(const PromptParams& pp, int s) {
   return (item * pp.p.n_splits + s) * pp.part_rows;
 }
 
-// A CTA's work: row block `blk` of kv head g, its split's K / V tiles.
-struct Item {
-  int blk, split, n_splits, g, b, n;
-  int pages;      // of a shared prefix
-  size_t share0;  // of a group: where the item's shares start
-};
-
-// CTA c of a launch over prefixes: of its group's CTAs the row blocks vary fastest (the CTAs that
-// read the same tiles run side by side), then the splits, then the kv heads.
-__device__ __forceinline__ Item shared_item(const PrefixTable& t, int hkv, int lg) {
-  const int c = (int)blockIdx.x, i = t.group_of_cta(c);
-  const PrefixTable::Group& q = t.group[i];
-  const int rows = q.count << lg;
-  const int blocks = (rows + 2 * kTileRows - 1) / (2 * kTileRows), at = c - q.cta0;
-  Item it;
-  it.blk = at % blocks;
-  it.split = at / blocks % q.splits;
-  it.n_splits = q.splits;
-  it.g = at / blocks / q.splits;
-  it.b = q.first;
-  it.n = q.count;
-  it.pages = q.pages;
-  it.share0 = (size_t)q.part0 + (size_t)at * min(rows, 2 * kTileRows);
-  return it;
-}
-
-// The lowest x bits (0 <= x <= 32).
-__device__ __forceinline__ uint32_t low_bits(int x) { return (uint32_t)((1ull << x) - 1ull); }
-// A weight row's threads: 128 scores to weights.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Packed fp32 pairs: one instruction for two lanes' worth of arithmetic.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// 32 bytes, 32-byte aligned.
-__device__ __forceinline__ void store8(float* to, const uint32_t* x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]),
-               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
-__device__ __forceinline__ bool not_finite(const uint32_t* o) {
-  bool x = false;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) x |= (o[k] & 0x7f800000u) == 0x7f800000u;
-  return x;
-}
-
-// The attention of one work item.  kShared: its rows are the query tokens of a group's sequences
-// (one each, so that token i of the group is sequence first + i), its tokens the prefix that they
-// share, without a causal mask; what a row sees ends with the prefix or with its own sequence.
-template <int P, bool kShared>
-__device__ __forceinline__ void prompt_body(const PromptParams& pp, const PrefixTable* table,
-                                            const CUtensorMap& map_q, const CUtensorMap& map_k,
-                                            const CUtensorMap& map_v) {
+template <int P>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ unsigned char smem_raw[];
   constexpr int PPT = kTileTokens / P;  // pages of a K / V tile
   const Params& p = pp.p;
@@ -379,18 +142,8 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lg = pp.log_g, G = 1 << lg, TT = kTileRows >> lg;  // tokens of a query tile
 
-  Item it;
-  if constexpr (kShared) {
-    it = shared_item(*table, p.Hkv, lg);
-  } else {
-    it.blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
-    it.split = (int)blockIdx.x % p.n_splits;
-    it.n_splits = p.n_splits;
-    it.g = (int)blockIdx.y;
-    it.b = (int)blockIdx.z;
-    it.n = pp.n_tokens;
-  }
-  const int n = kShared ? it.n : pp.n_tokens, tok0 = it.blk * 2 * TT;
+  const int blk = (int)(gridDim.x - 1 - blockIdx.x) / p.n_splits;  // the longest rows first
+  const int n = pp.n_tokens, tok0 = blk * 2 * TT;
   const int tok1 = min(n, tok0 + 2 * TT);
   const bool two = tok1 - tok0 > TT;
   const int n_q = two ? 2 : 1;  // query tiles with rows
@@ -418,45 +171,24 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
 
   // ---- the CTA's work (its length and first pages are looked up while the barriers and TMEM
   // are set up)
-  const int g = it.g, b = it.b;  // (of a group, b is its first sequence)
+  const int split = (int)blockIdx.x % p.n_splits;
+  const int g = (int)blockIdx.y, b = (int)blockIdx.z;
+  int L = p.seq_lens[b];
+  if (L < 0 || (long long)L > (long long)p.max_pages * P) {
+    if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
+    L = 0;
+  }
+  const int pos0 = L - n;  // position of query token 0 (may be negative)
+  const int end = pos0 + tok1;
   PageList list{0, 0, 0, 0};
-  int pos0 = 0, end;  // position of query token 0 (may be negative); the end of what rows see
-  auto length = [&](int seq) {
-    const int L = p.seq_lens[seq];
-    if (L >= 0 && (long long)L <= (long long)p.max_pages * P) return L;
-    record(p, QUEST_ERR_BAD_LENGTH, seq, -1);
-    return 0;
-  };
-  if constexpr (kShared) {
-    int most = 0;
-    for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(b + i));
-    end = min(__reduce_max_sync(0xffffffffu, most), it.pages * P);
-    list.count = (end + P - 1) / P;
-  } else {
-    int L = p.seq_lens[b];
-    if (L < 0 || (long long)L > (long long)p.max_pages * P) {
-      if (threadIdx.x == 0) record(p, QUEST_ERR_BAD_LENGTH, b, -1);
-      L = 0;
-    }
-    pos0 = L - n;
-    end = pos0 + tok1;
-    if (end > 0) {
-      list.lo = max(0, max(0, pos0 + tok0) - pp.window + 1);
-      list.first = list.lo / P;
-      list.n_sink = min((min(pp.sink, list.lo) + P - 1) / P, list.first);
-      list.count = list.n_sink + (end + P - 1) / P - list.first;
-    }
+  if (end > 0) {
+    list.lo = max(0, max(0, pos0 + tok0) - pp.window + 1);
+    list.first = list.lo / P;
+    list.n_sink = min((min(pp.sink, list.lo) + P - 1) / P, list.first);
+    list.count = list.n_sink + (end + P - 1) / P - list.first;
   }
   const int tiles = (list.count + PPT - 1) / PPT;
-  const int j0 = tiles * it.split / it.n_splits, j1 = tiles * (it.split + 1) / it.n_splits;
-  // the first of the item's rows of q, out and lse, in tokens
-  // (taken where it is used: a value kept over the loops makes the compiler spill)
-  auto q_tok0 = [&]() { return kShared ? (size_t)b + tok0 : (size_t)b * n + tok0; };
-  // where the item's row r keeps its share
-  auto share0 = [&]() {
-    return kShared ? shared_item(*table, p.Hkv, lg).share0
-                   : part_slot(pp, (int)blockIdx.x % p.n_splits);
-  };
+  const int j0 = tiles * split / p.n_splits, j1 = tiles * (split + 1) / p.n_splits;
 
   // Pages of the list, for the fetch warps: 32 at a time, a page per lane, the next 32 on their
   // way; entries behind the list's end repeat its last page (their tokens are hidden).
@@ -477,7 +209,7 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
     mbar_arrive_expect_tx(&bars.q_full, n_q * kTileBytes);
     for (int i = 0; i < 2 * n_q; ++i)
       tma_3d(smem + PromptSmem::q + (i >> 1) * kTileBytes + (i & 1) * kHalfBytes, &map_q,
-             64 * (i & 1), g * G, (int)q_tok0() + (i >> 1) * TT, &bars.q_full);
+             64 * (i & 1), g * G, b * n + tok0 + (i >> 1) * TT, &bars.q_full);
   }
   __syncwarp();
 
@@ -629,19 +361,14 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
     // ---- softmax: a thread a row
     const int t = warp >> 2, row = threadIdx.x & 127;
     const int tok = tok0 + t * TT + (row >> lg);
-    int pr = pos0 + tok;  // the row's position
-    int least = 0;  // of a group: of the warp's rows (they go together)
-    if constexpr (kShared) {
-      pr = tok < tok1 ? length(b + tok) - 1 : end - 1;
-      least = __reduce_min_sync(0xffffffffu, pr);
-    }
+    const int pr = pos0 + tok;  // the row's position
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + 256 + t * 128;
     float m = -CUDART_INF_F, l = 0.f;
     bool ok = true;
     if (t < n_q) {
-      const int r0 = kShared ? least : pos0 + tok0 + t * TT;
-      const int r1 = kShared ? end - 1 : min(r0 + TT, end) - 1;
+      const int r0 = pos0 + tok0 + t * TT;
+      const int r1 = min(r0 + TT, end) - 1;
       for (int j = j0; j < j1; ++j) {
         const uint32_t turn = (uint32_t)(j - j0) / kScores;  // (counters would spill here)
         ok = __all_sync(0xffffffffu, prompt_wait(p, &bars.s_full[t][(uint32_t)(j - j0) - turn * kScores],
@@ -765,10 +492,10 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
       const bool none = l == 0.f;  // (a NaN sum is not: its NaN goes out)
       const bool mine = tok < tok1;
       bool odd = false;  // some of the row's O is not finite
-      if (!kShared && ok && p.n_splits == 1) {
+      if (ok && p.n_splits == 1) {
         // ---- out = O / l, through the tile's own query space (its products are done): a row
         // of 256 B per thread goes to shared memory, two rows at a time leave as whole lines
-        const size_t row0 = (q_tok0() + t * TT) * p.Hq + ((size_t)g << lg);
+        const size_t row0 = ((size_t)b * n + tok0 + t * TT) * p.Hq + ((size_t)g << lg);
         unsigned char* stage = smem + PromptSmem::q + t * kTileBytes;
         const float inv = none ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -806,7 +533,7 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
         }
       } else if (ok) {
         // ---- a split's share: O, m and l as they are (the loads are the whole warp's)
-        const size_t slot = share0() + t * kTileRows + row;
+        const size_t slot = part_slot(pp, split) + t * kTileRows + row;
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           uint32_t o[32];
@@ -870,8 +597,8 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
       const float2 ml = *stash(r / kTileRows, r % kTileRows);
       const float m_r = ml.x, l_r = ml.y;
       if (l_r < 0.f) continue;  // warp-uniform
-      const int pos_r = kShared ? length(b + tok0 + (r >> lg)) - 1 : pos0 + tok0 + (r >> lg);
-      const size_t at = ((q_tok0() + (r >> lg)) * p.Hq + ((size_t)g << lg) +
+      const int pos_r = pos0 + tok0 + (r >> lg);
+      const size_t at = (((size_t)b * n + tok0 + (r >> lg)) * p.Hq + ((size_t)g << lg) +
                          (r & (G - 1))) * kHeadDim + 4 * lane;
       const uint2 qw = *reinterpret_cast<const uint2*>(p.q + at);
       const float2 qa = h2f(qw.x), qb = h2f(qw.y);
@@ -886,7 +613,7 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
 #pragma unroll 4
         for (int k = 0; k < P; ++k) {
           const int pos = lp * P + k;
-          if (pos > pos_r || pos >= end || (pos >= pp.sink && pos <= pos_r - pp.window)) continue;
+          if (pos > pos_r || (pos >= pp.sink && pos <= pos_r - pp.window)) continue;
           const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + from + k * kHeadDim);
           const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + from + k * kHeadDim);
           const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
@@ -900,32 +627,14 @@ __device__ __forceinline__ void prompt_body(const PromptParams& pp, const Prefix
           acc[3] = fmaf(w, vb.y, acc[3]);
         }
       }
-      if (!kShared && p.n_splits == 1)
+      if (p.n_splits == 1)
         *reinterpret_cast<uint2*>(p.out + at) =
             make_uint2(pack2(acc[0] / l_r, acc[1] / l_r), pack2(acc[2] / l_r, acc[3] / l_r));
       else
-        *reinterpret_cast<float4*>(p.part_acc + (share0() + r) * kHeadDim + 4 * lane) =
+        *reinterpret_cast<float4*>(p.part_acc + (part_slot(pp, split) + r) * kHeadDim + 4 * lane) =
             make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
   }
-}
-
-template <int P>
-__global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_kernel(PromptParams pp, const __grid_constant__ CUtensorMap map_q,
-                  const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v) {
-  prompt_body<P, false>(pp, nullptr, map_q, map_k, map_v);
-}
-
-// grid: PrefixTable::ctas
-template <int P>
-__global__ void __launch_bounds__(kPromptThreads, 1)
-    prefix_kernel(const __grid_constant__ PromptParams pp, const __grid_constant__ PrefixTable table,
-                  const __grid_constant__ CUtensorMap map_q,
-                  const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v) {
-  prompt_body<P, true>(pp, &table, map_q, map_k, map_v);
 }
 
 // The shares of the rows' splits into out and lse: a warp a row, lane l the dims 4 l .. 4 l + 3
@@ -985,43 +694,6 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptParams 
     p.lse[at] = none ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
 }
 
-// cuTensorMapEncodeTiled, taken from the driver at run time (nothing links against it).
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encode_fn(EncodeFn* fn) {
-  static std::mutex mu;
-  static EncodeFn found = nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!found) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    const cudaError_t e =
-        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r);
-    if (e != cudaSuccess) return e;
-    if (r != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-    found = reinterpret_cast<EncodeFn>(f);
-  }
-  *fn = found;
-  return cudaSuccess;
-}
-
-// A map of fp16 boxes whose inner 64 dims are a 128-byte swizzle span.
-cudaError_t make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                     const cuuint64_t* strides, const cuuint32_t* box) {
-  EncodeFn fn = nullptr;
-  const cudaError_t e = encode_fn(&fn);
-  if (e != cudaSuccess) return e;
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-                        const_cast<void*>(base), dims, strides, box, one,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 static int prompt_blocks(int G, int n_tokens) {
@@ -1031,40 +703,6 @@ static int prompt_blocks(int G, int n_tokens) {
 
 int prompt_part_rows(int G, int n_tokens) {
   return (int)std::min<long long>(2 * kTileRows, (long long)n_tokens * G);
-}
-
-// Descriptors of the queries ([tokens][Hq][128], boxes of a tile's tokens and a group's heads) and
-// of a pool.
-static cudaError_t prompt_maps(const Params& p, long long tokens, CUtensorMap* mq, CUtensorMap* mk,
-                               CUtensorMap* mv) {
-  const int G = p.Hq / p.Hkv;
-  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)tokens};
-  const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
-  const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
-  cudaError_t e = make_map(mq, p.q, 3, qd, qs, qb);
-  if (e != cudaSuccess) return e;
-  // a pool as [8-row group][half of the dims][row][64 dims]
-  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
-  const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
-  const cuuint32_t kb[4] = {64, 8, 2, (cuuint32_t)(p.P / 8)};
-  if ((e = make_map(mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
-  return make_map(mv, p.v_pool, 4, kd, ks, kb);
-}
-
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s) {
-  PromptParams pp{};
-  pp.p = p;
-  pp.window = 1 << 30;
-  const int G = p.Hq / p.Hkv;
-  pp.log_g = G == 8 ? 3 : G / 2;
-  CUtensorMap mq, mk, mv;
-  cudaError_t e = prompt_maps(p, p.B, &mq, &mk, &mv);
-  if (e != cudaSuccess) return e;
-  const void* fn = p.P == 16 ? (const void*)prefix_kernel<16> : (const void*)prefix_kernel<32>;
-  const size_t smem = PromptSmem::total + 1024;
-  if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
-  void* args[] = {&pp, const_cast<PrefixTable*>(&t), &mq, &mk, &mv};
-  return launch_pdl(fn, dim3((unsigned)t.ctas), dim3(kPromptThreads), smem, s, args);
 }
 
 // Few work items share their K / V tiles with as many CTAs as fill the GPU once, at least two
@@ -1087,8 +725,17 @@ cudaError_t launch_prompt(const Params& p, int n_tokens, int sink, int window, c
   pp.log_g = G == 8 ? 3 : G / 2;
   pp.part_rows = prompt_part_rows(G, n_tokens);
   CUtensorMap mq, mk, mv;
-  cudaError_t e = prompt_maps(p, (long long)p.B * n_tokens, &mq, &mk, &mv);
+  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * n_tokens};
+  const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
+  cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
   if (e != cudaSuccess) return e;
+  // a pool as [8-row group][half of the dims][row][64 dims]
+  const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
+  const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
+  const cuuint32_t kb[4] = {64, 8, 2, (cuuint32_t)(p.P / 8)};
+  if ((e = make_map(&mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
+  if ((e = make_map(&mv, p.v_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
   const void* fn = p.P == 16 ? (const void*)prompt_kernel<16> : (const void*)prompt_kernel<32>;
   const size_t smem = PromptSmem::total + 1024;
   if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;

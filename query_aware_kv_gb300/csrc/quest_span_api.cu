@@ -185,11 +185,11 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   if (saved == 0 || (!user && saved < kShareBytes))
     for (int i = 0; i < n; ++i) t.group[i].pages = 0;
   auto tiles = [&](int i) {
-    return (t.group[i].pages * c.page_size + kPromptTokens - 1) / kPromptTokens;
+    return (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
   };
   auto items = [&](int i) {
     return (long long)c.num_kv_heads *
-           (((long long)t.group[i].count * G + kPromptRows - 1) / kPromptRows);
+           (((long long)t.group[i].count * G + kPrefixRows - 1) / kPrefixRows);
   };
   int most = 0;
   for (int i = 0; i < n; ++i) most = std::max(most, tiles(i));
@@ -201,7 +201,7 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   const int least = std::max(2, (most + kPrefixSplits - 1) / kPrefixSplits);
   int per = std::max(1, most);
   if (user) {
-    per = std::max(1, user * c.page_size / kPromptTokens);
+    per = std::max(1, user * c.page_size / kPrefixTokens);
     per = std::max(per, (most + kPrefixSplits - 1) / kPrefixSplits);
   } else if (most > least) {
     long long best = 0;
@@ -227,7 +227,7 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
     if (g.pages > 0) {
       const int mine = (int)items(i) * g.splits;
       t.ctas += mine;
-      t.parts += mine * (int)std::min<long long>(kPromptRows, (long long)g.count * G);
+      t.parts += mine * (int)std::min<long long>(kPrefixRows, (long long)g.count * G);
     }
     t.most_pages = std::max(t.most_pages, c.max_pages - g.pages);
   }

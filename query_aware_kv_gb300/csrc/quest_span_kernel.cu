@@ -850,10 +850,10 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
   const int shared = q.pages > 0 ? q.splits : 0, n = shared + p.n_splits;
   size_t slot0 = 0, step = 0;  // of the prefix's
   if (shared) {
-    const int rows = q.count * G, part_rows = min(rows, kPromptRows);
-    const int blocks = (rows + kPromptRows - 1) / kPromptRows;
+    const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
+    const int blocks = (rows + kPrefixRows - 1) / kPrefixRows;
     const int r = (b - q.first) * G + h % G;
-    slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPromptRows) * part_rows + r % kPromptRows;
+    slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPrefixRows) * part_rows + r % kPrefixRows;
     step = (size_t)blocks * part_rows;
   }
   const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * p.n_splits * G + h % G;

@@ -87,6 +87,31 @@ def test_matches_64_bits(batch, geom, pps):
     right(cache, qq, out, lse)
 
 
+@pytest.mark.parametrize("geom", GEOMS, ids=str)
+@pytest.mark.parametrize("tokens", [200, 700, 1900])
+def test_scores_that_grow_along_the_prefix(tokens, geom):
+    """The running maximum moves again and again (also within a work item, and in one half of a
+    tile alone): large queries against keys that grow."""
+    cache, groups = make([(tokens, [tokens + 9] * 6)], *geom, seed=tokens)
+    P = cache.page_size
+    qq = queries(cache) * 3
+    for page in range(-(-(tokens + 9) // P)):
+        for b in range(cache.batch if page * P >= tokens // P * P else 1):
+            cache.k_pool[int(cache.block_table[b, page])] *= 0.25 + 2.5 * page * P / tokens
+    for pps in (0, 1000):
+        out, lse = run(cache, groups, qq, pps)
+        right(cache, qq, out, lse)
+
+
+@pytest.mark.parametrize("rows", [32, 9])
+def test_work_items_of_many_tiles(rows):
+    """Sixteen tiles a work item, all of its rows in use, or a few."""
+    cache, groups = make([(2100, [2100 + 7 * i for i in range(rows)])], 8, 2, 16, seed=rows)
+    qq = queries(cache) * 2
+    out, lse = run(cache, groups, qq, 2048 // 16)
+    right(cache, qq, out, lse)
+
+
 def test_long_prefixes_and_pools_past_4_gib():
     """16K-token prefixes at the end of pools of 4.6 GB each."""
     cache, groups = make([(16400, [16500, 16401, 17000, 16400, 16899]), (8000, [8001, 9000])], 32, 8, 16)
