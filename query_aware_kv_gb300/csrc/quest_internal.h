@@ -236,10 +236,10 @@ struct PrefixTable {
     int first, count;  // sequences
     int pages;         // of the prefix that is read once
     int splits;        // of its K / V tiles
-    int cta0;          // the group's first CTA of the launch over prefixes
+    int cta0;          // the group's first job
     int part0;         // its first row of part_ml / part_acc
   };
-  int n, ctas;    // groups; CTAs of the launch over prefixes (0: nothing is shared)
+  int n, ctas;    // groups; jobs of the prefixes (0: nothing is shared)
   int parts;      // rows of part_ml / part_acc of the prefixes' shares
   int most_pages; // of a sequence behind its prefix
   Group group[QUEST_MAX_PREFIX_GROUPS];
@@ -255,7 +255,7 @@ struct PrefixTable {
     }
     return lo;
   }
-  // (a group without CTAs starts where the next one does)
+  // (a group without jobs starts where the next one does)
   __host__ __device__ int group_of_cta(int c) const {
     return last(c, [](const Group& g) { return g.cta0; });
   }
@@ -264,13 +264,11 @@ struct PrefixTable {
   }
 };
 
-// Attention over prefixes: the prefixes' shares (prefix_kernel, quest_prefix_kernel.cu), the tails'
-// (tail_kernel, quest_span_kernel.cu), and both into out and lse (prefix_join_kernel).
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s);
-// Splits of a tail; part_ml / part_acc rows of the tails start at t.parts.
-int tail_splits(const Params& p, const PrefixTable& t, int user_pps);
-cudaError_t launch_tail(const Params& p, const PrefixTable& t, int splits, cudaStream_t s);
-cudaError_t launch_prefix_join(const Params& p, const PrefixTable& t, int splits, cudaStream_t s);
+constexpr int kPrefixSms = 152;     // CTAs that take jobs (a GB300's SMs)
+constexpr int kPrefixSplits = 64;   // of a prefix, and of a tail
+// The cuts of the prefixes (t.ctas jobs), then `splits` jobs for every sequence's and kv head's tail
+// (part_ml / part_acc rows from t.parts on), then all shares into out and lse: two launches.
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, cudaStream_t s);
 
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
 // p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of

@@ -1,20 +1,24 @@
-// quest_prefix_kernel.cu - attention of a group's query tokens over the prefix that their
-// sequences share, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands
-// by TMA).
+// quest_prefix_kernel.cu - attention of one query token per sequence where groups of sequences
+// share a prefix, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands by
+// TMA).
 //
-// A row is (sequence of the group, query head of a kv head's group); a CTA takes 128 rows and a
-// run of the prefix's tokens, 128 to a K / V tile, so that a tile is read once for up to 128 rows:
+// The work is a queue of jobs, each a run of pages that up to 128 rows attend over, a row being
+// (sequence, query head): first the cuts of the prefixes, whose rows are a group's query tokens with
+// the G heads of a kv head (so that a prefix is read once for all of them), then every sequence's own
+// tokens behind its prefix (G rows).  A CTA an SM takes jobs in turn; the lengths are on the device
+// only, so nobody could deal them out evenly beforehand.  Per 128 tokens of a job:
 //   S = Q K^T,   P = 2^(S c - m + 8),   O += P V
-// with a running maximum m and sum of weights per row.  There is no causal mask (queries come
-// after the prefix); a row ends with its own sequence where that is shorter.  What leaves is a
-// share (m, sum, O) per row, which prefix_join_kernel joins with the other shares and the tail's.
+// with a running maximum m and sum of weights per row.  There is no causal mask (the queries come
+// after everything); a row of a prefix ends with its own sequence where that is shorter.  What a job
+// leaves is a share (m, sum, O) per row; prefix_join_kernel joins a row's shares.
 //
 // Eight softmax warps share a tile: warps 0-3 its first 64 tokens, warps 4-7 the other 64, a thread
 // a row of 64 scores in registers.  Either half has a maximum, a sum and an O of its own (two O in
-// TMEM), so that the halves never wait for one another; they are added at the end, in registers.
-// Scores have two buffers in TMEM: Q K^T of tile j + 1 runs while tile j is in its softmax, P V
-// while tile j + 1 is.  Warps 8 and 9 fetch K and V (a page a TMA box, three tiles of each in
-// flight), warp 10 issues the products.
+// TMEM), so that the halves never wait for one another; they are added at a job's end, in registers.
+// Scores have two buffers in TMEM: Q K^T of tile t + 1 runs while tile t is in its softmax, P V
+// while tile t + 1 is.  Warps 8 and 9 fetch K and V (a page a TMA box, three tiles of each in
+// flight, over the ends of jobs), warp 10 issues the products, warp 11 takes jobs from the queue and
+// fetches their queries.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -27,7 +31,7 @@ namespace quest {
 
 namespace {
 
-constexpr int kPrefixThreads = 352;
+constexpr int kPrefixThreads = 384;
 constexpr int kRows = kPrefixRows, kTokens = kPrefixTokens;
 constexpr int kTile = kTokens * kHeadDim * 2;  // 32 KiB
 constexpr int kHalf = kTile / 2;  // 64 dims of every row: one 128-byte swizzle span
@@ -35,14 +39,48 @@ constexpr int kSlots = 3;         // K tiles, and V tiles, in flight
 constexpr float kBias = 8.f;      // as the tail's: shares of both are joined
 constexpr float kLazy = 6.f;      // the maximum moves when a row exceeds it by 2^6
 
-// The queries, then K and V of each slot side by side.
+// A run of pages that a row block attends over.
+struct Job {
+  int n;       // tiles, of 128 tokens from page0's first on; 0: its rows see nothing; -1: no more jobs
+  int shared;  // of a prefix: the rows are tokens q_tok .. of a group, which may end early
+  int seq;     // the row of the block table
+  int g;       // the kv head
+  int page0, end;   // the first page; the position behind the last token
+  int q_tok, rows;  // the first query token; rows in use
+  int share;        // the first row's place in part_ml / part_acc
+};
+
+struct Bars {
+  uint64_t q_full, q_free;                        // a job's queries: fetched; last read
+  uint64_t full[kSlots][2], free[kSlots][2];      // of a slot's K and V: fetched; read
+  // Scores and weights of a buffer: tile t (of all jobs, counted through) is in buffer t % 2.  Nobody
+  // is late by a phase: Q K^T of tile t + 2 is issued after the weights of tile t have been waited
+  // for, which every softmax warp gave after it had seen the scores of tile t.
+  uint64_t s_full[2], p_full[2];
+  // P V of a tile is done.  Who asks for tile t - 1 has seen the scores of tile t, whose barrier
+  // also says that P V of tile t - 2 is done.
+  uint64_t pv_done;
+  uint64_t o_full, o_free;             // a job's O: complete; read
+  uint64_t job_full[2], job_free[2];   // a job's description: written; read by every warp
+  uint64_t pair[4];                    // a row's halves have left their maxima and sums
+  uint64_t drain;
+  Job job[2];
+  uint32_t tmem;
+  int give_up;
+  int fetched[2], q_fetched;  // K and V tiles, and queries, whose copies have been issued
+};
+
+// The queries, then K and V of each slot side by side.  (There is no room to align the start: the
+// kernel checks it.)
 struct Smem {
   static constexpr int q = 0;
   static constexpr int kv = kTile;  // [kSlots][K, V]
-  static constexpr int bars = kv + 2 * kSlots * kTile;
-  static constexpr int total = bars + 256;
+  static constexpr int stash = kv + 2 * kSlots * kTile;  // [2][128] a half's maximum and sum
+  static constexpr int bars = stash + 2 * kRows * 8;
+  static constexpr int total = bars + 512;
 };
-static_assert(Smem::total + 1024 <= (int)kMaxSmem, "shared memory of a CTA");
+static_assert(sizeof(Bars) <= 512, "barrier area");
+static_assert(Smem::total <= (int)kMaxSmem, "shared memory of a CTA");
 
 // Operands as in the prompt kernel: Q as the atoms of dims 0-63 of all rows, then those of dims
 // 64-127; K and V per 8 tokens the atoms of both halves side by side, so that a page is one box.
@@ -51,38 +89,12 @@ constexpr int kAtomBytes = 1024, kGroupBytes = 2 * kAtomBytes;
 constexpr uint32_t kIdescQK = 1u << 4 | (kTokens >> 3) << 17 | (kRows >> 4) << 24;
 constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kRows >> 4) << 24;
 
-struct Bars {
-  uint64_t q_full;
-  uint64_t full[kSlots][2], free[kSlots][2];  // of a slot's K and V: fetched; read by its product
-  // Scores and weights of a buffer: tile i (from the CTA's first) is in buffer i % 2.  Nobody is
-  // late by a phase: Q K^T of tile i + 2 is issued after the weights of tile i have been waited for,
-  // which every softmax warp gave after it had seen the scores of tile i.
-  uint64_t s_full[2], p_full[2];
-  // P V of a tile is done.  Who asks for tile i - 1 has seen the scores of tile i, whose barrier
-  // also says that P V of tile i - 2 is done.
-  uint64_t pv_done, o_full, drain;
-  uint32_t tmem;
-  int give_up;
-  int fetched[2];  // K and V tiles whose copies have been issued
+struct PrefixParams {
+  Params p;      // exited: the queue's counter
+  int log_g;
+  int splits;    // jobs of a tail
+  int jobs;
 };
-static_assert(sizeof(Bars) <= 256, "barrier area");
-
-// A CTA's work: a row block of a kv head, and a split's tiles.
-struct Item {
-  int blk, split, n_splits, g, first, count, pages;
-};
-
-// Of a group's CTAs the row blocks vary fastest (the CTAs that read the same tiles run side by
-// side), then the splits, then the kv heads; *share: where the item's shares start.
-__device__ __forceinline__ Item item_of(const PrefixTable& t, int log_g, size_t* share) {
-  const int c = (int)blockIdx.x;
-  const PrefixTable::Group& q = t.group[t.group_of_cta(c)];
-  const int rows = q.count << log_g;
-  const int blocks = (rows + kRows - 1) / kRows, at = c - q.cta0;
-  if (share) *share = (size_t)q.part0 + (size_t)at * min(rows, kRows);
-  return Item{at % blocks, at / blocks % q.splits, q.splits, at / blocks / q.splits,
-              q.first, q.count, q.pages};
-}
 
 // What brings a half's part of a softmax to the maximum M of both (as part_factor of the span
 // decode: a part without a weight is 0, one of NaN scores goes on, an infinite O stays one).
@@ -92,119 +104,174 @@ __device__ __forceinline__ float half_factor(float m, float l, float M) {
 
 template <int P>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
-    prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixTable table,
-                  int log_g, const __grid_constant__ CUtensorMap map_q,
+    prefix_kernel(const __grid_constant__ PrefixParams pp, const __grid_constant__ PrefixTable table,
+                  const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_1,
                   const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v) {
-  extern __shared__ unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int PPT = kTokens / P;  // pages of a tile
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const Params& p = pp.p;
+  if (smem_u32(smem) & 1023) {  // (the swizzle's atoms; no compiler has placed it elsewhere)
+    if (threadIdx.x == 0) record_at<kSitePrefix>(p, QUEST_ERR_UNSUPPORTED, -1, -1);
+    return;
+  }
   Bars& bars = *reinterpret_cast<Bars*>(smem + Smem::bars);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // (uniform to the compiler)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_free, 1);
     for (int i = 0; i < kSlots; ++i)
       for (int kv = 0; kv < 2; ++kv) {
         mbar_init(&bars.full[i][kv], 1);
         mbar_init(&bars.free[i][kv], 1);
       }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.job_full[i], 1);
+      mbar_init(&bars.job_free[i], 11);
     }
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_full, 1);
+    mbar_init(&bars.o_free, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars.pair[i], 2);
     mbar_init(&bars.drain, 1);
-    bars.give_up = bars.fetched[0] = bars.fetched[1] = 0;
+    bars.give_up = bars.fetched[0] = bars.fetched[1] = bars.q_fetched = 0;
     fence_mbar_init();
   }
   if (warp == 10) tmem_alloc(&bars.tmem);
-  if (warp == 8 && lane < 3)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v)
+  if (warp == 8 && lane < 4)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0   ? &map_q
+                                                  : lane == 1 ? &map_k
+                                                  : lane == 2 ? &map_v
+                                                              : &map_1)
                  : "memory");
-  const int lg = log_g, G = 1 << lg;
-  const Item it = item_of(table, lg, nullptr);
-  const int tok0 = it.blk * (kRows >> lg), tok1 = min(it.count, tok0 + (kRows >> lg));
-  const int tiles = (it.pages + PPT - 1) / PPT;
-  const int j0 = tiles * it.split / it.n_splits;
-  int j1 = tiles * (it.split + 1) / it.n_splits;
+  fence_before();
+  __syncthreads();
+  fence_after();
   pdl_wait();
-  pdl_trigger();  // the tails' launch, which waits for this one only at its end
+  pdl_trigger();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+  volatile int* give_up = &bars.give_up;
+  const int lg = pp.log_g;
 
-  // Pages for the fetch warps: 32 at a time, a page per lane, the next 32 on their way (the first
-  // ones beside the lengths); entries behind the prefix's end repeat its last page (its tokens are
-  // hidden there).
-  auto entry = [&](int i) {
-    return p.block_table[(size_t)it.first * p.max_pages + min(i, it.pages - 1)];
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, bar, parity, give_up)) != 0;
   };
-  int now = 0, next = 0;
-  if (warp == 8 || warp == 9) {
-    now = entry(j0 * PPT + lane);
-    next = entry(j0 * PPT + 32 + lane);
-  }
   auto length = [&](int seq) {
     const int L = p.seq_lens[seq];
     if (L >= 0 && (long long)L <= (long long)p.max_pages * P) return L;
     record_at<kSitePrefix>(p, QUEST_ERR_BAD_LENGTH, seq, -1);
     return 0;
   };
-  int most = 0;
-  for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(it.first + i));
-  // the end of what some row sees
-  const int end = min(__reduce_max_sync(0xffffffffu, most), it.pages * P);
-  j1 = max(j0, min(j1, (end + kTokens - 1) / kTokens));
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
-  volatile int* give_up = &bars.give_up;
-
-  const int n = j1 - j0;  // the CTA's tiles
-
-  // A row's places for maxima and sums (of its halves, of a row that is taken again), in the
-  // queries' space once the last product is done.
-  auto stash = [&](int t, int row) {
-    return reinterpret_cast<float2*>(smem + Smem::q) + t * kRows + row;
+  // The k-th job of the CTA, for every warp but the one that writes them; false: there is none.
+  auto take = [&](int k, Job& job) {
+    if (!wait(&bars.job_full[k & 1], (uint32_t)(k >> 1) & 1)) return false;
+    job = bars.job[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.job_free[k & 1]);
+    return job.n >= 0;
   };
-  bool again = false;
-  bool ok = true;
-  float m = -CUDART_INF_F, l = 0.f;  // of a softmax thread's half
-  const int half = warp >> 2, row = threadIdx.x & 127;
-  const bool mine = warp < 8 && tok0 + (row >> lg) < tok1;
-  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  if (warp >= 8) {
-    if (warp < 10) {
-      // ---- fetch: warp 8 the queries and K tiles, warp 9 the V tiles
-      const int kv = warp == 9;
-      if (!kv && elect_lane()) {
-        mbar_arrive_expect_tx(&bars.q_full, kTile);
-        for (int i = 0; i < 2; ++i)
-          tma_3d(smem + Smem::q + i * kHalf, &map_q, 64 * i, it.g * G, it.first + tok0, &bars.q_full);
+
+  if (warp == 11) {
+    // ---- jobs and their queries
+    int index = (int)blockIdx.x, k = 0, loads = 0;
+    while (true) {
+      Job job{-1, 0, 0, 0, 0, 0, 0, 0, 0};
+      int next = 0;
+      if (index < pp.jobs) {
+        if (lane == 0) next = (int)(gridDim.x + atomicAdd(p.exited, 1u));
+        if (index < table.ctas) {
+          const PrefixTable::Group& q = table.group[table.group_of_cta(index)];
+          const int rows = q.count << lg, blocks = (rows + kRows - 1) / kRows, at = index - q.cta0;
+          const int blk = at % blocks, split = at / blocks % q.splits;
+          const int tok0 = blk * (kRows >> lg), tok1 = min(q.count, tok0 + (kRows >> lg));
+          const int tiles = (q.pages + PPT - 1) / PPT;
+          const int j0 = tiles * split / q.splits, j1 = tiles * (split + 1) / q.splits;
+          int most = 0;  // the longest of the rows' sequences
+          for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(q.first + i));
+          job.shared = 1;
+          job.seq = q.first;
+          job.g = at / blocks / q.splits;
+          job.page0 = j0 * PPT;
+          job.end = min(__reduce_max_sync(0xffffffffu, most), min(j1 * PPT, q.pages) * P);
+          job.q_tok = q.first + tok0;
+          job.rows = (tok1 - tok0) << lg;
+          job.share = q.part0 + at * min(rows, kRows);
+        } else {
+          const int t = index - table.ctas, split = t % pp.splits, row = t / pp.splits;
+          job.seq = job.q_tok = row / p.Hkv;
+          job.g = row % p.Hkv;
+          const int first = table.group[table.group_of_seq(job.seq)].pages;
+          const int L = length(job.seq), count = max(0, (L + P - 1) / P - first);
+          job.page0 = first + (int)((long long)count * split / pp.splits);
+          job.end = min(L, (first + (int)((long long)count * (split + 1) / pp.splits)) * P);
+          job.rows = 1 << lg;
+          job.share = table.parts + (t << lg);
+        }
+        job.n = max(0, job.end - job.page0 * P + kTokens - 1) / kTokens;
+      }
+      if (k >= 2 && !wait(&bars.job_free[k & 1], (uint32_t)((k >> 1) - 1) & 1)) break;
+      if (lane == 0) {
+        bars.job[k & 1] = job;
+        mbar_arrive(&bars.job_full[k & 1]);
       }
       __syncwarp();
+      if (job.n < 0) break;
+      if (job.n > 0) {
+        if (loads > 0 && !wait(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
+        if (elect_lane()) {
+          // of a tail only its own G rows: the others' scores may be anything
+          mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : (kHeadDim * 2) << lg);
+          for (int i = 0; i < 2; ++i)
+            tma_3d(smem + Smem::q + i * kHalf, job.shared ? &map_q : &map_1, 64 * i, job.g << lg,
+                   job.q_tok, &bars.q_full);
+        }
+        __syncwarp();
+        ++loads;
+      }
+      index = __shfl_sync(0xffffffffu, next, 0);
+      ++k;
+    }
+    if (lane == 0) bars.q_fetched = loads;
+  } else if (warp >= 8 && warp < 10) {
+    // ---- fetch: warp 8 the K tiles, warp 9 the V tiles
+    const int kv = warp - 8;
+    Job job;
+    int slot = 0, total = 0;
+    uint32_t ph = 1;  // (of the phase before a slot's first: over)
+    bool ok = true;
+    for (int k = 0; ok && take(k, job); ++k) {
+      // Pages, 32 at a time, a page per lane, the next 32 on their way; entries behind the job's
+      // end repeat its last page (its tokens are hidden there).
+      const int pages = (job.end + P - 1) / P - job.page0;
+      auto entry = [&](int i) {
+        return p.block_table[(size_t)job.seq * p.max_pages + job.page0 + min(i, pages - 1)];
+      };
       auto checked = [&](int phys, int i) {
         if (phys >= 0 && phys < p.num_phys) return phys;
-        if (i < it.pages) record_at<kSitePrefix>(p, QUEST_ERR_BAD_PAGE, it.first, i);
+        if (i < pages) record_at<kSitePrefix>(p, QUEST_ERR_BAD_PAGE, job.seq, job.page0 + i);
         return 0;
       };
-      now = checked(now, j0 * PPT + lane);
-      int slot = 0;
-      uint32_t ph = 1;  // (of the phase before a slot's first: over)
-      int j = j0;
-      for (; j < j1; ++j) {
-        // (a test of the waits: the last V tile of a work item never comes)
-        if (kv && j == j1 - 1 && (p.debug_flags & QUEST_DEBUG_WITHHOLD_VALUES)) break;
-        const int at = (j - j0) * PPT & 31;
-        if (at == 0 && j > j0) {
-          now = checked(next, j * PPT + lane);
-          next = entry(j * PPT + 32 + lane);
-        }
-        if (j - j0 >= kSlots &&
-            !__all_sync(0xffffffffu, wait_at<kSitePrefix>(p, &bars.free[slot][kv], ph, give_up)))
+      int now = 0, next = 0;
+      if (job.n > 0) {
+        now = checked(entry(lane), lane);
+        if (pages > 32) next = entry(32 + lane);
+      }
+      for (int i = 0; i < job.n; ++i) {
+        // (a test of the waits: the last V tile of a job never comes)
+        if (kv && i == job.n - 1 && (p.debug_flags & QUEST_DEBUG_WITHHOLD_VALUES)) {
+          ok = false;
           break;
+        }
+        const int at = i * PPT & 31;
+        if (at == 0 && i > 0) {
+          now = checked(next, i * PPT + lane);
+          next = entry(i * PPT + 32 + lane);
+        }
+        if (total >= kSlots && !(ok = wait(&bars.free[slot][kv], ph))) break;
         const bool leader = elect_lane();
         if (leader) mbar_arrive_expect_tx(&bars.full[slot][kv], kTile);
 #pragma unroll
@@ -212,58 +279,59 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           const int phys = __shfl_sync(0xffffffffu, now, at + e);
           if (leader)
             tma_page(smem + Smem::kv + (2 * slot + kv) * kTile + e * P * kHeadDim * 2,
-                     kv ? &map_v : &map_k, (phys * p.Hkv + it.g) * (P / 8), &bars.full[slot][kv]);
+                     kv ? &map_v : &map_k, (phys * p.Hkv + job.g) * (P / 8), &bars.full[slot][kv]);
         }
         __syncwarp();
+        ++total;
         if (++slot == kSlots) {
           slot = 0;
           ph ^= 1u;
         }
       }
-      if (lane == 0) bars.fetched[kv] = j - j0;
-    } else {
-      // ---- issue
-      const uint64_t q_desc = smem_desc(smem_u32(smem + Smem::q), 16, kAtomBytes);
-      const uint64_t k_desc = smem_desc(smem_u32(smem + Smem::kv), 16, kGroupBytes);
-      const uint64_t v_desc = smem_desc(smem_u32(smem + Smem::kv + kTile), kAtomBytes, kGroupBytes);
-      constexpr uint32_t kSlotStep = 2 * kTile >> 4;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, bar, parity, give_up)) != 0;
-      };
-      auto qk = [&](int buffer, int slot) {
-        if (elect_lane()) {
+    }
+    if (lane == 0) bars.fetched[kv] = total;
+  } else if (warp == 10) {
+    // ---- issue
+    const uint64_t q_desc = smem_desc(smem_u32(smem + Smem::q), 16, kAtomBytes);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + Smem::kv), 16, kGroupBytes);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + Smem::kv + kTile), kAtomBytes, kGroupBytes);
+    constexpr uint32_t kSlotStep = 2 * kTile >> 4;
+    int ks = 0, vs = 0;  // slots of the next K and of the next V tile
+    uint32_t kph = 0, vph = 0;
+    // Q K^T of the next K tile into a buffer (whose weights P V has been given before); `last` of
+    // its job.
+    auto qk = [&](int buffer, bool last) {
+      if (!wait(&bars.full[ks][0], kph)) return false;
+      fence_after();
+      if (elect_lane()) {
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint32_t oq = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            const uint32_t ok = ((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4;
-            mma_ss(tmem + buffer * kTokens, q_desc + oq, k_desc + slot * kSlotStep + ok, kIdescQK,
-                   k > 0);
-          }
-          commit(&bars.s_full[buffer]);
-          commit(&bars.free[slot][0]);
+        for (int k = 0; k < kHeadDim / 16; ++k) {
+          const uint32_t oq = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          const uint32_t ok = ((k >> 2) * kAtomBytes + (k & 3) * 32) >> 4;
+          mma_ss(tmem + buffer * kTokens, q_desc + oq, k_desc + ks * kSlotStep + ok, kIdescQK, k > 0);
         }
-        __syncwarp();
-      };
-      int ks = 1, vs = 0;  // slots of the next K and of the V tile
-      uint32_t kph = 0, vph = 0;
-      ok = n > 0 && wait(&bars.q_full, 0) && wait(&bars.full[0][0], 0);
-      if (ok) {
-        fence_after();
-        qk(0, 0);
+        commit(&bars.s_full[buffer]);
+        commit(&bars.free[ks][0]);
+        if (last) commit(&bars.q_free);
       }
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {  // (its buffer held the weights of tile i - 1, which P V has been given)
-          if (!(ok = wait(&bars.full[ks][0], kph))) break;
-          fence_after();
-          qk((i + 1) & 1, ks);
-          if (++ks == kSlots) {
-            ks = 0;
-            kph ^= 1u;
-          }
-        }
+      __syncwarp();
+      if (++ks == kSlots) {
+        ks = 0;
+        kph ^= 1u;
+      }
+      return true;
+    };
+    Job job;
+    int t = 0, done = 0;  // tiles and jobs (with tiles) before this one
+    bool ok = true;
+    for (int k = 0; ok && take(k, job); ++k) {
+      if (job.n == 0) continue;
+      ok = wait(&bars.q_full, (uint32_t)done & 1) && qk(t & 1, job.n == 1);
+      for (int i = 0; ok && i < job.n; ++i, ++t) {
+        if (i + 1 < job.n && !(ok = qk((t + 1) & 1, i + 2 == job.n))) break;
         if (!(ok = wait(&bars.full[vs][1], vph))) break;
-        // values that no row of the CTA sees may be anything: 0 * NaN is not 0
-        const int behind = end - (j0 + i) * kTokens;
+        // values that no row of the job sees may be anything: 0 * NaN is not 0
+        const int behind = job.end - job.page0 * P - i * kTokens;
         if (behind < kTokens) {
           for (int c = behind + lane; c < kTokens; c += 32)
 #pragma unroll
@@ -274,17 +342,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!(ok = wait(&bars.p_full[i & 1], (uint32_t)(i >> 1) & 1))) break;
+        if (!(ok = wait(&bars.p_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
+        if (i == 0 && done > 0 && !(ok = wait(&bars.o_free, (uint32_t)(done - 1) & 1))) break;
         fence_after();
         if (elect_lane()) {
 #pragma unroll
           for (int k = 0; k < kTokens / 16; ++k)  // the first half's four, then the other's
             mma_ts(tmem + 256 + (k >> 2) * kHeadDim,
-                   tmem + (i & 1) * kTokens + (k >> 2) * 64 + 8 * (k & 3),
+                   tmem + (t & 1) * kTokens + (k >> 2) * 64 + 8 * (k & 3),
                    v_desc + (uint32_t)(vs * kSlotStep + k * (2 * kGroupBytes >> 4)), kIdescPV,
                    i > 0 || (k & 3) > 0);
           commit(&bars.free[vs][1]);
-          commit(i + 1 < n ? &bars.pv_done : &bars.o_full);
+          commit(&bars.pv_done);
+          if (i + 1 == job.n) commit(&bars.o_full);
         }
         __syncwarp();
         if (++vs == kSlots) {
@@ -292,206 +362,301 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           vph ^= 1u;
         }
       }
+      ++done;
     }
   } else {
     // ---- softmax: a thread a row's 64 tokens
-    // the last position that the row sees; the least of the warp's rows, which go together
-    const int pr = mine ? min(length(it.first + tok0 + (row >> lg)), end) - 1 : end - 1;
-    const int least = __reduce_min_sync(0xffffffffu, pr);
-    const bool some = __any_sync(0xffffffffu, mine);
+    const int half = warp >> 2, row = threadIdx.x & 127, G = 1 << lg;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + 64 * half, o_col = tmem + lanes + 256 + 128 * half;
-    for (int i = 0; i < n; ++i) {
-      const uint32_t phase = (uint32_t)(i >> 1) & 1;
-      ok = __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, &bars.s_full[i & 1], phase, give_up));
-      if (!ok) break;
-      if (some) {  // (without a query in the warp's rows their weights may be anything)
-        fence_after();
-        const uint32_t s_now = s_col + (i & 1) * kTokens;
-        float s[64];
-        tmem_ld32(s_now, reinterpret_cast<uint32_t*>(s));
-        tmem_ld32(s_now + 32, reinterpret_cast<uint32_t*>(s) + 32);
-        tmem_wait_ld();
-        const int base = (j0 + i) * kTokens + 64 * half;
-        if (base + 63 > least) {
+    float2* stash = reinterpret_cast<float2*>(smem + Smem::stash);  // [half][row]
+    Job job;
+    int t = 0, done = 0;
+    uint32_t pairs = 0;
+    bool ok = true;
+    for (int k = 0; ok && take(k, job); ++k) {
+      const bool mine = row < job.rows;
+      const bool some = (row & ~31) < job.rows;  // (the warp's)
+      const int pos0 = job.page0 * P;
+      // the last position that the row sees; the least of the warp's rows, which go together
+      int pr = job.end - 1;
+      if (job.shared && mine) pr = min(pr, length(job.q_tok + (row >> lg)) - 1);
+      const int least = __reduce_min_sync(0xffffffffu, pr);
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int i = 0; i < job.n; ++i, ++t) {
+        if (!(ok = wait(&bars.s_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
+        if (some) {  // (without a query in the warp's rows their weights may be anything)
+          fence_after();
+          const uint32_t s_now = s_col + (t & 1) * kTokens;
+          float s[64];
+          tmem_ld32(s_now, reinterpret_cast<uint32_t*>(s));
+          tmem_ld32(s_now + 32, reinterpret_cast<uint32_t*>(s) + 32);
+          tmem_wait_ld();
+          const int base = pos0 + i * kTokens + 64 * half;
+          if (base + 63 > least) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (base + k > pr) s[k] = -CUDART_INF_F;
-        }
-        float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            for (int e = 0; e < 64; ++e)
+              if (base + e > pr) s[e] = -CUDART_INF_F;
+          }
+          float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int k = 0; k < 64; k += 4)
+          for (int e = 0; e < 64; e += 4)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) best[e] = max3(best[e], s[k + e], s[k + 2 + e]);
-        const float top = fmaxf(best[0], best[1]) * p.qscale;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float mn = fmaxf(m, top);
-          const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (i > 0) {
-            ok = __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, &bars.pv_done, (uint32_t)(i - 1) & 1,
-                                                              give_up));
-            if (!ok) break;
-            fence_after();
+            for (int u = 0; u < 2; ++u) best[u] = max3(best[u], s[e + u], s[e + 2 + u]);
+          const float top = fmaxf(best[0], best[1]) * p.qscale;
+          // The reference moves only when a row exceeds it by 2^kLazy; the warp's rows move theirs
+          // together, l and O with them.
+          if (__any_sync(0xffffffffu, top > m + kLazy)) {
+            const float mn = fmaxf(m, top);
+            const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (i > 0) {
+              if (!(ok = wait(&bars.pv_done, (uint32_t)(t - 1) & 1))) break;
+              fence_after();
 #pragma unroll 1
-            for (int u = 0; u < 8; ++u) {
-              uint32_t o[16];
-              tmem_ld16(o_col + 16 * u, o);
-              tmem_wait_ld();
+              for (int u = 0; u < 8; ++u) {
+                uint32_t o[16];
+                tmem_ld16(o_col + 16 * u, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(o_col + 16 * u, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_col + 16 * u, o);
+              }
             }
           }
-        }
-        uint32_t w[32];
-        uint64_t sum[2] = {0, 0};
-        const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
-        const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
+          uint32_t w[32];
+          uint64_t sum[2] = {0, 0};
+          const float shift = kBias - (m == -CUDART_INF_F ? 0.f : m);
+          const uint64_t shift2 = pair(shift, shift), scale2 = pair(p.qscale, p.qscale);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
+          for (int e = 0; e < 32; ++e) {
+            float a, c;
+            unpair(fma2(pair(s[2 * e], s[2 * e + 1]), scale2, shift2), a, c);
+            a = ex2(a);
+            c = ex2(c);
+            sum[e & 1] = add2(sum[e & 1], pair(a, c));
+            w[e] = pack2(a, c);
+          }
+          tmem_st32(s_now, w);
           float a, c;
-          unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale2, shift2), a, c);
-          a = ex2(a);
-          c = ex2(c);
-          sum[k & 1] = add2(sum[k & 1], pair(a, c));
-          w[k] = pack2(a, c);
+          unpair(add2(sum[0], sum[1]), a, c);
+          l += a + c;
+          tmem_wait_st();
+          fence_before();
         }
-        tmem_st32(s_now, w);
-        float a, c;
-        unpair(add2(sum[0], sum[1]), a, c);
-        l += a + c;
-        tmem_wait_st();
-        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[t & 1]);
       }
+      if (!ok) break;
+      // ---- the rows' shares: warps 0-3 the dims 0-63, warps 4-7 the others
+      const int dim0 = 64 * half;
+      float M = -CUDART_INF_F, Z = 0.f, f0 = 0.f, f1 = 0.f;
+      if (job.n > 0) {
+        if (!(ok = wait(&bars.o_full, (uint32_t)done & 1))) break;
+        ++done;
+        fence_after();
+        if (some) {
+          // a row's halves are in warps w and w + 4
+          stash[half * kRows + row] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.pair[warp & 3]);
+          if (!(ok = wait(&bars.pair[warp & 3], pairs & 1))) break;
+          ++pairs;
+          const float2 other = stash[(half ^ 1) * kRows + row];
+          M = fmaxf(m, other.x);
+          const float fm = half_factor(m, l, M), fo = half_factor(other.x, other.y, M);
+          Z = fmaf(l, fm, other.y * fo);
+          f0 = half ? fo : fm;
+          f1 = half ? fm : fo;
+        }
+      }
+      const bool none = Z == 0.f;  // (a NaN sum is not: its NaN goes out)
+      bool odd = false;            // some of the row's O is not finite
+      const size_t slot = (size_t)job.share + row;
+      if (some) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t o[32], x[32];
+          tmem_ld32(tmem + lanes + 256 + dim0 + 32 * u, o);  // (without a tile anything: not used)
+          tmem_ld32(tmem + lanes + 384 + dim0 + 32 * u, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            o[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), f1, __uint_as_float(o[e]) * f0));
+            odd |= (o[e] & 0x7f800000u) == 0x7f800000u;
+            if (none) o[e] = 0u;  // (it may be 0 * NaN)
+          }
+          if (mine) {  // whole sectors: a lane's row is 512 B from its neighbour's
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              store8(p.part_acc + slot * kHeadDim + dim0 + 32 * u + 8 * e, o + 8 * e);
+          }
+          __syncwarp();
+        }
+        if (mine && half == 0) {
+          p.part_ml[2 * slot] = M;
+          p.part_ml[2 * slot + 1] = Z;
+        }
+      }
+      fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_full[i & 1]);
-    }
-    // the last product, and with it all (where none ran, the queries have landed)
-    if (ok)
-      ok = __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, n > 0 ? &bars.o_full : &bars.q_full, 0,
-                                                        give_up));
-    if (ok) *stash(half, row) = make_float2(m, l);
-  }
-  __syncthreads();
-  fence_after();
-  if (warp < 8 && __all_sync(0xffffffffu, ok && *give_up == 0)) {
-    // ---- the row's share: warps 0-3 the dims 0-63 of it, warps 4-7 the others
-    const float2 other = *stash(half ^ 1, row);
-    const float M = fmaxf(m, other.x);
-    const float f_mine = half_factor(m, l, M), f_other = half_factor(other.x, other.y, M);
-    const float Z = fmaf(l, f_mine, other.y * f_other);
-    const float f0 = half ? f_other : f_mine, f1 = half ? f_mine : f_other;
-    const bool none = Z == 0.f;  // (a NaN sum is not: its NaN goes out)
-    bool odd = false;            // some of the row's O is not finite
-    size_t slot;
-    item_of(table, lg, &slot);
-    slot += row;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t o[32], x[32];
-      const int dim = 64 * half + 32 * u;
-      tmem_ld32(tmem + lanes + 256 + dim, o);  // (without a tile anything: it is not used)
-      tmem_ld32(tmem + lanes + 384 + dim, x);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        o[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), f1, __uint_as_float(o[k]) * f0));
-        odd |= (o[k] & 0x7f800000u) == 0x7f800000u;
-        if (none || n == 0) o[k] = 0u;  // (it may be 0 * NaN)
+      if (job.n > 0 && lane == 0) mbar_arrive(&bars.o_free);
+      // An infinity or NaN among the values of a tile reaches all of its rows, as 0 * NaN, those too
+      // that do not see its token.  Such a row (its scores are finite, its O is not) is taken again
+      // from what it sees, by its warp, a token at a time.
+      unsigned todo = __ballot_sync(0xffffffffu, mine && odd && !none && Z <= FLT_MAX);
+      while (todo) {  // (the warp's)
+        const int from = __ffs(todo) - 1, r = (row & ~31) + from;
+        todo &= todo - 1u;
+        const float m_r = __shfl_sync(0xffffffffu, M, from);
+        const int last = __shfl_sync(0xffffffffu, pr, from) + 1;
+        const int seq = job.q_tok + (r >> lg);
+        const uint2 qw = *reinterpret_cast<const uint2*>(
+            p.q + ((size_t)seq * p.Hq + ((size_t)job.g << lg) + (r & (G - 1))) * kHeadDim + 4 * lane);
+        const float2 qa = h2f(qw.x), qb = h2f(qw.y);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int page = job.page0; page * P < last; ++page) {
+          const int phys = p.block_table[(size_t)job.seq * p.max_pages + page];
+          if (phys < 0 || phys >= p.num_phys) continue;
+          const size_t at = ((size_t)phys * p.Hkv + job.g) * P * kHeadDim + 4 * lane;
+#pragma unroll 1
+          for (int e = 0; e < min(P, last - page * P); ++e) {
+            const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + at + e * kHeadDim);
+            const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + at + e * kHeadDim);
+            const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
+            const float x = warp_sum(fmaf(qa.x, ka.x, qa.y * ka.y) + fmaf(qb.x, kb.x, qb.y * kb.y));
+            // (a visible infinity counts however small its weight: 0 * inf is not it)
+            const float w =
+                x == -CUDART_INF_F ? 0.f : fmaxf(ex2(fmaf(x, p.qscale, kBias - m_r)), FLT_MIN);
+            acc[0] = fmaf(w, va.x, acc[0]);
+            acc[1] = fmaf(w, va.y, acc[1]);
+            acc[2] = fmaf(w, vb.x, acc[2]);
+            acc[3] = fmaf(w, vb.y, acc[3]);
+          }
+        }
+        if (lane >> 4 == half)  // (the other half's warp does its dims)
+          *reinterpret_cast<float4*>(p.part_acc + ((size_t)job.share + r) * kHeadDim + 4 * lane) =
+              make_float4(acc[0], acc[1], acc[2], acc[3]);
       }
-      if (mine) {  // whole sectors: a lane's row is 512 B from its neighbour's
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          store8(p.part_acc + slot * kHeadDim + dim + 8 * e, o + 8 * e);
-      }
-      __syncwarp();
     }
-    if (mine && half == 0) {
-      p.part_ml[2 * slot] = M;
-      p.part_ml[2 * slot + 1] = Z;
-    }
-    again = mine && odd && !none && Z <= FLT_MAX;
-    // (maximum and sum of a row that has to be taken again, below; a sum < 0: it has not)
-    *stash(2 + half, row) = again ? make_float2(M, Z) : make_float2(0.f, -1.f);
   }
   fence_before();
-  bool any_again = __syncthreads_or(again);
+  __syncthreads();
   fence_after();
   if (*give_up) {  // (nobody sets it any more)
     // A wait ran out: copies and products in flight end before their memory goes.  (Otherwise the
     // results were waited for, and with them everything that went into them.)
-    any_again = false;
     if (warp == 10) {
       if (elect_lane()) commit(&bars.drain);  // the products that this thread issued
       __syncwarp();
       settle(&bars.drain, 0);
     } else if ((warp == 8 || warp == 9) && lane < kSlots) {
       // copies into slot `lane`: its phases so far
-      const int phases = (bars.fetched[warp == 9] + kSlots - 1 - lane) / kSlots;
-      if (phases > 0) settle(&bars.full[lane][warp == 9], (uint32_t)(phases - 1) & 1);
-    } else if (warp == 8 && lane == kSlots) {
-      settle(&bars.q_full, 0);
+      const int phases = (bars.fetched[warp - 8] + kSlots - 1 - lane) / kSlots;
+      if (phases > 0) settle(&bars.full[lane][warp - 8], (uint32_t)(phases - 1) & 1);
+    } else if (warp == 11 && lane == 0 && bars.q_fetched > 0) {
+      settle(&bars.q_full, (uint32_t)(bars.q_fetched - 1) & 1);
     }
     __syncthreads();
   }
   if (warp == 10) tmem_free(tmem);
+}
 
-  // An infinity or NaN among the values of a tile reaches all of its rows, as 0 * NaN, those too
-  // that do not see its token.  Such a row (its scores are finite, its O is not) is taken again
-  // from what it sees, by a warp, a token at a time.
-  if (any_again) {
-    size_t share;
-    item_of(table, lg, &share);
-    for (int r = warp; r < (tok1 - tok0) * G; r += kPrefixThreads / 32) {
-      const float2 a0 = *stash(2, r), a1 = *stash(3, r);
-      if (a0.y < 0.f && a1.y < 0.f) continue;  // warp-uniform
-      const float m_r = a0.y < 0.f ? a1.x : a0.x;
-      const int seq = it.first + tok0 + (r >> lg);
-      const int last = min(min(length(seq), end), j1 * kTokens);
-      const uint2 qw = *reinterpret_cast<const uint2*>(
-          p.q + ((size_t)seq * p.Hq + ((size_t)it.g << lg) + (r & (G - 1))) * kHeadDim + 4 * lane);
-      const float2 qa = h2f(qw.x), qb = h2f(qw.y);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int page = j0 * PPT; page * P < last; ++page) {
-        const int phys = p.block_table[(size_t)it.first * p.max_pages + page];
-        if (phys < 0 || phys >= p.num_phys) continue;
-        const size_t from = ((size_t)phys * p.Hkv + it.g) * P * kHeadDim + 4 * lane;
-#pragma unroll 4
-        for (int k = 0; k < P; ++k) {
-          if (page * P + k >= last) break;
-          const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + from + k * kHeadDim);
-          const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + from + k * kHeadDim);
-          const float2 ka = h2f(kw.x), kb = h2f(kw.y), va = h2f(vw.x), vb = h2f(vw.y);
-          const float x = warp_sum(fmaf(qa.x, ka.x, qa.y * ka.y) + fmaf(qb.x, kb.x, qb.y * kb.y));
-          // (a visible infinity counts however small its weight: 0 * inf is not it)
-          const float w =
-              x == -CUDART_INF_F ? 0.f : fmaxf(ex2(fmaf(x, p.qscale, kBias - m_r)), FLT_MIN);
-          acc[0] = fmaf(w, va.x, acc[0]);
-          acc[1] = fmaf(w, va.y, acc[1]);
-          acc[2] = fmaf(w, vb.x, acc[2]);
-          acc[3] = fmaf(w, vb.y, acc[3]);
-        }
+// The shares of a prefix and of a tail into out and lse: a warp a row (sequence, query head), lane l
+// the dims 4 l .. 4 l + 3, kTogether shares on their way together.  First come the prefix's splits
+// (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, G apart).
+constexpr int kPrefixJoinThreads = 128;
+__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
+    const __grid_constant__ Params p, const __grid_constant__ PrefixTable t) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
+  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
+  const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
+  if (at >= p.B * p.Hq) return;  // (the warp's)
+  const int h = at % p.Hq, b = at / p.Hq, g = h / G;
+  const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
+  const int shared = q.pages > 0 ? q.splits : 0, n = shared + p.n_splits;
+  size_t slot0 = 0, step = 0;  // of the prefix's
+  if (shared) {
+    const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
+    const int blocks = (rows + kPrefixRows - 1) / kPrefixRows;
+    const int r = (b - q.first) * G + h % G;
+    slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPrefixRows) * part_rows + r % kPrefixRows;
+    step = (size_t)blocks * part_rows;
+  }
+  const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * p.n_splits * G + h % G;
+  auto slot = [&](int s) {
+    return s < shared ? slot0 + s * step : tail0 + (size_t)(s - shared) * G;
+  };
+  constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
+  float f[kOf], Z = 0.f, M = -CUDART_INF_F;
+  {
+    float2 ml[kOf];
+#pragma unroll
+    for (int e = 0; e < kOf; ++e) {
+      const int s = lane + 32 * e;
+      ml[e] = s < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s))
+                    : make_float2(-CUDART_INF_F, 0.f);
+      M = fmaxf(M, ml[e].x);
+    }
+    M = warp_max(M);
+#pragma unroll
+    for (int e = 0; e < kOf; ++e) {
+      f[e] = half_factor(ml[e].x, ml[e].y, M);
+      Z = fmaf(ml[e].y, f[e], Z);
+    }
+    Z = warp_sum(Z);
+  }
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kTogether = 8;
+#pragma unroll
+  for (int e = 0; e < kOf; ++e) {
+    for (int s0 = 32 * e; s0 < min(n, 32 * e + 32); s0 += kTogether) {
+      float4 a[kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i)
+        a[i] = s0 + i < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s0 + i) * kHeadDim) + lane)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f[e], (s0 + i) & 31);
+        A.x = fmaf(a[i].x, w, A.x);
+        A.y = fmaf(a[i].y, w, A.y);
+        A.z = fmaf(a[i].z, w, A.z);
+        A.w = fmaf(a[i].w, w, A.w);
       }
-      *reinterpret_cast<float4*>(p.part_acc + (share + r) * kHeadDim + 4 * lane) =
-          make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
   }
+  const bool none = Z == 0.f;
+  const float inv = none ? 0.f : 1.f / Z;
+  reinterpret_cast<uint2*>(p.out + (size_t)at * kHeadDim)[lane] =
+      none ? make_uint2(0u, 0u)
+           : make_uint2(pack2(A.x * inv, A.y * inv), pack2(A.z * inv, A.w * inv));
+  if (lane == 0 && p.lse)
+    p.lse[at] = none ? -CUDART_INF_F : (M - kBias + log2f(Z)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s) {
-  Params pp = p;
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, cudaStream_t s) {
+  PrefixParams pp{};
+  pp.p = p;
+  pp.p.n_splits = splits;
   const int G = p.Hq / p.Hkv;
-  int log_g = G == 8 ? 3 : G / 2;
-  CUtensorMap mq, mk, mv;
+  pp.log_g = G == 8 ? 3 : G / 2;
+  pp.splits = splits;
+  pp.jobs = t.ctas + p.B * p.Hkv * splits;
+  CUtensorMap mq, m1, mk, mv;
   const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B};
   const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
   const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G)};
+  const cuuint32_t q1[3] = {64, (cuuint32_t)G, 1};
   cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
   if (e != cudaSuccess) return e;
+  if ((e = make_map(&m1, p.q, 3, qd, qs, q1)) != cudaSuccess) return e;
   // a pool as [8-row group][half of the dims][row][64 dims]
   const cuuint64_t kd[4] = {64, 8, 2, (cuuint64_t)p.num_phys * p.Hkv * (p.P / 8)};
   const cuuint64_t ks[3] = {kHeadDim * 2, kHeadDim, 8 * kHeadDim * 2};
@@ -499,10 +664,15 @@ cudaError_t launch_prefix(const Params& p, const PrefixTable& t, cudaStream_t s)
   if ((e = make_map(&mk, p.k_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
   if ((e = make_map(&mv, p.v_pool, 4, kd, ks, kb)) != cudaSuccess) return e;
   const void* fn = p.P == 16 ? (const void*)prefix_kernel<16> : (const void*)prefix_kernel<32>;
-  const size_t smem = Smem::total + 1024;
-  if ((e = ensure_smem(fn, smem)) != cudaSuccess) return e;
-  void* args[] = {&pp, const_cast<PrefixTable*>(&t), &log_g, &mq, &mk, &mv};
-  return launch_pdl(fn, dim3((unsigned)t.ctas), dim3(kPrefixThreads), smem, s, args);
+  if ((e = ensure_smem(fn, Smem::total)) != cudaSuccess) return e;
+  void* args[] = {&pp, const_cast<PrefixTable*>(&t), &mq, &m1, &mk, &mv};
+  e = launch_pdl(fn, dim3((unsigned)std::min(pp.jobs, kPrefixSms)), dim3(kPrefixThreads), Smem::total, s,
+                 args);
+  if (e != cudaSuccess) return e;
+  void* join_args[] = {&pp.p, const_cast<PrefixTable*>(&t)};
+  constexpr int per = kPrefixJoinThreads / 32;
+  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * p.Hq + per - 1) / per)),
+                    dim3(kPrefixJoinThreads), 0, s, join_args);
 }
 
 }  // namespace quest

@@ -163,12 +163,10 @@ int check_groups(const quest_cache_t& c, const quest_prefix_group_t* groups, int
 
 // Whether sharing pays: below this many bytes of keys and values that sequences would read again.
 constexpr long long kShareBytes = 0;
-constexpr int kPrefixCtas = 152;      // CTAs of the prefixes' launch that run at once
-constexpr int kPrefixSplits = 64;     // of a prefix
-constexpr int kPrefixStart = 3;       // what a CTA's start and end cost, in tiles
+constexpr int kPrefixStart = 3;  // what a job's start and end cost, in tiles
 
-// How the launch over prefixes is cut.  Its CTAs take `per` K / V tiles each, so that they fill
-// their places once, or twice, ..., whichever takes the fewest tiles one after another.
+// How the prefixes are cut.  A job takes `per` K / V tiles, so that the jobs fill the SMs once, or
+// twice, ..., whichever takes the fewest tiles one after another.
 PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* groups, int n,
                        const quest_opts_t* o) {
   PrefixTable t{};
@@ -209,10 +207,10 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
       int lo = least, hi = most;  // the fewest tiles a CTA with that many waves (hi: all of them)
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (ctas(mid) <= (long long)waves * kPrefixCtas) hi = mid;
+        if (ctas(mid) <= (long long)waves * kPrefixSms) hi = mid;
         else lo = mid + 1;
       }
-      const long long cost = (ctas(lo) + kPrefixCtas - 1) / kPrefixCtas * (lo + kPrefixStart);
+      const long long cost = (ctas(lo) + kPrefixSms - 1) / kPrefixSms * (lo + kPrefixStart);
       if (best == 0 || cost < best) {
         best = cost;
         per = lo;
@@ -232,6 +230,16 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
     t.most_pages = std::max(t.most_pages, c.max_pages - g.pages);
   }
   return t;
+}
+
+// Jobs of a tail: six tiles each where it fills its table row, ten jobs an SM at most.
+int tail_splits(const quest_cache_t& c, const PrefixTable& t, const quest_opts_t* o) {
+  const int user = user_split(o);
+  const long long tiles = ((long long)t.most_pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
+  const long long rows = (long long)c.batch * c.num_kv_heads;
+  const long long n = user ? (t.most_pages + user - 1) / user
+                           : std::min((tiles + 5) / 6, std::max(1LL, 10 * kPrefixSms / rows));
+  return (int)std::max(1LL, std::min<long long>(n, kPrefixSplits));
 }
 
 // One span-decode launch over rows of at most `pages` pages.
@@ -424,11 +432,7 @@ size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefi
   if (cache->batch == 0) return span_layout(*cache, 0, opts).total;
   if (check_groups(*cache, groups, n_groups)) return 0;
   const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
-  Params p{};
-  p.B = cache->batch;
-  p.Hkv = cache->num_kv_heads;
-  p.P = cache->page_size;
-  const size_t tails = (size_t)cache->batch * cache->num_q_heads * tail_splits(p, t, user_split(opts));
+  const size_t tails = (size_t)cache->batch * cache->num_q_heads * tail_splits(*cache, t, opts);
   return span_layout(*cache, 0, opts, 1, t.parts + tails).total;
 }
 
@@ -442,10 +446,7 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q,
   if ((rc = check_io(q, out, lse))) return rc;
   const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
   SpanParams sp{};
-  sp.p.B = cache->batch;
-  sp.p.Hkv = cache->num_kv_heads;
-  sp.p.P = cache->page_size;
-  const int splits = tail_splits(sp.p, t, user_split(opts));
+  const int splits = tail_splits(*cache, t, opts);
   const size_t tails = (size_t)cache->batch * cache->num_q_heads * splits;
   const SpanLayout L = span_layout(*cache, 0, opts, 1, t.parts + tails);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
@@ -459,11 +460,8 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q,
   sp.p.lse = lse;
   if (opts && opts->wait_limit_ns > 0) sp.p.wait_limit_ns = opts->wait_limit_ns;
   if (opts) sp.p.debug_flags = opts->debug_flags;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_prefix(sp.p, t, s);
-  if (e == cudaSuccess) e = launch_tail(sp.p, t, splits, s);
-  if (e == cudaSuccess) e = launch_prefix_join(sp.p, t, splits, s);
-  return launched(e, "quest_prefix_decode");
+  return launched(launch_prefix(sp.p, t, splits, static_cast<cudaStream_t>(stream)),
+                  "quest_prefix_decode");
 }
 
 int quest_narrow_window_decode(const quest_narrow_cache_t* cache, const void* q,

@@ -354,9 +354,7 @@ struct RowShape {
   int L, N, n_sink, first, count;
 };
 
-// With a table of shared prefixes, those behind its group's prefix.
-__device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b,
-                                              const PrefixTable* tails = nullptr) {
+__device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b) {
   const Params& p = sp.p;
   RowShape x;
   x.L = step_len(p, b, p.seq_lens[b], kSiteSpan);
@@ -364,11 +362,6 @@ __device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b,
   x.vis = Visible{x.L, 0, 0};
   x.n_sink = x.first = 0;
   x.count = x.N;
-  if (tails) {
-    x.first = tails->group[tails->group_of_seq(b)].pages;
-    x.count = max(0, x.N - x.first);
-    return x;
-  }
   if (sp.mode == kSpanWindow) {
     x.vis.lo = max(0, x.L - sp.window);
     x.vis.sink_end = min(sp.sink, x.vis.lo);
@@ -389,12 +382,11 @@ __device__ __forceinline__ RowShape row_shape(const SpanParams& sp, int b,
 template <bool N8, int kSpanWarps>
 __device__ __forceinline__ void take_again(const SpanParams& sp, int row, int split,
                                            const int* list, int count,
-                                           const float (&s_m)[kSpanWarps][8], float* red,
-                                           const PrefixTable* tails = nullptr) {
+                                           const float (&s_m)[kSpanWarps][8], float* red) {
   const Params& p = sp.p;
   const int b = row / p.Hkv, g = row % p.Hkv, G = p.Hq / p.Hkv, P = p.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowShape x = row_shape(sp, b, tails);
+  const RowShape x = row_shape(sp, b);
   if (sp.mode == kSpanList) count = max(0, min(count, x.count));
   else count = x.count;
   const int i1 = count * (split + 1) / p.n_splits;
@@ -455,20 +447,15 @@ __device__ __forceinline__ void take_again(const SpanParams& sp, int row, int sp
 // the shared memory of a cluster (the row's CTAs), or by the CTA that comes last to the row.
 // kSelect (a chain step without a top-K kernel): every CTA of a row takes the row's selection from
 // the scores itself, the same in each; split 0 also writes the caller's copy.
-// kTail (sp.mode is kSpanWindow): the pages behind the prefix that a sequence's group shares; every
-// CTA leaves a part, which another kernel joins with the prefix's.  The launch follows the prefix's,
-// and starts with it: only CTA 0 waits for that one, at its end, so that no later launch runs before
-// both are done.  (What it reads was there before: the prefix's CTAs let it start after their own
-// wait.)
-template <bool N8, int kSpanWarps, int kDepth, bool kSelect, bool kTail>
-__device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTable* tails) {
+template <bool N8, int kSpanWarps, int kCtas, int kDepth, bool kSelect>
+__global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams sp) {
   constexpr int kSpanThreads = 32 * kSpanWarps;
   __shared__ float s_m[kSpanWarps][8], s_l[kSpanWarps][8];
   __shared__ __align__(16) float s_red[kSpanWarps][8 * kHeadDim];
   __shared__ float s_part[2][8];  // a part's maxima and sums, for the cluster
   __shared__ int s_flag;
   const Params& p = sp.p;
-  if (!kTail || tails->ctas == 0) pdl_wait();
+  pdl_wait();
   pdl_trigger();  // the next call's CTAs may take the places that this one's free
   const int split = (int)(blockIdx.x % (unsigned)p.n_splits);
   const int row = (int)(blockIdx.x / (unsigned)p.n_splits);  // b * Hkv + g
@@ -476,7 +463,7 @@ __device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTabl
   const int G = p.Hq / p.Hkv, P = p.P;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 
-  const RowShape shape = row_shape(sp, b, tails);
+  const RowShape shape = row_shape(sp, b);
   const int L = shape.L, N = shape.N, n_sink = shape.n_sink, first = shape.first;
   const Visible vis = shape.vis;
   int count = shape.count;
@@ -665,8 +652,7 @@ __device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTabl
     }
   }
   __syncthreads();
-  // parts: [row][split][head]
-  const size_t slot0 = (size_t)row * p.n_splits * G + (kTail ? tails->parts : 0);
+  const size_t slot0 = (size_t)row * p.n_splits * G;  // parts: [row][split][head]
   const size_t mine = slot0 + (size_t)split * G;
   for (int pass = 0;; ++pass) {
     bool odd = false;  // (found on the sums: a check of every warp's O cost the e4m3 rows 2 %)
@@ -681,10 +667,10 @@ __device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTabl
         Z = fmaf(s_l[w][h], part_factor(s_m[w][h], s_l[w][h], M), Z);
       }
       odd |= !(fabsf(A) <= FLT_MAX) && Z <= FLT_MAX;
-      if (!kTail && p.n_splits == 1) {
+      if (p.n_splits == 1) {
         p.out[(head0 + h) * kHeadDim + d] = row_out(A, Z);
         if (d == 0 && p.lse) p.lse[head0 + h] = row_lse(M, Z);
-      } else if (!kTail && sp.cluster) {
+      } else if (sp.cluster) {
         s_red[0][o] = A;  // (this thread's alone to read and write)
         if (d == 0) {
           s_part[0][h] = M;
@@ -708,12 +694,8 @@ __device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTabl
     } else if (sp.mode == kSpanList) {
       given = p.sel_count[row];
     }
-    take_again<N8, kSpanWarps>(sp, row, split, list, given, s_m, s_red[warp], tails);
+    take_again<N8, kSpanWarps>(sp, row, split, list, given, s_m, s_red[warp]);
     __syncthreads();
-  }
-  if constexpr (kTail) {
-    if (blockIdx.x == 0) pdl_wait();
-    return;
   }
   if (p.n_splits > 1 && sp.cluster) {
     // ---- every CTA of the row (rank = split) joins its share of the outputs
@@ -824,88 +806,6 @@ __device__ __forceinline__ void span_body(const SpanParams& sp, const PrefixTabl
   }
 }
 
-template <bool N8, int kSpanWarps, int kCtas, int kDepth, bool kSelect>
-__global__ void __launch_bounds__(32 * kSpanWarps, kCtas) span_kernel(SpanParams sp) {
-  span_body<N8, kSpanWarps, kDepth, kSelect, false>(sp, nullptr);
-}
-template <int kSpanWarps, int kCtas, int kDepth>
-__global__ void __launch_bounds__(32 * kSpanWarps, kCtas)
-    tail_kernel(const __grid_constant__ SpanParams sp, const __grid_constant__ PrefixTable tails) {
-  span_body<false, kSpanWarps, kDepth, false, true>(sp, &tails);
-}
-
-// The shares of a prefix and of a tail into out and lse: a warp a row (sequence, query head), lane l
-// the dims 4 l .. 4 l + 3, kTogether shares on their way together.  First come the prefix's splits
-// (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, G apart).
-constexpr int kPrefixJoinThreads = 128;
-__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
-    const __grid_constant__ Params p, const __grid_constant__ PrefixTable t) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
-  const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
-  if (at >= p.B * p.Hq) return;  // (the warp's)
-  const int h = at % p.Hq, b = at / p.Hq, g = h / G;
-  const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
-  const int shared = q.pages > 0 ? q.splits : 0, n = shared + p.n_splits;
-  size_t slot0 = 0, step = 0;  // of the prefix's
-  if (shared) {
-    const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
-    const int blocks = (rows + kPrefixRows - 1) / kPrefixRows;
-    const int r = (b - q.first) * G + h % G;
-    slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPrefixRows) * part_rows + r % kPrefixRows;
-    step = (size_t)blocks * part_rows;
-  }
-  const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * p.n_splits * G + h % G;
-  auto slot = [&](int s) {
-    return s < shared ? slot0 + s * step : tail0 + (size_t)(s - shared) * G;
-  };
-  constexpr int kOf = 2 * kMaxSplitsSpan / 32;  // shares of a lane
-  float f[kOf], Z = 0.f, M = -CUDART_INF_F;
-  {
-    float2 ml[kOf];
-#pragma unroll
-    for (int e = 0; e < kOf; ++e) {
-      const int s = lane + 32 * e;
-      ml[e] = s < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s))
-                    : make_float2(-CUDART_INF_F, 0.f);
-      M = fmaxf(M, ml[e].x);
-    }
-    M = warp_max(M);
-#pragma unroll
-    for (int e = 0; e < kOf; ++e) {
-      f[e] = part_factor(ml[e].x, ml[e].y, M);
-      Z = fmaf(ml[e].y, f[e], Z);
-    }
-    Z = warp_sum(Z);
-  }
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kTogether = 8;
-#pragma unroll
-  for (int e = 0; e < kOf; ++e) {
-    for (int s0 = 32 * e; s0 < min(n, 32 * e + 32); s0 += kTogether) {
-      float4 a[kTogether];
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i)
-        a[i] = s0 + i < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s0 + i) * kHeadDim) + lane)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kTogether; ++i) {
-        const float w = __shfl_sync(0xffffffffu, f[e], (s0 + i) & 31);
-        A.x = fmaf(a[i].x, w, A.x);
-        A.y = fmaf(a[i].y, w, A.y);
-        A.z = fmaf(a[i].z, w, A.z);
-        A.w = fmaf(a[i].w, w, A.w);
-      }
-    }
-  }
-  const __half2 lo = __halves2half2(row_out(A.x, Z), row_out(A.y, Z));
-  const __half2 hi = __halves2half2(row_out(A.z, Z), row_out(A.w, Z));
-  reinterpret_cast<uint2*>(p.out + (size_t)at * kHeadDim)[lane] = make_uint2(
-      *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (lane == 0 && p.lse) p.lse[at] = row_lse(M, Z);
-}
-
 }  // namespace
 
 // Launch shapes: warps of a CTA, CTAs that an SM holds, blocks in flight a warp.  A narrow
@@ -990,35 +890,6 @@ cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream
   const cudaError_t e = ensure_smem(fn, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(fn, grid, block, smem, s, args, together);
-}
-
-// ---- attention over shared prefixes
-int tail_splits(const Params& p, const PrefixTable& t, int user_pps) {
-  SpanParams sp{};
-  sp.p = p;
-  sp.run_pages = user_pps;
-  return span_splits(sp, span_shape(false, (long long)p.B * p.Hkv), t.most_pages).n;
-}
-
-cudaError_t launch_tail(const Params& p, const PrefixTable& t, int splits, cudaStream_t s) {
-  SpanParams sp{};
-  sp.p = p;
-  sp.p.n_splits = splits;
-  sp.mode = kSpanWindow;
-  const long long rows = (long long)p.B * p.Hkv;
-  const bool many = rows > kSms;  // (as for the span decode's own launches)
-  const void* fn = many ? (const void*)tail_kernel<4, 2, 2> : (const void*)tail_kernel<8, 1, 2>;
-  void* args[] = {&sp, const_cast<PrefixTable*>(&t)};
-  return launch_pdl(fn, dim3((unsigned)(rows * splits)), dim3(many ? 128 : 256), 0, s, args);
-}
-
-cudaError_t launch_prefix_join(const Params& p, const PrefixTable& t, int splits, cudaStream_t s) {
-  Params pp = p;
-  pp.n_splits = splits;
-  void* args[] = {&pp, const_cast<PrefixTable*>(&t)};
-  constexpr int per = kPrefixJoinThreads / 32;
-  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * p.Hq + per - 1) / per)),
-                    dim3(kPrefixJoinThreads), 0, s, args);
 }
 
 }  // namespace quest
