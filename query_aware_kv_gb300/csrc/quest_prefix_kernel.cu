@@ -17,8 +17,8 @@
 // TMEM), so that the halves never wait for one another; they are added at a job's end, in registers.
 // Scores have two buffers in TMEM: Q K^T of tile t + 1 runs while tile t is in its softmax, P V
 // while tile t + 1 is.  Warps 8 and 9 fetch K and V (a page a TMA box, three tiles of each in
-// flight, over the ends of jobs), warp 10 issues the products, warp 11 takes jobs from the queue and
-// fetches their queries.
+// flight, over the ends of jobs), warp 10 issues the products, warp 11 takes jobs from the queue, one
+// ahead, warp 12 fetches their queries.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -31,7 +31,7 @@ namespace quest {
 
 namespace {
 
-constexpr int kPrefixThreads = 384;
+constexpr int kPrefixThreads = 416;
 constexpr int kRows = kPrefixRows, kTokens = kPrefixTokens;
 constexpr int kTile = kTokens * kHeadDim * 2;  // 32 KiB
 constexpr int kHalf = kTile / 2;  // 64 dims of every row: one 128-byte swizzle span
@@ -92,9 +92,39 @@ constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kRow
 struct PrefixParams {
   Params p;      // exited: the queue's counter
   int log_g;
-  int splits;    // jobs of a tail
-  int jobs;
+  int splits;       // jobs of a tail, at most
+  int piece_pages;  // pages of such a job, where splits allow it
 };
+
+// What a sequence of length L has behind its group's prefix: pages, and the jobs they are cut into.
+struct Tail {
+  int pages, jobs;
+};
+__device__ __forceinline__ Tail tail_of(const PrefixParams& pp, int first, int L) {
+  Tail t;
+  t.pages = max(0, (L + pp.p.P - 1) / pp.p.P - first);
+  t.jobs = min(pp.splits, max(1, (t.pages + pp.piece_pages - 1) / pp.piece_pages));
+  return t;
+}
+
+// Job c of the prefixes: of a group's jobs the row blocks vary fastest (those that read the same
+// tiles run side by side), then the splits, then the kv heads.
+struct Cut {
+  int group, at, blk, page0, page1;
+};
+template <int PPT>
+__device__ __forceinline__ Cut cut_of(const PrefixTable& t, int lg, int c) {
+  Cut x;
+  x.group = t.group_of_cta(c);
+  const PrefixTable::Group& q = t.group[x.group];
+  const int blocks = ((q.count << lg) + kRows - 1) / kRows;
+  x.at = c - q.cta0;
+  x.blk = x.at % blocks;
+  const int split = x.at / blocks % q.splits, tiles = (q.pages + PPT - 1) / PPT;
+  x.page0 = tiles * split / q.splits * PPT;
+  x.page1 = min(tiles * (split + 1) / q.splits * PPT, q.pages);
+  return x;
+}
 
 // What brings a half's part of a softmax to the maximum M of both (as part_factor of the span
 // decode: a part without a weight is 0, one of NaN scores goes on, an infinite O stays one).
@@ -131,7 +161,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i], 8);
       mbar_init(&bars.job_full[i], 1);
-      mbar_init(&bars.job_free[i], 11);
+      mbar_init(&bars.job_free[i], 12);
     }
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_full, 1);
@@ -171,48 +201,79 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (!wait(&bars.job_full[k & 1], (uint32_t)(k >> 1) & 1)) return false;
     job = bars.job[k & 1];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.job_free[k & 1]);
     return job.n >= 0;
+  };
+  // The softmax warps give a job's description back when they are done with the job, so that the
+  // queue is not emptied ahead of the work, the others once they have read it.
+  auto give_back = [&](int k) {
+    if (lane == 0) mbar_arrive(&bars.job_free[k & 1]);
   };
 
   if (warp == 11) {
-    // ---- jobs and their queries
-    int index = (int)blockIdx.x, k = 0, loads = 0;
-    while (true) {
+    // ---- jobs
+    const int sequences = p.B;
+    int index = (int)blockIdx.x;
+    // 32 sequences at a time, a sequence a lane: its tail's jobs (of all kv heads), the sum up to it;
+    // `base`: the index of the first one's first job
+    int b0 = -32, base = table.ctas, chunk = 0, sum = 0, first = 0;
+    Tail tail{0, 0};
+    int L = 0;
+    for (int k = 0;; ++k) {
       Job job{-1, 0, 0, 0, 0, 0, 0, 0, 0};
       int next = 0;
-      if (index < pp.jobs) {
-        if (lane == 0) next = (int)(gridDim.x + atomicAdd(p.exited, 1u));
-        if (index < table.ctas) {
-          const PrefixTable::Group& q = table.group[table.group_of_cta(index)];
-          const int rows = q.count << lg, blocks = (rows + kRows - 1) / kRows, at = index - q.cta0;
-          const int blk = at % blocks, split = at / blocks % q.splits;
-          const int tok0 = blk * (kRows >> lg), tok1 = min(q.count, tok0 + (kRows >> lg));
-          const int tiles = (q.pages + PPT - 1) / PPT;
-          const int j0 = tiles * split / q.splits, j1 = tiles * (split + 1) / q.splits;
-          int most = 0;  // the longest of the rows' sequences
-          for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(q.first + i));
-          job.shared = 1;
-          job.seq = q.first;
-          job.g = at / blocks / q.splits;
-          job.page0 = j0 * PPT;
-          job.end = min(__reduce_max_sync(0xffffffffu, most), min(j1 * PPT, q.pages) * P);
-          job.q_tok = q.first + tok0;
-          job.rows = (tok1 - tok0) << lg;
-          job.share = q.part0 + at * min(rows, kRows);
-        } else {
-          const int t = index - table.ctas, split = t % pp.splits, row = t / pp.splits;
-          job.seq = job.q_tok = row / p.Hkv;
-          job.g = row % p.Hkv;
-          const int first = table.group[table.group_of_seq(job.seq)].pages;
-          const int L = length(job.seq), count = max(0, (L + P - 1) / P - first);
-          job.page0 = first + (int)((long long)count * split / pp.splits);
-          job.end = min(L, (first + (int)((long long)count * (split + 1) / pp.splits)) * P);
-          job.rows = 1 << lg;
-          job.share = table.parts + (t << lg);
+      if (lane == 0) next = (int)(gridDim.x + atomicAdd(p.exited, 1u));
+      if (index < table.ctas) {
+        const Cut x = cut_of<PPT>(table, lg, index);
+        const PrefixTable::Group& q = table.group[x.group];
+        const int tok0 = x.blk * (kRows >> lg), tok1 = min(q.count, tok0 + (kRows >> lg));
+        int most = 0;  // the longest of the rows' sequences
+        for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(q.first + i));
+        job.shared = 1;
+        job.seq = q.first;
+        job.g = x.at / (((q.count << lg) + kRows - 1) / kRows) / q.splits;
+        job.page0 = x.page0;
+        job.end = min(__reduce_max_sync(0xffffffffu, most), x.page1 * P);
+        job.q_tok = q.first + tok0;
+        job.rows = (tok1 - tok0) << lg;
+        job.share = q.part0 + x.at * min(q.count << lg, kRows);
+        job.n = 0;
+      } else {
+        while (index >= base + chunk && b0 + 32 < sequences) {
+          base += chunk;
+          b0 += 32;
+          const int b = b0 + lane;
+          int mine = 0;
+          if (b < sequences) {
+            L = length(b);
+            first = table.group[table.group_of_seq(b)].pages;
+            tail = tail_of(pp, first, L);
+            mine = tail.jobs * p.Hkv;
+          }
+          sum = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+          }
+          chunk = __shfl_sync(0xffffffffu, sum, 31);
         }
-        job.n = max(0, job.end - job.page0 * P + kTokens - 1) / kTokens;
+        if (index < base + chunk) {
+          const int at = __ffs(__ballot_sync(0xffffffffu, index - base < sum)) - 1;
+          const int jobs = __shfl_sync(0xffffffffu, tail.jobs, at);
+          const int pages = __shfl_sync(0xffffffffu, tail.pages, at);
+          const int start = __shfl_sync(0xffffffffu, first, at);
+          const int local = index - base - __shfl_sync(0xffffffffu, sum, at) + jobs * p.Hkv;
+          const int split = local / p.Hkv;
+          job.seq = job.q_tok = b0 + at;
+          job.g = local % p.Hkv;
+          job.page0 = start + pages * split / jobs;
+          job.end = min(__shfl_sync(0xffffffffu, L, at), (start + pages * (split + 1) / jobs) * P);
+          job.rows = 1 << lg;
+          job.share = table.parts + (((job.seq * p.Hkv + job.g) * pp.splits + split) << lg);
+          job.n = 0;
+        }
       }
+      if (job.n == 0) job.n = max(0, job.end - job.page0 * P + kTokens - 1) / kTokens;
       if (k >= 2 && !wait(&bars.job_free[k & 1], (uint32_t)((k >> 1) - 1) & 1)) break;
       if (lane == 0) {
         bars.job[k & 1] = job;
@@ -220,20 +281,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       }
       __syncwarp();
       if (job.n < 0) break;
-      if (job.n > 0) {
-        if (loads > 0 && !wait(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
-        if (elect_lane()) {
-          // of a tail only its own G rows: the others' scores may be anything
-          mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : (kHeadDim * 2) << lg);
-          for (int i = 0; i < 2; ++i)
-            tma_3d(smem + Smem::q + i * kHalf, job.shared ? &map_q : &map_1, 64 * i, job.g << lg,
-                   job.q_tok, &bars.q_full);
-        }
-        __syncwarp();
-        ++loads;
-      }
       index = __shfl_sync(0xffffffffu, next, 0);
-      ++k;
+    }
+  } else if (warp == 12) {
+    // ---- queries
+    Job job;
+    int loads = 0;
+    for (int k = 0; take(k, job); ++k) {
+      give_back(k);
+      if (job.n == 0) continue;
+      if (loads > 0 && !wait(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
+      if (elect_lane()) {
+        // of a tail only its own G rows: the others' scores may be anything
+        mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : (kHeadDim * 2) << lg);
+        for (int i = 0; i < 2; ++i)
+          tma_3d(smem + Smem::q + i * kHalf, job.shared ? &map_q : &map_1, 64 * i, job.g << lg,
+                 job.q_tok, &bars.q_full);
+      }
+      __syncwarp();
+      ++loads;
     }
     if (lane == 0) bars.q_fetched = loads;
   } else if (warp >= 8 && warp < 10) {
@@ -243,7 +309,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     int slot = 0, total = 0;
     uint32_t ph = 1;  // (of the phase before a slot's first: over)
     bool ok = true;
+    // the first job's pages are looked up beside its lengths
+    int early = 0;
+    if ((int)blockIdx.x < table.ctas) {
+      const Cut x = cut_of<PPT>(table, lg, (int)blockIdx.x);
+      early = p.block_table[(size_t)table.group[x.group].first * p.max_pages +
+                            min(x.page0 + lane, table.group[x.group].pages - 1)];
+    }
     for (int k = 0; ok && take(k, job); ++k) {
+      give_back(k);
       // Pages, 32 at a time, a page per lane, the next 32 on their way; entries behind the job's
       // end repeat its last page (its tokens are hidden there).
       const int pages = (job.end + P - 1) / P - job.page0;
@@ -257,7 +331,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       };
       int now = 0, next = 0;
       if (job.n > 0) {
-        now = checked(entry(lane), lane);
+        now = checked(k == 0 && job.shared ? early : entry(lane), lane);
         if (pages > 32) next = entry(32 + lane);
       }
       for (int i = 0; i < job.n; ++i) {
@@ -325,6 +399,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     int t = 0, done = 0;  // tiles and jobs (with tiles) before this one
     bool ok = true;
     for (int k = 0; ok && take(k, job); ++k) {
+      give_back(k);
       if (job.n == 0) continue;
       ok = wait(&bars.q_full, (uint32_t)done & 1) && qk(t & 1, job.n == 1);
       for (int i = 0; ok && i < job.n; ++i, ++t) {
@@ -540,6 +615,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           *reinterpret_cast<float4*>(p.part_acc + ((size_t)job.share + r) * kHeadDim + 4 * lane) =
               make_float4(acc[0], acc[1], acc[2], acc[3]);
       }
+      give_back(k);
     }
   }
   fence_before();
@@ -556,7 +632,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       // copies into slot `lane`: its phases so far
       const int phases = (bars.fetched[warp - 8] + kSlots - 1 - lane) / kSlots;
       if (phases > 0) settle(&bars.full[lane][warp - 8], (uint32_t)(phases - 1) & 1);
-    } else if (warp == 11 && lane == 0 && bars.q_fetched > 0) {
+    } else if (warp == 12 && lane == 0 && bars.q_fetched > 0) {
       settle(&bars.q_full, (uint32_t)(bars.q_fetched - 1) & 1);
     }
     __syncthreads();
@@ -569,16 +645,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 // (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, G apart).
 constexpr int kPrefixJoinThreads = 128;
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
-    const __grid_constant__ Params p, const __grid_constant__ PrefixTable t) {
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
+    const __grid_constant__ PrefixParams pp, const __grid_constant__ PrefixTable t) {
+  const Params& p = pp.p;
   const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
   const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
-  if (at >= p.B * p.Hq) return;  // (the warp's)
-  const int h = at % p.Hq, b = at / p.Hq, g = h / G;
+  const int h = at % p.Hq, b = min(at / p.Hq, p.B - 1), g = h / G;
   const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
-  const int shared = q.pages > 0 ? q.splits : 0, n = shared + p.n_splits;
+  // (where things are is worked out before the wait; the lengths are older than the jobs' launch,
+  // which waited for whatever wrote them before it let this one start)
+  const int L = p.seq_lens[b];
+  const bool known = L >= 0 && (long long)L <= (long long)p.max_pages * p.P;
+  const int shared = q.pages > 0 ? q.splits : 0, n = shared + tail_of(pp, q.pages, known ? L : 0).jobs;
   size_t slot0 = 0, step = 0;  // of the prefix's
   if (shared) {
     const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
@@ -587,10 +664,14 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
     slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPrefixRows) * part_rows + r % kPrefixRows;
     step = (size_t)blocks * part_rows;
   }
-  const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * p.n_splits * G + h % G;
+  const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * pp.splits * G + h % G;
   auto slot = [&](int s) {
     return s < shared ? slot0 + s * step : tail0 + (size_t)(s - shared) * G;
   };
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
+  if (at >= p.B * p.Hq) return;  // (the warp's)
   constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
   float f[kOf], Z = 0.f, M = -CUDART_INF_F;
   {
@@ -641,14 +722,14 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
 
 }  // namespace
 
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, cudaStream_t s) {
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, int piece_pages,
+                          cudaStream_t s) {
   PrefixParams pp{};
   pp.p = p;
-  pp.p.n_splits = splits;
   const int G = p.Hq / p.Hkv;
   pp.log_g = G == 8 ? 3 : G / 2;
   pp.splits = splits;
-  pp.jobs = t.ctas + p.B * p.Hkv * splits;
+  pp.piece_pages = piece_pages;
   CUtensorMap mq, m1, mk, mv;
   const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B};
   const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
@@ -666,10 +747,10 @@ cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, cud
   const void* fn = p.P == 16 ? (const void*)prefix_kernel<16> : (const void*)prefix_kernel<32>;
   if ((e = ensure_smem(fn, Smem::total)) != cudaSuccess) return e;
   void* args[] = {&pp, const_cast<PrefixTable*>(&t), &mq, &m1, &mk, &mv};
-  e = launch_pdl(fn, dim3((unsigned)std::min(pp.jobs, kPrefixSms)), dim3(kPrefixThreads), Smem::total, s,
+  e = launch_pdl(fn, dim3((unsigned)std::min(t.ctas + (long long)p.B * p.Hkv * splits, (long long)kPrefixSms)), dim3(kPrefixThreads), Smem::total, s,
                  args);
   if (e != cudaSuccess) return e;
-  void* join_args[] = {&pp.p, const_cast<PrefixTable*>(&t)};
+  void* join_args[] = {&pp, const_cast<PrefixTable*>(&t)};
   constexpr int per = kPrefixJoinThreads / 32;
   return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * p.Hq + per - 1) / per)),
                     dim3(kPrefixJoinThreads), 0, s, join_args);

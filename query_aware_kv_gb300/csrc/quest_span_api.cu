@@ -232,13 +232,17 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   return t;
 }
 
-// Jobs of a tail: six tiles each where it fills its table row, ten jobs an SM at most.
-int tail_splits(const quest_cache_t& c, const PrefixTable& t, const quest_opts_t* o) {
+// Jobs of a tail: six tiles each.  How many there can be is bound by the table's rows, and to ten
+// jobs an SM where every row is as long (then they are longer).
+int tail_piece(const quest_cache_t& c, const quest_opts_t* o) {
   const int user = user_split(o);
-  const long long tiles = ((long long)t.most_pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
+  return user ? user : 6 * kPrefixTokens / c.page_size;
+}
+int tail_splits(const quest_cache_t& c, const PrefixTable& t, const quest_opts_t* o) {
   const long long rows = (long long)c.batch * c.num_kv_heads;
-  const long long n = user ? (t.most_pages + user - 1) / user
-                           : std::min((tiles + 5) / 6, std::max(1LL, 10 * kPrefixSms / rows));
+  const int piece = tail_piece(c, o);
+  long long n = (t.most_pages + piece - 1) / piece;
+  if (!user_split(o)) n = std::min(n, 10 * kPrefixSms / rows);
   return (int)std::max(1LL, std::min<long long>(n, kPrefixSplits));
 }
 
@@ -460,7 +464,8 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q,
   sp.p.lse = lse;
   if (opts && opts->wait_limit_ns > 0) sp.p.wait_limit_ns = opts->wait_limit_ns;
   if (opts) sp.p.debug_flags = opts->debug_flags;
-  return launched(launch_prefix(sp.p, t, splits, static_cast<cudaStream_t>(stream)),
+  return launched(launch_prefix(sp.p, t, splits, tail_piece(*cache, opts),
+                                static_cast<cudaStream_t>(stream)),
                   "quest_prefix_decode");
 }
 
