@@ -18,7 +18,7 @@
 // Scores have two buffers in TMEM: Q K^T of tile t + 1 runs while tile t is in its softmax, P V
 // while tile t + 1 is.  Warps 8 and 9 fetch K and V (a page a TMA box, three tiles of each in
 // flight, over the ends of jobs), warp 10 issues the products, warp 11 takes jobs from the queue, one
-// ahead, warp 12 fetches their queries.
+// ahead of the fetches, warp 12 fetches their queries.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -62,6 +62,7 @@ struct Bars {
   uint64_t pv_done;
   uint64_t o_full, o_free;             // a job's O: complete; read
   uint64_t job_full[2], job_free[2];   // a job's description: written; read by every warp
+  uint64_t want;                       // a job's K tiles have been asked for: the next may be taken
   uint64_t pair[4];                    // a row's halves have left their maxima and sums
   uint64_t drain;
   Job job[2];
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_init(&bars.job_full[i], 1);
       mbar_init(&bars.job_free[i], 12);
     }
+    mbar_init(&bars.want, 1);
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_full, 1);
     mbar_init(&bars.o_free, 8);
@@ -203,8 +205,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncwarp();
     return job.n >= 0;
   };
-  // The softmax warps give a job's description back when they are done with the job, so that the
-  // queue is not emptied ahead of the work, the others once they have read it.
+  // The softmax warps give a job's description back when they are done with the job, the others once
+  // they have read it.
   auto give_back = [&](int k) {
     if (lane == 0) mbar_arrive(&bars.job_free[k & 1]);
   };
@@ -220,8 +222,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     int L = 0;
     for (int k = 0;; ++k) {
       Job job{-1, 0, 0, 0, 0, 0, 0, 0, 0};
-      int next = 0;
-      if (lane == 0) next = (int)(gridDim.x + atomicAdd(p.exited, 1u));
+      if (k > 0) {
+        // not before this CTA's fetches are through with the job before: taken any earlier (all
+        // CTAs took their first three at the start) the jobs were dealt out, not queued for
+        if (!wait(&bars.want, (uint32_t)(k - 1) & 1)) break;
+        if (lane == 0) index = (int)(gridDim.x + atomicAdd(p.exited, 1u));
+        index = __shfl_sync(0xffffffffu, index, 0);
+      }
       if (index < table.ctas) {
         const Cut x = cut_of<PPT>(table, lg, index);
         const PrefixTable::Group& q = table.group[x.group];
@@ -281,7 +288,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       }
       __syncwarp();
       if (job.n < 0) break;
-      index = __shfl_sync(0xffffffffu, next, 0);
     }
   } else if (warp == 12) {
     // ---- queries
@@ -362,6 +368,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           ph ^= 1u;
         }
       }
+      if (kv == 0 && lane == 0) mbar_arrive(&bars.want);
     }
     if (lane == 0) bars.fetched[kv] = total;
   } else if (warp == 10) {
@@ -641,7 +648,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 }
 
 // The shares of a prefix and of a tail into out and lse: a warp a row (sequence, query head), lane l
-// the dims 4 l .. 4 l + 3, kTogether shares on their way together.  First come the prefix's splits
+// the dims 4 l .. 4 l + 3.  First come the prefix's splits
 // (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, G apart).
 constexpr int kPrefixJoinThreads = 128;
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
@@ -673,34 +680,38 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
   if (at >= p.B * p.Hq) return;  // (the warp's)
   constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
-  float f[kOf], Z = 0.f, M = -CUDART_INF_F;
-  {
-    float2 ml[kOf];
-#pragma unroll
-    for (int e = 0; e < kOf; ++e) {
-      const int s = lane + 32 * e;
-      ml[e] = s < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s))
-                    : make_float2(-CUDART_INF_F, 0.f);
-      M = fmaxf(M, ml[e].x);
-    }
-    M = warp_max(M);
-#pragma unroll
-    for (int e = 0; e < kOf; ++e) {
-      f[e] = half_factor(ml[e].x, ml[e].y, M);
-      Z = fmaf(ml[e].y, f[e], Z);
-    }
-    Z = warp_sum(Z);
-  }
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kTogether = 8;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto share = [&](int s) {
+    return s < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s) * kHeadDim) + lane)
+                 : zero;
+  };
+  // the maxima and sums of all shares and the first shares themselves are on their way together
+  float2 ml[kOf];
 #pragma unroll
   for (int e = 0; e < kOf; ++e) {
-    for (int s0 = 32 * e; s0 < min(n, 32 * e + 32); s0 += kTogether) {
-      float4 a[kTogether];
+    const int s = lane + 32 * e;
+    ml[e] = s < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s))
+                  : make_float2(-CUDART_INF_F, 0.f);
+  }
+  float4 a[kTogether];
 #pragma unroll
-      for (int i = 0; i < kTogether; ++i)
-        a[i] = s0 + i < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s0 + i) * kHeadDim) + lane)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kTogether; ++i) a[i] = share(i);
+  float f[kOf], Z = 0.f, M = -CUDART_INF_F;
+#pragma unroll
+  for (int e = 0; e < kOf; ++e) M = fmaxf(M, ml[e].x);
+  M = warp_max(M);
+#pragma unroll
+  for (int e = 0; e < kOf; ++e) {
+    f[e] = half_factor(ml[e].x, ml[e].y, M);
+    Z = fmaf(ml[e].y, f[e], Z);
+  }
+  Z = warp_sum(Z);
+  float4 A = zero;
+#pragma unroll
+  for (int e = 0; e < kOf; ++e) {  // (share s has its factor in lane s % 32's f[s / 32])
+#pragma unroll 1
+    for (int s0 = 32 * e; s0 < min(n, 32 * e + 32); s0 += kTogether) {
 #pragma unroll
       for (int i = 0; i < kTogether; ++i) {
         const float w = __shfl_sync(0xffffffffu, f[e], (s0 + i) & 31);
@@ -708,6 +719,7 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
         A.y = fmaf(a[i].y, w, A.y);
         A.z = fmaf(a[i].z, w, A.z);
         A.w = fmaf(a[i].w, w, A.w);
+        a[i] = share(s0 + kTogether + i);
       }
     }
   }

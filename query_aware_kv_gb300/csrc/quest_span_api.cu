@@ -163,6 +163,7 @@ int check_groups(const quest_cache_t& c, const quest_prefix_group_t* groups, int
 
 // Whether sharing pays: below this many bytes of keys and values that sequences would read again.
 constexpr long long kShareBytes = 0;
+constexpr int kPrefixJobs = 96;  // of the prefixes, in one go
 constexpr int kPrefixStart = 3;  // what a job's start and end cost, in tiles
 
 // How the prefixes are cut.  A job takes `per` K / V tiles, so that the jobs fill the SMs once, or
@@ -207,10 +208,10 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
       int lo = least, hi = most;  // the fewest tiles a CTA with that many waves (hi: all of them)
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
-        if (ctas(mid) <= (long long)waves * kPrefixSms) hi = mid;
+        if (ctas(mid) <= (long long)waves * kPrefixJobs) hi = mid;
         else lo = mid + 1;
       }
-      const long long cost = (ctas(lo) + kPrefixSms - 1) / kPrefixSms * (lo + kPrefixStart);
+      const long long cost = (ctas(lo) + kPrefixJobs - 1) / kPrefixJobs * (lo + kPrefixStart);
       if (best == 0 || cost < best) {
         best = cost;
         per = lo;
