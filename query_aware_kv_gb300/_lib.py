@@ -988,32 +988,47 @@ class RotaryPlan:
         self._fn = _rotary_fn(cache)
         self._io = QuestRotaryIo(n_tokens=1, q_out=q_out.data_ptr(),
                                  position_offsets=_ptr(offsets))
+        # the descriptor's words: q, k, v, then the strides of each (setting a word of an array is
+        # cheaper than setting a field)
+        self._words = (ctypes.c_uint64 * 9).from_buffer(self._io)
+        self._batch, self._dtype = B, None
         self._args = (ctypes.byref(cache.desc), rope.ref, ctypes.byref(self._io), ws.data_ptr(),
                       ws.numel(), _stream(stream))
+
+    def _refuse(self, q, k_new, v_new):
+        for name, t, shape in (("q", q, self._qshape), ("k_new", k_new, self._kvshape),
+                               ("v_new", v_new, self._kvshape)):
+            _heads(t, name, shape)
+            if t.dtype not in (torch.float16, torch.bfloat16):
+                raise TypeError("q, k_new and v_new must be float16 or bfloat16")
+            if t.dtype != q.dtype:
+                raise TypeError("q, k_new and v_new must be of one type")
+            if t.get_device() != self._dev:
+                raise ValueError("q / k_new / v_new are on another device than the cache")
 
     def append(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor) -> torch.Tensor:
         """Write (k_new, v_new) with the key turned; returns the turned queries."""
         if self._many and _current_device() != self._dev:
             _not_current()
-        io, dtype = self._io, q.dtype
-        for name, t, shape in (("q", q, self._qshape), ("k", k_new, self._kvshape),
-                               ("v", v_new, self._kvshape)):
-            s = t.stride()
-            if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and
-                    t.get_device() == self._dev and s[2] == 1 and (s[1] == HEAD_DIM or shape[1] == 1)):
-                _heads(t, name, shape)
-                if t.dtype != dtype:
-                    raise TypeError("q, k_new and v_new must be of one type")
-                if t.get_device() != self._dev:
-                    raise ValueError("q / k_new / v_new are on another device than the cache")
-            setattr(io, name, t.data_ptr())
-            getattr(io, name + "_stride")[0] = s[0] if shape[0] > 1 else 0
-        if dtype is torch.float16:
-            io.dtype = 0
-        elif dtype is torch.bfloat16:
-            io.dtype = 1
-        else:
-            raise TypeError("q, k_new and v_new must be float16 or bfloat16")
+        w, dev, kv = self._words, self._dev, self._kvshape
+        dtype = q.dtype
+        if not (type(q) is torch.Tensor and type(k_new) is torch.Tensor and
+                type(v_new) is torch.Tensor and k_new.dtype is dtype and v_new.dtype is dtype and
+                (dtype is torch.float16 or dtype is torch.bfloat16) and q.shape == self._qshape and
+                k_new.shape == kv and v_new.shape == kv and q.get_device() == dev and
+                k_new.get_device() == dev and v_new.get_device() == dev):
+            self._refuse(q, k_new, v_new)
+        sq, sk, sv = q.stride(), k_new.stride(), v_new.stride()
+        if not (sq[2] == 1 and sk[2] == 1 and sv[2] == 1 and
+                (sq[1] == HEAD_DIM or self._qshape[1] == 1) and
+                ((sk[1] == HEAD_DIM and sv[1] == HEAD_DIM) or kv[1] == 1)):
+            self._refuse(q, k_new, v_new)
+        w[0], w[1], w[2] = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr()
+        if self._batch > 1:
+            w[3], w[5], w[7] = sq[0], sk[0], sv[0]
+        if dtype is not self._dtype:
+            self._io.dtype = _DTYPES[dtype]
+            self._dtype = dtype
         rc = self._fn(*self._args)
         if rc:
             _check(rc)

@@ -658,11 +658,7 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
   const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
   const int h = at % p.Hq, b = min(at / p.Hq, p.B - 1), g = h / G;
   const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
-  // (where things are is worked out before the wait; the lengths are older than the jobs' launch,
-  // which waited for whatever wrote them before it let this one start)
-  const int L = p.seq_lens[b];
-  const bool known = L >= 0 && (long long)L <= (long long)p.max_pages * p.P;
-  const int shared = q.pages > 0 ? q.splits : 0, n = shared + tail_of(pp, q.pages, known ? L : 0).jobs;
+  const int shared = q.pages > 0 ? q.splits : 0;
   size_t slot0 = 0, step = 0;  // of the prefix's
   if (shared) {
     const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
@@ -679,24 +675,34 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
   if (at >= p.B * p.Hq) return;  // (the warp's)
+  const int L = __ldcg(p.seq_lens + b);
+  const bool known = L >= 0 && (long long)L <= (long long)p.max_pages * p.P;
   constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
   constexpr int kTogether = 8;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto share = [&](int s) {
-    return s < n ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s) * kHeadDim) + lane)
-                 : zero;
+  auto load = [&](int s) {
+    return __ldcg(reinterpret_cast<const float4*>(p.part_acc + slot(s) * kHeadDim) + lane);
   };
-  // the maxima and sums of all shares and the first shares themselves are on their way together
+  auto load_ml = [&](int s) { return __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s)); };
+  // The prefix's shares and the tail's first, which every row has, are on their way beside the
+  // length, which says how many more the tail has.
   float2 ml[kOf];
 #pragma unroll
-  for (int e = 0; e < kOf; ++e) {
-    const int s = lane + 32 * e;
-    ml[e] = s < n ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot(s))
-                  : make_float2(-CUDART_INF_F, 0.f);
-  }
+  for (int e = 0; e < kOf; ++e)
+    ml[e] = lane + 32 * e <= shared ? load_ml(lane + 32 * e) : make_float2(-CUDART_INF_F, 0.f);
   float4 a[kTogether];
 #pragma unroll
-  for (int i = 0; i < kTogether; ++i) a[i] = share(i);
+  for (int i = 0; i < kTogether; ++i) a[i] = i <= shared ? load(i) : zero;
+  const int n = shared + tail_of(pp, q.pages, known ? L : 0).jobs;
+  auto share = [&](int s) { return s < n ? load(s) : zero; };
+  if (n > shared + 1) {
+#pragma unroll
+    for (int e = 0; e < kOf; ++e)
+      if (lane + 32 * e > shared && lane + 32 * e < n) ml[e] = load_ml(lane + 32 * e);
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+      if (i > shared) a[i] = share(i);
+  }
   float f[kOf], Z = 0.f, M = -CUDART_INF_F;
 #pragma unroll
   for (int e = 0; e < kOf; ++e) M = fmaxf(M, ml[e].x);

@@ -8,8 +8,8 @@
 //
 // Angles: f_i comes as a fraction of a turn in 2^-64 units, so t f_i mod 1 is one 64-bit integer
 // product whose overflow drops the whole turns exactly, at any 32-bit position.  Its upper 32
-// bits (an angle within 2^-32 of a turn, 1.5e-9) go through sincospif; the turn itself is in
-// fp32, rounded once to the output's type.
+// bits (an angle within 2^-32 of a turn, 1.5e-9) lose their quarter turns, the rest goes through
+// polynomials; the turn itself is in fp32, rounded once to the output's type.
 //
 // Bound by DRAM: a value costs its read and its write, and 3 flops.  A half-warp takes a row of
 // 128 dims, lane c two pieces of 4 dims whose four pairs are whole within the lane for either
@@ -63,11 +63,26 @@ template <> struct Four<float> {
 // ---- the turn of a position
 __device__ __forceinline__ void cos_sin(uint64_t turns, long long pos, float m, float& c, float& s) {
   // (a product modulo 2^64 is the same for signed and unsigned factors)
-  const uint64_t at = turns * (uint64_t)pos;
-  const float half_turns = (float)(int)(uint32_t)(at >> 32) * 4.656612873077393e-10f;  // 2^-31
-  sincospif(half_turns, &s, &c);
-  c *= m;
-  s *= m;
+  const uint32_t at = (uint32_t)(turns * (uint64_t)pos >> 32);
+  // the nearest quarter turn and the rest, within an eighth of a turn, which keeps fp32's relative
+  // precision (of the whole angle as one fp32 number, 2^-25 of half a turn would be lost)
+  const uint32_t quarter = at + 0x20000000u >> 30;
+  const float rest = (float)(int)(at - (quarter << 30)) * 4.656612873077393e-10f;  // 2^-31
+  // sin(pi r) / r and (cos(pi r) - 1) / r^2 as polynomials in r^2, interpolated at the Chebyshev
+  // nodes of [0, 1/16]: with fp32 sums within 9e-8 of the sine and 6e-8 of the cosine for |r| <= 1/4.
+  // (sincospif, which reduces its argument once more, made a block's table its longest part.)
+  const float u = rest * rest;
+  float a = fmaf(0x1.4bc85cp-4f, u, -0x1.32ca9ep-1f);
+  a = fmaf(a, u, 0x1.466bbap+1f);
+  a = fmaf(a, u, -0x1.4abbcep+2f);
+  a = fmaf(a, u, 0x1.921fb6p+1f) * rest;
+  float b = fmaf(0x1.db6492p-3f, u, -0x1.55cb98p+0f);
+  b = fmaf(b, u, 0x1.03c1eap+2f);
+  b = fmaf(b, u, -0x1.3bd3ccp+2f);
+  b = fmaf(b, u, 1.f);
+  const float x = quarter & 1u ? a : b, y = quarter & 1u ? b : a;
+  c = (quarter + 1u & 2u ? -x : x) * m;
+  s = (quarter & 2u ? -y : y) * m;
 }
 
 // Lane c's two pieces (offsets in dims), and whether they are turned.
@@ -142,6 +157,17 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(
   const T* x = static_cast<const T*>(r.x) + t * r.x_stride;
   T* out = static_cast<T*>(r.out) + t * r.out_stride;
   const int pos = r.positions[t];
+  constexpr int R = 4;  // rows on their way together
+  raw p[R], z[R];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const T* row = x + (size_t)min(h + i, h1 - 1) * kHeadDim;
+      p[i] = *reinterpret_cast<const raw*>(row + at.a);
+      z[i] = *reinterpret_cast<const raw*>(row + at.b);
+    }
+  };
+  load(h0);  // (beside the position and its cosines)
   float2 cs[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -149,16 +175,9 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(
     if (at.turned) cos_sin(r.rope.turns[4 * c + i], pos, r.rope.magnitude, cs[i].x, cs[i].y);
     if (r.transposed) cs[i].y = -cs[i].y;
   }
-  constexpr int R = 4;  // rows on their way together
 #pragma unroll 1
   for (int h = h0; h < h1; h += R) {
-    raw p[R], z[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const T* row = x + (size_t)min(h + i, h1 - 1) * kHeadDim;
-      p[i] = *reinterpret_cast<const raw*>(row + at.a);
-      z[i] = *reinterpret_cast<const raw*>(row + at.b);
-    }
+    if (h > h0) load(h);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (h + i >= h1) break;
@@ -351,7 +370,10 @@ __device__ __forceinline__ void copy_rows(const T* in, long long in_tok, __half*
 // block (x, j, b) has logical page L / P + j of sequence b.  In the first columns warp w writes
 // the page's new tokens of kv head 4x + w (keys turned, values, box); in the others it turns two
 // query heads of the same tokens.  The block's cosines and sines are a table in shared memory: a
-// position's 64 pairs are taken once for its four (eight) heads.
+// position's 64 pairs are taken once for its four (eight) heads.  (Blocks of a head a
+// warp, or of eight warps, fill more tables and more waves: 519 tokens of four sequences into a
+// narrow cache took 18 and 19 us instead of 14.)
+// Measured: 32K tokens of 32 query and 32 kv heads 250 us (1.64 GB, 6.6 TB/s).
 template <class T, int P>
 __device__ __forceinline__ void queries(const WriteParams& w, int b, int h0, int t0, int t1, int L,
                                         const Pieces& at, const float2 (*table)[64], int lane) {
@@ -472,106 +494,87 @@ __device__ __forceinline__ void turn_page(const WriteParams& w, int b, int g, in
   store_box(p, box, at, b, g, page, s0 > 0, hw);
 }
 
-// The complete pages of a chunk, and all of its queries; grid as above.
+// A chunk into a narrow cache; grid as above.  The blocks of the first page also write what the chunk
+// leaves in the open page: they alone read its old rows, which the page that the chunk completes
+// takes first.  A chunk that does not fit, or that meets an unmapped page, leaves the open page and
+// its box alone (the launch that advances the lengths finds the same).
+//
+// Registers are bounded for warps' sake: 32K tokens of 32 kv heads take 163 us so at page size 16
+// (169 at the compiler's 96 registers) and 176 at 32, whose warps hold 32 rows; blocks of eight
+// warps, four for the keys and four for the values, took 177 and 211.  (Without the turn 134 and 141:
+// the rest is its instructions, between the loads of a page and its stores.)
 template <class T, int P>
-__global__ void __launch_bounds__(kWriteThreads) rotary_pages_kernel(
+__global__ void __launch_bounds__(kWriteThreads, P == 16 ? 7 : 4) rotary_pages_kernel(
     const __grid_constant__ WriteParams w) {
   __shared__ __align__(16) float2 table[P][64];
   pdl_wait();
-  pdl_trigger();
   const Params& p = w.p;
   const int b = blockIdx.z, n = w.n;
   const int kv_blocks = (p.Hkv + kWriteWarps - 1) / kWriteWarps;
   const int L = p.seq_lens[b];
-  if (L < 0 || (long long)L + n > (long long)p.max_pages * P) return;  // the open kernel reports
+  if (L < 0 || (long long)L + n > (long long)p.max_pages * P) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+      report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);
+    return;
+  }
   const int page = L / P + (int)blockIdx.y;
   const int t0 = max(page * P, L), t1 = min(page * P + P, L + n);
   const bool for_q = (int)blockIdx.x >= kv_blocks;
-  if (t0 >= t1 || (!for_q && t1 < page * P + P)) return;  // (the block's)
+  const bool whole = t1 == page * P + P;
+  const int e = blockIdx.y == 0 && !for_q ? (L + n) % P : 0;  // rows that the chunk leaves open
+  if (t0 >= t1 || (!for_q && !whole && e == 0)) return;  // (the block's)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  fill_table<kWriteThreads>(w.rope, (long long)t0 + (w.offsets ? w.offsets[b] : 0), t1 - t0, table);
-  __syncthreads();
+  const long long shift = w.offsets ? w.offsets[b] : 0;
   const Pieces at = pieces(w.rope, lane & 15);
+  if (for_q || whole) fill_table<kWriteThreads>(w.rope, t0 + shift, t1 - t0, table);
+  __syncthreads();
   if (for_q) {
     queries<T, P>(w, b, ((int)blockIdx.x - kv_blocks) * kQHeads + 2 * warp, t0, t1, L, at, table,
                   lane);
     return;
   }
-  const int g = (int)blockIdx.x * kWriteWarps + warp;
-  if (g >= p.Hkv) return;
-  const int phys = p.block_table[(size_t)b * p.max_pages + page];
-  if (phys < 0 || phys >= p.num_phys) return;
-  const int s0 = t0 - page * P;
-  // the open page becomes complete: not where the chunk meets an unmapped page
-  if (blockIdx.y == 0 && s0 > 0) {
+  const int g = (int)blockIdx.x * kWriteWarps + warp, s0 = t0 - page * P;
+  bool bad = false;
+  if (e > 0 || (blockIdx.y == 0 && s0 > 0)) {  // the open page: every touched page has to be mapped
     const int last = (L + n - 1) / P;
-    bool bad = false;
 #pragma unroll 8
     for (int pg = page + lane; pg <= last; pg += 32) {
       const int entry = p.block_table[(size_t)b * p.max_pages + pg];
       bad |= entry < 0 || entry >= p.num_phys;
     }
-    if (__any_sync(0xffffffffu, bad)) return;
+    bad = __any_sync(0xffffffffu, bad);
   }
-  turn_page<T, P>(w, b, g, page, phys, s0,
-                  static_cast<const T*>(w.k) + b * w.k_seq + (t0 - L) * w.k_tok + g * kHeadDim,
-                  static_cast<const T*>(w.v) + b * w.v_seq + (t0 - L) * w.v_tok + g * kHeadDim, at,
-                  table, lane);
-}
-
-// What a chunk leaves in the open page of a narrow cache, then the lengths: grid (ceil(Hkv / 4),
-// B).  A chunk that does not fit, or that meets an unmapped page, leaves the open page and the
-// length alone; the last block of a sequence advances its length.
-template <class T, int P>
-__global__ void __launch_bounds__(kWriteThreads) rotary_open_kernel(
-    const __grid_constant__ WriteParams w) {
-  __shared__ __align__(16) float2 table[P][64];
-  __shared__ int s_flag;
-  pdl_wait();  // before any read: the lengths and the table may be an earlier call's work
-  const Params& p = w.p;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, n = w.n;
-  const int g = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
-  const int L = p.seq_lens[b];
-  const bool fits = L >= 0 && (long long)L + n <= (long long)p.max_pages * P;
-  int bad = -1;  // a touched page that is not mapped
-  if (fits) {
-    const int last = (L + n - 1) / P;
-    const int* entries = p.block_table + (size_t)b * p.max_pages;
-    for (int pg = L / P + (int)threadIdx.x; pg <= last; pg += 8 * kWriteThreads) {
-      int phys[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) phys[i] = entries[min(pg + i * kWriteThreads, last)];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (phys[i] < 0 || phys[i] >= p.num_phys) bad = min(pg + i * kWriteThreads, last);
-    }
-    if (bad >= 0 && blockIdx.x == 0) report(p, QUEST_ERR_BAD_PAGE, b, bad, kSiteAppend);
-  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
-    report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);
+  if (whole && g < p.Hkv) {
+    const int phys = p.block_table[(size_t)b * p.max_pages + page];
+    const bool mapped = phys >= 0 && phys < p.num_phys;
+    if (!mapped && g == 0 && lane == 0) report(p, QUEST_ERR_BAD_PAGE, b, page, kSiteAppend);
+    if (mapped && !(bad && s0 > 0))
+      turn_page<T, P>(w, b, g, page, phys, s0,
+                      static_cast<const T*>(w.k) + b * w.k_seq + (t0 - L) * w.k_tok + g * kHeadDim,
+                      static_cast<const T*>(w.v) + b * w.v_seq + (t0 - L) * w.v_tok + g * kHeadDim,
+                      at, table, lane);
   }
-  const bool ok = fits && !__syncthreads_or(bad >= 0);
-  const int e = ok ? (L + n) % P : 0;
-  if (e > 0) {  // (the block's)
-    const int page = (L + n) / P, t0 = max(page * P, L), s0 = t0 - page * P;
-    fill_table<kWriteThreads>(w.rope, (long long)t0 + (w.offsets ? w.offsets[b] : 0), e - s0, table);
-    __syncthreads();
-    if (g < p.Hkv) {
-      const Pieces at = pieces(w.rope, lane & 15);
-      const size_t to = (((size_t)b * p.Hkv + g) * P + s0) * kHeadDim;
-      PieceBox box;
-      clear(box);
-      turn_rows<T, true>(static_cast<const T*>(w.k) + b * w.k_seq + (t0 - L) * w.k_tok + g * kHeadDim,
-                         w.k_tok, w.nar.k_open + to, kHeadDim, e - s0, at, w.rope.interleaved != 0,
-                         table, lane, box);
-      copy_rows<T>(static_cast<const T*>(w.v) + b * w.v_seq + (t0 - L) * w.v_tok + g * kHeadDim,
-                   w.v_tok, w.nar.v_open + to, e - s0, lane);
-      store_box(p, box, at, b, g, page, s0 > 0, lane >> 4);
-    }
+  if (e == 0) return;  // (the block's)
+  const int open = (L + n) / P, o0 = max(open * P, L), r0 = o0 - open * P;
+  __syncthreads();  // the table, and the open page's old rows, have been read
+  fill_table<kWriteThreads>(w.rope, o0 + shift, e - r0, table);
+  __syncthreads();
+  if (g >= p.Hkv) return;
+  if (bad) {
+    const int phys = p.block_table[(size_t)b * p.max_pages + open];
+    if ((phys < 0 || phys >= p.num_phys) && g == 0 && lane == 0)
+      report(p, QUEST_ERR_BAD_PAGE, b, open, kSiteAppend);
+    return;
   }
-  if (arrive_last<kWriteThreads, false>(&p.seq_done[b], gridDim.x, &s_flag) && threadIdx.x == 0) {
-    p.seq_done[b] = 0u;
-    if (ok) p.seq_lens[b] = L + n;
-  }
+  const size_t to = (((size_t)b * p.Hkv + g) * P + r0) * kHeadDim;
+  PieceBox box;
+  clear(box);
+  turn_rows<T, true>(static_cast<const T*>(w.k) + b * w.k_seq + (o0 - L) * w.k_tok + g * kHeadDim,
+                     w.k_tok, w.nar.k_open + to, kHeadDim, e - r0, at, w.rope.interleaved != 0, table,
+                     lane, box);
+  copy_rows<T>(static_cast<const T*>(w.v) + b * w.v_seq + (o0 - L) * w.v_tok + g * kHeadDim, w.v_tok,
+               w.nar.v_open + to, e - r0, lane);
+  store_box(p, box, at, b, g, open, r0 > 0, lane >> 4);
 }
 
 // ---- one token per sequence: a block per sequence, a half-warp a row (keys with their boxes,
@@ -583,82 +586,98 @@ template <class T, int P, bool kNarrow>
 __global__ void __launch_bounds__(kAppendThreads) rotary_append_kernel(
     const __grid_constant__ WriteParams w) {
   __shared__ __align__(16) float2 table[1][64];
-  __shared__ int s_len, s_phys;
-  pdl_wait();
-  pdl_trigger();  // the decode that follows may start its prologue
   const Params& p = w.p;
-  const int b = blockIdx.x;
-  if (threadIdx.x == 0) {
-    int L = p.seq_lens[b], phys = -1;
-    if (L < 0 || (long long)L + 1 > (long long)p.max_pages * P) {
-      report(p, QUEST_ERR_BAD_LENGTH, b, -1, kSiteAppend);
-      L = -1;
-    } else {
-      phys = p.block_table[(size_t)b * p.max_pages + L / P];
-      if (phys < 0 || phys >= p.num_phys) {
-        report(p, QUEST_ERR_BAD_PAGE, b, L / P, kSiteAppend);
-        L = -1;
-      }
-    }
-    s_len = L;
-    s_phys = phys;
-  }
-  __syncthreads();
-  const int L = s_len, phys = s_phys;
-  if (L < 0) return;  // block-uniform
-  fill_table<kAppendThreads>(w.rope, (long long)L + (w.offsets ? w.offsets[b] : 0), 1, table);
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 15;
-  const int slot = L % P, page = L / P;
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 15;
   const bool inter = w.rope.interleaved != 0;
   const Pieces at = pieces(w.rope, c);
+  pdl_wait();
+  pdl_trigger();  // the decode that follows may start its prologue
   const T* k = static_cast<const T*>(w.k) + b * w.k_seq;
   const T* v = static_cast<const T*>(w.v) + b * w.v_seq;
+  // A half-warp's row u: a key, a value, or a query; the first is on its way beside the length, the
+  // length beside the table entry, and every thread looks both up itself: nobody waits for a barrier.
+  const int kv = 2 * p.Hkv, rows = kv + (w.q ? p.Hq : 0);
+  auto source = [&](int u) {
+    return u < p.Hkv ? k + u * kHeadDim
+           : u < kv  ? v + (u - p.Hkv) * kHeadDim
+                     : static_cast<const T*>(w.q) + b * w.q_seq + (u - kv) * kHeadDim;
+  };
+  uint2 x = make_uint2(0u, 0u), z = x;
+  auto load = [&](int u) {
+    x = *reinterpret_cast<const uint2*>(source(u) + at.a);
+    z = *reinterpret_cast<const uint2*>(source(u) + at.b);
+  };
+  int u = threadIdx.x >> 4;
+  if (u < rows) load(u);
+  const int L = p.seq_lens[b];
+  const int offset = w.offsets ? w.offsets[b] : 0;
+  const bool fits = L >= 0 && (long long)L + 1 <= (long long)p.max_pages * P;
+  const int page = fits ? L / P : 0, slot = fits ? L % P : 0;
+  const int phys = p.block_table[(size_t)b * p.max_pages + page];
+  const bool mapped = phys >= 0 && phys < p.num_phys;
+  if (!fits || !mapped) {  // (the block's)
+    if (threadIdx.x == 0)
+      report(p, fits ? QUEST_ERR_BAD_PAGE : QUEST_ERR_BAD_LENGTH, b, fits ? page : -1, kSiteAppend);
+    return;
+  }
   const bool whole = kNarrow && slot == P - 1;
   if constexpr (kNarrow) {
-    if (whole)
+    if (whole) {
+      fill_table<kAppendThreads>(w.rope, (long long)L + offset, 1, table);
+      __syncthreads();
       for (int g = warp; g < p.Hkv; g += kAppendThreads / 32)
         turn_page<T, P>(w, b, g, page, phys, slot, k + g * kHeadDim, v + g * kHeadDim, at, table, lane);
-  }
-  const int kv = whole ? 0 : 2 * p.Hkv, rows = kv + (w.q ? p.Hq : 0);
-  for (int u = threadIdx.x >> 4; u < rows; u += kAppendThreads / 16) {
-    const bool is_k = u < kv / 2, is_v = !is_k && u < kv;
-    const int h = is_k ? u : is_v ? u - kv / 2 : u - kv;
-    const size_t at_kv = kNarrow ? (((size_t)b * p.Hkv + h) * P + slot) * kHeadDim
-                                 : (((size_t)phys * p.Hkv + h) * P + slot) * kHeadDim;
-    if (is_v) {
-      __half* to = (kNarrow ? w.nar.v_open : p.v_pool) + at_kv + 8 * c;
-      *reinterpret_cast<uint4*>(to) =
-          to_half8<T>(*reinterpret_cast<const uint4*>(v + h * kHeadDim + 8 * c));
-      continue;
     }
-    const T* from = is_k ? k + h * kHeadDim
-                         : static_cast<const T*>(w.q) + b * w.q_seq + h * kHeadDim;
-    uint2 x = *reinterpret_cast<const uint2*>(from + at.a);
-    uint2 z = *reinterpret_cast<const uint2*>(from + at.b);
-    turn_row<T>(at, inter, &table[0][4 * c], x, z);
-    __half* to = is_k ? (kNarrow ? w.nar.k_open : p.k_pool) + at_kv
-                      : w.q_out + ((size_t)b * p.Hq + h) * kHeadDim;
-    *reinterpret_cast<uint2*>(to + at.a) = x;
-    *reinterpret_cast<uint2*>(to + at.b) = z;
-    if (is_k) {
-      __half* box = p.meta + box_offset(p, b, h, page);
+  }
+  float2 cs[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // (minimum, maximum) x (piece a, piece b)
-        uint2* at_box = reinterpret_cast<uint2*>(box + (e >> 1) * kHeadDim + ((e & 1) ? at.b : at.a));
-        uint2 mine = (e & 1) ? z : x;
-        if (slot != 0) {
-          const uint2 old = *at_box;
-          mine = (e >> 1) ? make_uint2(as_u32(__hmax2(as_h2(mine.x), as_h2(old.x))),
-                                       as_u32(__hmax2(as_h2(mine.y), as_h2(old.y))))
-                          : make_uint2(as_u32(__hmin2(as_h2(mine.x), as_h2(old.x))),
-                                       as_u32(__hmin2(as_h2(mine.y), as_h2(old.y))));
+  for (int i = 0; i < 4; ++i)
+    if (at.turned)
+      cos_sin(w.rope.turns[4 * c + i], (long long)L + offset, w.rope.magnitude, cs[i].x, cs[i].y);
+#pragma unroll 1
+  for (; u < rows; u += kAppendThreads / 16) {
+    const bool is_k = u < p.Hkv, is_v = !is_k && u < kv;
+    const int h = is_k ? u : is_v ? u - p.Hkv : u - kv;
+    __half* to = w.q_out + ((size_t)b * p.Hq + h) * kHeadDim;
+    if (is_k || is_v) {
+      const size_t at_kv = (((size_t)(kNarrow ? b : phys) * p.Hkv + h) * P + slot) * kHeadDim;
+      if constexpr (kNarrow) to = (is_k ? w.nar.k_open : w.nar.v_open) + at_kv;
+      else to = (is_k ? p.k_pool : p.v_pool) + at_kv;
+    }
+    if (!(whole && (is_k || is_v))) {
+      if (at.turned && !is_v) {
+        float a[4], e[4];
+        Four<T>::get(x, a);
+        Four<T>::get(z, e);
+        turn(inter, a, e, cs);
+        x = Four<__half>::put(a);
+        z = Four<__half>::put(e);
+      } else {
+        x = to_half<T>(x);
+        z = to_half<T>(z);
+      }
+      *reinterpret_cast<uint2*>(to + at.a) = x;
+      *reinterpret_cast<uint2*>(to + at.b) = z;
+      if (is_k) {
+        __half* box = p.meta + box_offset(p, b, h, page);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // (minimum, maximum) x (piece a, piece b)
+          uint2* at_box = reinterpret_cast<uint2*>(box + (e >> 1) * kHeadDim + ((e & 1) ? at.b : at.a));
+          uint2 mine = (e & 1) ? z : x;
+          if (slot != 0) {
+            const uint2 old = *at_box;
+            mine = (e >> 1) ? make_uint2(as_u32(__hmax2(as_h2(mine.x), as_h2(old.x))),
+                                         as_u32(__hmax2(as_h2(mine.y), as_h2(old.y))))
+                            : make_uint2(as_u32(__hmin2(as_h2(mine.x), as_h2(old.x))),
+                                         as_u32(__hmin2(as_h2(mine.y), as_h2(old.y))));
+          }
+          *at_box = mine;
         }
-        *at_box = mine;
       }
     }
+    if (u + kAppendThreads / 16 < rows) load(u + kAppendThreads / 16);
   }
-  __syncthreads();
+  __syncthreads();  // (every thread has read the length)
   if (threadIdx.x == 0) p.seq_lens[b] = L + 1;
 }
 
@@ -676,13 +695,10 @@ cudaError_t write(const WriteParams& w, bool narrow, cudaStream_t s) {
   const unsigned q_blocks = w.q ? (unsigned)((p.Hq + kQHeads - 1) / kQHeads) : 0u;
   const unsigned pages = (unsigned)((w.n + P - 1) / P + 1);
   const dim3 grid(heads + q_blocks, pages, p.B), block(kWriteThreads);
-  if (!narrow) {
-    const cudaError_t e = launch_pdl((const void*)rotary_prefill_kernel<T, P>, grid, block, 0, s, args);
-    return e == cudaSuccess ? launch_advance_lengths(p, w.n, s) : e;
-  }
-  const cudaError_t e = launch_pdl((const void*)rotary_pages_kernel<T, P>, grid, block, 0, s, args);
-  if (e != cudaSuccess) return e;
-  return launch_pdl((const void*)rotary_open_kernel<T, P>, dim3(heads, p.B), block, 0, s, args);
+  const void* fn = narrow ? (const void*)rotary_pages_kernel<T, P>
+                          : (const void*)rotary_prefill_kernel<T, P>;
+  const cudaError_t e = launch_pdl(fn, grid, block, 0, s, args);
+  return e == cudaSuccess ? launch_advance_lengths(p, w.n, s) : e;
 }
 
 }  // namespace
@@ -697,8 +713,10 @@ cudaError_t launch_rotate(const RotateCall& r, cudaStream_t s) {
   p.out_stride = r.out_stride;
   p.heads = r.heads;
   p.transposed = r.transposed;
-  // eight heads a half-warp; fewer where that leaves most SMs without work
-  p.per = (long long)r.tokens * r.heads >= 8LL * 152 * 64 ? 8 : 2;
+  // Eight heads a half-warp share a position's cosines (8192 tokens of 40 heads: 28.1 us, 33 at four,
+  // 56 at two; 1999 tokens of 24: 4.8, 5.1 and 7.7); few rows take two, for their latency (4 tokens of
+  // 32 heads: 3.5 us at eight, 3.1 at two).
+  p.per = (long long)r.tokens * r.heads >= 16384 ? 8 : 2;
   p.groups = (r.heads + p.per - 1) / p.per;
   p.units = (long long)r.tokens * p.groups;
   void* args[] = {&p};

@@ -161,9 +161,16 @@ int check_groups(const quest_cache_t& c, const quest_prefix_group_t* groups, int
   return total == c.batch ? QUEST_OK : bad("the groups' counts must sum to the batch");
 }
 
-// Whether sharing pays: below this many bytes of keys and values that sequences would read again.
-constexpr long long kShareBytes = 0;
-constexpr int kPrefixJobs = 96;  // of the prefixes, in one go
+// Whether sharing pays.  Two launches and a job's start and end cost some 8 us, and sequences that
+// read a short prefix each for itself find it in L2: 16 sequences of 32 / 8 heads behind 512 tokens
+// take 9.7 us each for itself and 11.0 shared, 32 behind 256 tokens 13.3 and 17.8, 4 of 32 MHA heads
+// behind 1024 tokens 14.3 and 15.1, behind 2048 tokens 4 of 32 / 8 heads 16.8 and 11.3.  Few rows
+// gain sooner (4 sequences of 8 kv heads behind 512 tokens 11.4 and 9.3): their span decode splits
+// them and joins.
+constexpr int kShareTokens = 1024, kShareTokensFewRows = 512, kFewRows = 32;
+constexpr int kPrefixJobs = 96;  // of the prefixes, in one go: five eighths of the SMs, the others
+                                 // begin with tails (152: 45.2 us for 40.0 at 32 tails of 512 tokens
+                                 // behind 32K, 42.2 for 34.7 at tails of 16)
 constexpr int kPrefixStart = 3;  // what a job's start and end cost, in tiles
 
 // How the prefixes are cut.  A job takes `per` K / V tiles, so that the jobs fill the SMs once, or
@@ -173,16 +180,17 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   PrefixTable t{};
   t.n = n;
   const int G = group_of(c), user = user_split(o);
-  long long saved = 0;
-  int first = 0;
+  int first = 0, longest = 0;
   for (int i = 0; i < n; ++i) {
     const int pages = groups[i].count > 1 ? groups[i].prefix_tokens / c.page_size : 0;
     t.group[i] = PrefixTable::Group{first, groups[i].count, pages, 1, 0, 0};
     first += groups[i].count;
-    saved += (groups[i].count - 1LL) * pages * c.page_size * c.num_kv_heads * (4 * kHeadDim);
+    longest = std::max(longest, pages * c.page_size);
   }
-  if (saved == 0 || (!user && saved < kShareBytes))
-    for (int i = 0; i < n; ++i) t.group[i].pages = 0;
+  const bool few = (long long)c.batch * c.num_kv_heads <= kFewRows;
+  const bool pays = longest >= (few ? kShareTokensFewRows : kShareTokens);
+  for (int i = 0; i < n && !user; ++i)  // (where some group shares, any that has a tile does)
+    if (!pays || t.group[i].pages * c.page_size < kPrefixTokens) t.group[i].pages = 0;
   auto tiles = [&](int i) {
     return (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
   };

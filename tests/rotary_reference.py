@@ -32,11 +32,11 @@ def turned(rope, x, positions, transposed=False):
     """(y, bound): x [..., heads, 128] turned, in 64 bits on the CPU, and how far fp32 arithmetic may
     be off before the last rounding.
 
-    The bound, relative to m (|x_a| + |x_b|): the angle is cut at 2^-32 of a turn (1.5e-9) and
-    rounded to 24 bits of half a turn (2^-25 * 2 pi = 1.9e-7, as the cosine's and sine's derivatives
-    are at most 1); a cosine or sine within an ulp (2^-24 of values up to 1), its product with m,
-    m's own rounding, the product with x and the sum: five roundings of 2^-24, 3e-7 in all.  Together
-    below 2^-20 (9.5e-7)."""
+    The bound, relative to m (|x_a| + |x_b|): the angle is cut at 2^-32 of a turn (1.5e-9) and its
+    rest within an eighth of a turn rounded to 24 bits (2^-25 * pi / 2 = 4.7e-8, as the cosine's and
+    sine's derivatives are at most 1); a cosine or sine within 1e-7, its product with m, m's own
+    rounding, the product with x and the sum: four roundings of 2^-24, 2.4e-7.  Together below 2^-20
+    (9.5e-7)."""
     x = x.double().cpu()
     t = angles(rope, positions.cpu())[..., None, :]
     cos, sin = torch.cos(t) * rope.magnitude, torch.sin(t) * rope.magnitude
