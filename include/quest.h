@@ -596,9 +596,10 @@ int quest_narrow_prefill_rotary(const quest_narrow_cache_t* cache, const quest_r
  * sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
  * batch (the counts sum to `batch`), whose first prefix_tokens tokens are the same; of these
  * the whole pages, prefix_tokens / page_size of them, are read once for the group, through the
- * block-table row of the group's first sequence.  (The other sequences' rows hold the same
- * entries: which row is read is the call's choice.)  A sequence shorter than its prefix sees its
- * own seq_len tokens.  prefix_tokens = 0: nothing is shared.
+ * block-table row of the group's first sequence.  The block-table rows of all sequences of the
+ * group hold the same entries for these pages, whatever the sequences' own lengths (which row is
+ * read is the call's choice).  A sequence shorter than its prefix sees its own seq_len tokens.
+ * prefix_tokens = 0: nothing is shared.
  */
 typedef struct quest_prefix_group {
     int32_t count;         /* >= 1 */
@@ -614,8 +615,9 @@ size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefi
 
 /* q fp16 [batch][num_q_heads][128]; groups: HOST array, copied by the call; out, lse as in
  * quest_dense_decode.  A row whose sequence is empty gives out = 0, lse = -inf; NaN and
- * infinities as in windowed attention.  Where sharing would not pay every sequence reads all of
- * its tokens itself.
+ * infinities as in windowed attention.  Where sharing would not pay (prefixes of a few hundred
+ * tokens) every sequence reads all of its tokens itself.  A call may be captured into a graph; the
+ * sequences may grow between calls.
  * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns, debug_flags. */
 int quest_prefix_decode(const quest_cache_t* cache, const void* q,
                         const quest_prefix_group_t* groups, int32_t n_groups, void* out,

@@ -861,27 +861,41 @@ def rotate(rope, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.T
     """Heads x [..., heads, 128] (fp16, bf16 or fp32) turned by their tokens' positions (int32, of
     x's leading dims).  ``transposed``: turned the other way, by the same magnitude: with a gradient
     of the output as x, the gradient of the input.  ``out`` may be x."""
-    if x.dim() < 3 or x.shape[-1] != HEAD_DIM:
-        raise ValueError("x must be [..., heads, 128]")
-    if x.dtype not in _DTYPES:
+    shape = x.shape
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise TypeError("x must be float16, bfloat16 or float32")
-    _heads(x, "x", None)
-    _need(positions, "positions", torch.int32, x.shape[:-2])
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype:
-        raise TypeError("out must have x's type")
-    _heads(out, "out", x.shape)
+    if len(shape) < 3 or shape[-1] != HEAD_DIM:
+        raise ValueError("x must be [..., heads, 128]")
     dev = x.get_device()
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    if len(shape) == 3 and type(x) is torch.Tensor and type(out) is torch.Tensor:
+        xs, os, heads = x.stride(), out.stride(), shape[1]
+        ok = (xs[2] == 1 and os[2] == 1 and (heads == 1 or (xs[1] == HEAD_DIM and os[1] == HEAD_DIM))
+              and out.dtype is x.dtype and out.shape == shape and dev >= 0)
+        x_stride, out_stride = (xs[0], os[0]) if shape[0] > 1 else (0, 0)
+    else:
+        ok = False
+    if not ok:  # more leading dims, or something to refuse
+        _heads(x, "x", None)
+        if out.dtype != x.dtype:
+            raise TypeError("out must have x's type")
+        _heads(out, "out", shape)
+        x_stride, out_stride = _token_stride(x, "x"), _token_stride(out, "out")
+    _need(positions, "positions", torch.int32, shape[:-2])
     if positions.get_device() != dev or out.get_device() != dev:
         raise ValueError("x, positions and out must be on one device")
     if _current_device() != dev:
         raise ValueError("x is on another device than the current one")
-    if x.numel() == 0:
+    tokens = positions.numel()
+    if tokens == 0 or shape[-2] == 0:
         return out
-    _check(load().quest_rotate(rope.ref, x.data_ptr(), _token_stride(x, "x"), positions.data_ptr(),
-                               positions.numel(), x.shape[-2], _DTYPES[x.dtype], int(transposed),
-                               out.data_ptr(), _token_stride(out, "out"), _stream(stream)))
+    rc = load().quest_rotate(rope.ref, x.data_ptr(), x_stride, positions.data_ptr(), tokens,
+                             shape[-2], dtype, int(transposed), out.data_ptr(), out_stride,
+                             _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -1038,6 +1052,8 @@ class RotaryPlan:
 # ---- prefixes that sequences share
 def _groups(groups: Sequence[Tuple[int, int]]):
     rows = [(int(count), int(tokens)) for count, tokens in groups]
+    if any(not -2 ** 31 <= x < 2 ** 31 for row in rows for x in row):
+        raise ValueError("a group's numbers must fit 32 bits")
     return (QuestPrefixGroup * max(1, len(rows)))(*rows), len(rows)
 
 

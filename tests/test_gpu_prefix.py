@@ -194,6 +194,56 @@ def test_odd_values_reach_the_rows_that_see_them(geom, at, value, name):
         assert torch.equal(out[unseen], want[unseen]) and torch.equal(lse[unseen], want_lse[unseen])
 
 
+@pytest.mark.parametrize("geom", [(4, 4, 16), (8, 1, 32), (8, 2, 16)], ids=str)
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("at", [64, 200, 333, 900])
+def test_odd_values_in_a_tail_stay_in_its_sequence(geom, at, value):
+    """A value of one sequence's own tokens (in either half of a tile, in any of its jobs)."""
+    hq, hkv, P = geom
+    cache, groups = make([(64, [1000, 980, 70])], hq, hkv, P, seed=at)
+    qq = queries(cache)
+    want, want_lse = run(cache, groups, qq, 6)
+    phys = int(cache.block_table[1, at // P])
+    clean = cache.v_pool.clone()
+    cache.v_pool[phys, :, at % P, 5] = value
+    out, lse = run(cache, groups, qq, 6)
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, :, 5] = False
+    got = out[1, :, 5]
+    assert torch.isnan(got).all() if value != value else bool((got == value).all())
+    cache.v_pool.copy_(clean)
+    out[~keep] = want[~keep]
+    right(cache, qq, out, lse)
+    assert torch.equal(lse, want_lse)
+    assert torch.equal(out[[0, 2]], want[[0, 2]])
+
+
+@pytest.mark.parametrize("lens", [[3, 600, 200], [0, 130, 600], [64, 64, 64]])
+def test_a_first_sequence_shorter_than_its_prefix(lens):
+    """The others read the prefix through its row of the block table all the same."""
+    cache, groups = make([(192, lens), (256, [300] * 3)], 8, 2, 16, seed=lens[0])
+    qq = queries(cache)
+    for pps in (0, 3):
+        out, lse = run(cache, groups, qq, pps)
+        right(cache, qq, out, lse)
+
+
+def test_many_groups_and_many_sequences():
+    """128 groups (the most there are), and 300 short sequences in a few: the queue's chunks of 32
+    sequences, jobs without a token, tails of every number of tiles."""
+    cache, groups = make([(130 + 16 * (i % 5), [150 + 40 * (i % 7), 200]) for i in range(128)], 4, 2, 16)
+    qq = queries(cache)
+    for pps in (0, 2):
+        out, lse = run(cache, groups, qq, pps)
+        right(cache, qq, out, lse)
+    cache, groups = make([(1040, [1040 + (i * 37) % 700 for i in range(150)]),
+                          (0, [(i * 53) % 300 for i in range(100)]),
+                          (2000, [2000 - 9 * i for i in range(50)])], 4, 1, 32)
+    qq = queries(cache)
+    out, lse = run(cache, groups, qq)
+    right(cache, qq, out, lse)
+
+
 def test_a_query_with_nan_stays_in_its_row():
     cache, groups = make(BATCHES["few"], 8, 2, 16)
     qq = queries(cache)
