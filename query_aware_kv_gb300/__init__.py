@@ -1,7 +1,9 @@
 """Quest decode-time hot path for GB300 (sm_103a): paged fp16 KV cache with per-page key
 min/max boxes, query-aware page scoring, per-head top-K page selection and split-K
 sparse flash-decode, as a C-ABI library (``libquest.so``) with a thin ctypes binding; caches
-of 8-bit pages (``NarrowCache``) and attention with a sliding window and sink tokens.
+of 8-bit pages (``NarrowCache``), attention with a sliding window and sink tokens, rotary
+positions (``Rope``) turned on the way into a cache, and attention over prefixes that sequences
+share.
 
 The names below mirror the C entry points of ``include/quest.h``.
 """

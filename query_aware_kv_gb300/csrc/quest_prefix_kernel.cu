@@ -19,6 +19,20 @@
 // while tile t + 1 is.  Warps 8 and 9 fetch K and V (a page a TMA box, three tiles of each in
 // flight, over the ends of jobs), warp 10 issues the products, warp 11 takes jobs from the queue, one
 // ahead of the fetches, warp 12 fetches their queries.
+//
+// What bounds it: DRAM where there is enough to read.  A tile takes a CTA 0.85 us when nothing waits
+// for memory (Q K^T, softmax and P V hand over to one another four times; the tensor core has 1024 of
+// these 1650 cycles), which is 64 KiB, so 152 CTAs could take 11.7 TB/s; a job's start and end cost
+// 2.2 us with its last tile, of which 0.8 are the share on its way out, and its loads go on
+// meanwhile.  Measured: 16 sequences of 32 MHA heads with 2K tokens of their own behind 8K shared ones
+// 80 us (483 MB: 6.0 TB/s, 6.7 in the jobs' launch), 32 sequences of 32 / 8 heads with 512 behind
+// 32K 41 us (177 MB), of which 3 are the first lengths, pages and tiles, some 4 the last jobs, which
+// not every CTA has, and 6 the join with its launch.
+//
+// (Two chains a CTA, which took whole tiles in turn with an issue warp each, faulted on long runs of
+// full row blocks for a reason that was not found, and are not here; tails on the span decode, in a
+// launch that starts with the prefixes', took 93 us for the 80 and 45 for the 41: its CTAs do not fit
+// beside these, and each begins with its own look-ups.)
 #include <math_constants.h>
 
 #include <algorithm>
@@ -603,7 +617,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           const int phys = p.block_table[(size_t)job.seq * p.max_pages + page];
           if (phys < 0 || phys >= p.num_phys) continue;
           const size_t at = ((size_t)phys * p.Hkv + job.g) * P * kHeadDim + 4 * lane;
-#pragma unroll 1
+#pragma unroll 4
           for (int e = 0; e < min(P, last - page * P); ++e) {
             const uint2 kw = *reinterpret_cast<const uint2*>(p.k_pool + at + e * kHeadDim);
             const uint2 vw = *reinterpret_cast<const uint2*>(p.v_pool + at + e * kHeadDim);
