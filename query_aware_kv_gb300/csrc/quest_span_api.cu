@@ -2,6 +2,7 @@
 // (declared in include/quest.h): argument checks, workspace layout and dispatch.  No call
 // allocates memory or synchronises.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdio>
 
@@ -191,18 +192,16 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   const bool pays = longest >= (few ? kShareTokensFewRows : kShareTokens);
   for (int i = 0; i < n && !user; ++i)  // (where some group shares, any that has a tile does)
     if (!pays || t.group[i].pages * c.page_size < kPrefixTokens) t.group[i].pages = 0;
-  auto tiles = [&](int i) {
-    return (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
-  };
-  auto items = [&](int i) {
-    return (long long)c.num_kv_heads *
-           (((long long)t.group[i].count * G + kPrefixRows - 1) / kPrefixRows);
-  };
-  int most = 0;
-  for (int i = 0; i < n; ++i) most = std::max(most, tiles(i));
+  int tiles[QUEST_MAX_PREFIX_GROUPS], items[QUEST_MAX_PREFIX_GROUPS], most = 0;
+  for (int i = 0; i < n; ++i) {
+    tiles[i] = (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
+    items[i] = (int)(c.num_kv_heads *
+                     (((long long)t.group[i].count * G + kPrefixRows - 1) / kPrefixRows));
+    most = std::max(most, tiles[i]);
+  }
   auto ctas = [&](int per) {
     long long sum = 0;
-    for (int i = 0; i < n; ++i) sum += items(i) * ((tiles(i) + per - 1) / per);
+    for (int i = 0; i < n; ++i) sum += (long long)items[i] * ((tiles[i] + per - 1) / per);
     return sum;
   };
   const int least = std::max(2, (most + kPrefixSplits - 1) / kPrefixSplits);
@@ -226,18 +225,21 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
       }
     }
   }
+  long long jobs = 0, parts = 0;
   for (int i = 0; i < n; ++i) {
     PrefixTable::Group& g = t.group[i];
-    g.splits = std::max(1, (tiles(i) + per - 1) / per);
-    g.cta0 = t.ctas;
-    g.part0 = t.parts;
+    g.splits = std::max(1, (tiles[i] + per - 1) / per);
+    g.cta0 = (int)std::min<long long>(jobs, INT_MAX);
+    g.part0 = (int)std::min<long long>(parts, INT_MAX);
     if (g.pages > 0) {
-      const int mine = (int)items(i) * g.splits;
-      t.ctas += mine;
-      t.parts += mine * (int)std::min<long long>(kPrefixRows, (long long)g.count * G);
+      const long long mine = (long long)items[i] * g.splits;
+      jobs += mine;
+      parts += mine * std::min<long long>(kPrefixRows, (long long)g.count * G);
     }
     t.most_pages = std::max(t.most_pages, c.max_pages - g.pages);
   }
+  t.ctas = (int)std::min<long long>(jobs, INT_MAX);
+  t.parts = (int)std::min<long long>(parts, INT_MAX);
   return t;
 }
 
@@ -253,6 +255,15 @@ int tail_splits(const quest_cache_t& c, const PrefixTable& t, const quest_opts_t
   long long n = (t.most_pages + piece - 1) / piece;
   if (!user_split(o)) n = std::min(n, 10 * kPrefixSms / rows);
   return (int)std::max(1LL, std::min<long long>(n, kPrefixSplits));
+}
+
+// Places of all shares; the kernels count them in 32 bits.
+int prefix_parts(const quest_cache_t& c, const PrefixTable& t, int splits, size_t* parts) {
+  const long long tails = (long long)c.batch * c.num_q_heads * splits;
+  if (t.parts + tails + t.ctas >= INT_MAX)
+    return set_last_error(QUEST_ERR_UNSUPPORTED, "the batch has too many rows for its splits");
+  *parts = (size_t)(t.parts + tails);
+  return QUEST_OK;
 }
 
 // One span-decode launch over rows of at most `pages` pages.
@@ -445,8 +456,9 @@ size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefi
   if (cache->batch == 0) return span_layout(*cache, 0, opts).total;
   if (check_groups(*cache, groups, n_groups)) return 0;
   const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
-  const size_t tails = (size_t)cache->batch * cache->num_q_heads * tail_splits(*cache, t, opts);
-  return span_layout(*cache, 0, opts, 1, t.parts + tails).total;
+  size_t parts = 0;
+  if (prefix_parts(*cache, t, tail_splits(*cache, t, opts), &parts)) return 0;
+  return span_layout(*cache, 0, opts, 1, parts).total;
 }
 
 int quest_prefix_decode(const quest_cache_t* cache, const void* q,
@@ -460,8 +472,9 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q,
   const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
   SpanParams sp{};
   const int splits = tail_splits(*cache, t, opts);
-  const size_t tails = (size_t)cache->batch * cache->num_q_heads * splits;
-  const SpanLayout L = span_layout(*cache, 0, opts, 1, t.parts + tails);
+  size_t parts = 0;
+  if ((rc = prefix_parts(*cache, t, splits, &parts))) return rc;
+  const SpanLayout L = span_layout(*cache, 0, opts, 1, parts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   sp.p = make_params(*cache, ws, L, opts);
   if (t.ctas == 0) {  // nothing is shared: every sequence on its own
