@@ -592,8 +592,8 @@ int quest_narrow_prefill_rotary(const quest_narrow_cache_t* cache, const quest_r
 /*
  * ---- Prefixes that sequences share ---------------------------------------------------
  *
- * Attention of one query token per sequence over every token of its sequence, where groups of
- * sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
+ * Attention of the last token of every sequence (or its last few, drafted ones) over the tokens up
+ * to it, where groups of sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
  * batch (the counts sum to `batch`), whose first prefix_tokens tokens are the same; of these
  * the whole pages, prefix_tokens / page_size of them, are read once for the group, through the
  * block-table row of the group's first sequence.  The block-table rows of all sequences of the
@@ -607,19 +607,22 @@ typedef struct quest_prefix_group {
 } quest_prefix_group_t;
 #define QUEST_MAX_PREFIX_GROUPS 128
 
-/* Bytes of workspace of quest_prefix_decode with these groups and opts; 0 if the arguments are
+/* Bytes of workspace of quest_prefix_decode with these groups, n_tokens and opts; 0 if the arguments are
  * invalid.  One workspace serves calls with the same groups, and no calls but
  * quest_prefix_decode. */
 size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefix_group_t* groups,
-                                   int32_t n_groups, const quest_opts_t* opts);
+                                   int32_t n_groups, int32_t n_tokens, const quest_opts_t* opts);
 
-/* q fp16 [batch][num_q_heads][128]; groups: HOST array, copied by the call; out, lse as in
- * quest_dense_decode.  A row whose sequence is empty gives out = 0, lse = -inf; NaN and
+/* q fp16 [batch][n_tokens][num_q_heads][128], token i of sequence b at position seq_lens[b] -
+ * n_tokens + i (their keys and values are written before); out: fp16 of the same shape; lse: fp32
+ * [batch][n_tokens][num_q_heads] or NULL.  n_tokens * (num_q_heads / num_kv_heads) is at most 128
+ * (QUEST_ERR_UNSUPPORTED).  groups: HOST array, copied by the call.  A row that sees no token (an
+ * empty sequence, a negative position) gives out = 0, lse = -inf; NaN and
  * infinities as in windowed attention.  Where sharing would not pay (prefixes of a few hundred
  * tokens) every sequence reads all of its tokens itself.  A call may be captured into a graph; the
  * sequences may grow between calls.
  * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns, debug_flags. */
-int quest_prefix_decode(const quest_cache_t* cache, const void* q,
+int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tokens,
                         const quest_prefix_group_t* groups, int32_t n_groups, void* out,
                         float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,
                         quest_stream_t stream);

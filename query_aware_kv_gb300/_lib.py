@@ -169,8 +169,8 @@ def load() -> ctypes.CDLL:
             "quest_window_workspace_size": (SZ, [C, I32, O]),
             "quest_window_decode": (ctypes.c_int, [C, V, I32, I32, V, V, V, SZ, O, V]),
             "quest_window_prefill": (ctypes.c_int, [C, V, I32, I32, I32, V, V, V, SZ, O, V]),
-            "quest_prefix_workspace_size": (SZ, [C, G, I32, O]),
-            "quest_prefix_decode": (ctypes.c_int, [C, V, G, I32, V, V, V, SZ, O, V]),
+            "quest_prefix_workspace_size": (SZ, [C, G, I32, I32, O]),
+            "quest_prefix_decode": (ctypes.c_int, [C, V, I32, G, I32, V, V, V, SZ, O, V]),
             "quest_rope_init": (ctypes.c_int, [R, I32, I32, ctypes.POINTER(ctypes.c_double),
                                                ctypes.c_double]),
             "quest_rotate": (ctypes.c_int, [R, V, I64, V, I32, I32, I32, I32, V, I64, V]),
@@ -1058,11 +1058,12 @@ def _groups(groups: Sequence[Tuple[int, int]]):
 
 
 def prefix_workspace(cache: PagedCache, groups: Sequence[Tuple[int, int]],
-                     o: Optional[QuestOpts] = None) -> torch.Tensor:
-    """A zeroed workspace for prefix_decode with these groups and opts."""
+                     o: Optional[QuestOpts] = None, n_tokens: int = 1) -> torch.Tensor:
+    """A zeroed workspace for prefix_decode with these groups, opts and query tokens a sequence."""
     lib = load()
     arr, n_groups = _groups(groups)
-    n = lib.quest_prefix_workspace_size(ctypes.byref(cache.desc), arr, n_groups, _opts_ref(o))
+    n = lib.quest_prefix_workspace_size(ctypes.byref(cache.desc), arr, n_groups, int(n_tokens),
+                                        _opts_ref(o))
     if n == 0:
         raise QuestError(QUEST_ERR_INVALID_ARG, lib.quest_last_error().decode())
     return torch.zeros(int(n), dtype=torch.uint8, device=cache.k_pool.device)
@@ -1070,24 +1071,36 @@ def prefix_workspace(cache: PagedCache, groups: Sequence[Tuple[int, int]],
 
 class PrefixPlan:
     """prefix_decode bound to its cache, groups, workspace, stream and outputs, for a decode loop
-    (the sequences may grow; a batch of other groups needs another plan): each call only checks q.
-    The outputs are overwritten by every call and returned by it."""
+    (the sequences may grow; a batch of other groups needs another plan): each call only checks q,
+    [B][Hq][128], or [B][n_tokens][Hq][128] with n_tokens given.  The outputs (of q's shape) are
+    overwritten by every call and returned by it."""
 
     def __init__(self, cache: PagedCache, groups: Sequence[Tuple[int, int]], ws: torch.Tensor,
                  o: Optional[QuestOpts] = None, out=None, lse=None, want_lse: bool = True,
-                 stream=None):
+                 stream=None, n_tokens: Optional[int] = None):
         if not isinstance(cache, PagedCache):
             raise TypeError("cache must be a PagedCache")
-        self._qshape = torch.Size((cache.batch, cache.desc.num_q_heads, HEAD_DIM))
+        B, Hq, dev = cache.batch, cache.desc.num_q_heads, cache.k_pool.device
+        rows = (B, Hq) if n_tokens is None else (B, int(n_tokens), Hq)
+        if min(rows) < 0:
+            raise ValueError("n_tokens must not be negative")
+        self._qshape = torch.Size((*rows, HEAD_DIM))
         self._dev, self._many = cache.k_pool.get_device(), torch.cuda.device_count() > 1
-        self.out, self.lse = _out(cache, cache.k_pool, out, lse, want_lse)
+        if out is None:
+            out = torch.empty(self._qshape, dtype=torch.float16, device=dev)
+        _need(out, "out", torch.float16, self._qshape)
+        if lse is None and want_lse:
+            lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        if lse is not None:
+            _need(lse, "lse", torch.float32, rows)
+        self.out, self.lse = out, lse
         _here(cache, ws, self.out, self.lse)
         arr, n_groups = _groups(groups)
         self._keep = (cache, ws, o, arr)  # alive as long as the plan
         self._fn = load().quest_prefix_decode
         self._desc = ctypes.byref(cache.desc)
-        self._tail = (arr, n_groups, self.out.data_ptr(), _ptr(self.lse), ws.data_ptr(),
-                      ws.numel(), _opts_ref(o), _stream(stream))
+        self._tail = (1 if n_tokens is None else int(n_tokens), arr, n_groups, self.out.data_ptr(),
+                      _ptr(self.lse), ws.data_ptr(), ws.numel(), _opts_ref(o), _stream(stream))
 
     def decode(self, q: torch.Tensor):
         """The attention of this step's queries over their sequences; returns (out, lse)."""
@@ -1109,8 +1122,10 @@ def prefix_decode(cache: PagedCache, q: torch.Tensor, groups: Sequence[Tuple[int
     """Attention of the last token of every sequence over its whole cache, where groups of
     sequences begin with the same tokens: ``groups`` holds (sequences, tokens of their common
     prefix) of the batch's sequences in order.  A prefix's whole pages are read once for its
-    group."""
-    return PrefixPlan(cache, groups, ws, o, out, lse, want_lse, stream).decode(q)
+    group.  q [B][Hq][128], or [B][n][Hq][128] for the last n tokens of every sequence (n Hq / Hkv
+    at most 128), which see what comes before them."""
+    n = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else None
+    return PrefixPlan(cache, groups, ws, o, out, lse, want_lse, stream, n).decode(q)
 
 
 def decode_layers(cache: PagedCache, layers: Sequence[PagedCache], q: Sequence[torch.Tensor],

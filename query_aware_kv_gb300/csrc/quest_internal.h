@@ -269,8 +269,8 @@ constexpr int kPrefixSplits = 64;   // of a prefix, and of a tail
 // The cuts of the prefixes (t.ctas jobs), then every sequence's and kv head's tail in jobs of
 // piece_pages pages, `splits` of them at most (part_ml / part_acc rows from t.parts on), then all
 // shares into out and lse: two launches.
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, int piece_pages,
-                          cudaStream_t s);
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int n_tokens, int splits,
+                          int piece_pages, cudaStream_t s);
 
 // Windowed attention of the last n_tokens tokens of every sequence (quest_prompt_kernel.cu):
 // p.n_splits CTAs per work item of 256 query rows, whose shares take prompt_part_rows rows of

@@ -1,15 +1,15 @@
-// quest_prefix_kernel.cu - attention of one query token per sequence where groups of sequences
-// share a prefix, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands by
+// quest_prefix_kernel.cu - attention of the last token or tokens of every sequence where groups of
+// sequences share a prefix, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands by
 // TMA).
 //
 // The work is a queue of jobs, each a run of pages that up to 128 rows attend over, a row being
-// (sequence, query head): first the cuts of the prefixes, whose rows are a group's query tokens with
+// (query token, query head): first the cuts of the prefixes, whose rows are a group's query tokens with
 // the G heads of a kv head (so that a prefix is read once for all of them), then every sequence's own
-// tokens behind its prefix (G rows).  A CTA an SM takes jobs in turn; the lengths are on the device
+// tokens behind its prefix (G rows a query token).  A CTA an SM takes jobs in turn; the lengths are on the device
 // only, so nobody could deal them out evenly beforehand.  Per 128 tokens of a job:
 //   S = Q K^T,   P = 2^(S c - m + 8),   O += P V
-// with a running maximum m and sum of weights per row.  There is no causal mask (the queries come
-// after everything); a row of a prefix ends with its own sequence where that is shorter.  What a job
+// with a running maximum m and sum of weights per row, which sees the tokens up to its own position:
+// of a prefix all of them but where its sequence is shorter.  What a job
 // leaves is a share (m, sum, O) per row; prefix_join_kernel joins a row's shares.
 //
 // Eight softmax warps share a tile: warps 0-3 its first 64 tokens, warps 4-7 the other 64, a thread
@@ -56,11 +56,12 @@ constexpr float kLazy = 6.f;      // the maximum moves when a row exceeds it by 
 // A run of pages that a row block attends over.
 struct Job {
   int n;       // tiles, of 128 tokens from page0's first on; 0: its rows see nothing; -1: no more jobs
-  int shared;  // of a prefix: the rows are tokens q_tok .. of a group, which may end early
+  int ragged;  // its rows may see different tokens (of a prefix, or of several query tokens)
+  int shared;  // of a prefix
   int seq;     // the row of the block table
   int g;       // the kv head
   int page0, end;   // the first page; the position behind the last token
-  int q_tok, rows;  // the first query token; rows in use
+  int q_tok, rows;  // the first query token (of all sequences' counted through); rows in use
   int share;        // the first row's place in part_ml / part_acc
 };
 
@@ -107,6 +108,7 @@ constexpr uint32_t kIdescPV = 1u << 4 | 1u << 16 | (kHeadDim >> 3) << 17 | (kRow
 struct PrefixParams {
   Params p;      // exited: the queue's counter
   int log_g;
+  int n;            // query tokens of a sequence
   int splits;       // jobs of a tail, at most
   int piece_pages;  // pages of such a job, where splits allow it
 };
@@ -128,11 +130,11 @@ struct Cut {
   int group, at, blk, page0, page1;
 };
 template <int PPT>
-__device__ __forceinline__ Cut cut_of(const PrefixTable& t, int lg, int c) {
+__device__ __forceinline__ Cut cut_of(const PrefixTable& t, int n, int lg, int c) {
   Cut x;
   x.group = t.group_of_cta(c);
   const PrefixTable::Group& q = t.group[x.group];
-  const int blocks = ((q.count << lg) + kRows - 1) / kRows;
+  const int blocks = ((q.count * n << lg) + kRows - 1) / kRows;
   x.at = c - q.cta0;
   x.blk = x.at % blocks;
   const int split = x.at / blocks % q.splits, tiles = (q.pages + PPT - 1) / PPT;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   pdl_trigger();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
   volatile int* give_up = &bars.give_up;
-  const int lg = pp.log_g;
+  const int lg = pp.log_g, nq = pp.n;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, bar, parity, give_up)) != 0;
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     Tail tail{0, 0};
     int L = 0;
     for (int k = 0;; ++k) {
-      Job job{-1, 0, 0, 0, 0, 0, 0, 0, 0};
+      Job job{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
       if (k > 0) {
         // not before this CTA's fetches are through with the job before: taken any earlier (all
         // CTAs took their first three at the start) the jobs were dealt out, not queued for
@@ -244,19 +246,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         index = __shfl_sync(0xffffffffu, index, 0);
       }
       if (index < table.ctas) {
-        const Cut x = cut_of<PPT>(table, lg, index);
+        const Cut x = cut_of<PPT>(table, nq, lg, index);
         const PrefixTable::Group& q = table.group[x.group];
-        const int tok0 = x.blk * (kRows >> lg), tok1 = min(q.count, tok0 + (kRows >> lg));
+        const int tokens = q.count * nq;
+        const int tok0 = x.blk * (kRows >> lg), tok1 = min(tokens, tok0 + (kRows >> lg));
         int most = 0;  // the longest of the rows' sequences
-        for (int i = tok0 + lane; i < tok1; i += 32) most = max(most, length(q.first + i));
-        job.shared = 1;
+        for (int i = tok0 / nq + lane; i * nq < tok1; i += 32) most = max(most, length(q.first + i));
+        job.ragged = job.shared = 1;
         job.seq = q.first;
-        job.g = x.at / (((q.count << lg) + kRows - 1) / kRows) / q.splits;
+        job.g = x.at / (((tokens << lg) + kRows - 1) / kRows) / q.splits;
         job.page0 = x.page0;
         job.end = min(__reduce_max_sync(0xffffffffu, most), x.page1 * P);
-        job.q_tok = q.first + tok0;
+        job.q_tok = q.first * nq + tok0;
         job.rows = (tok1 - tok0) << lg;
-        job.share = q.part0 + x.at * min(q.count << lg, kRows);
+        job.share = q.part0 + x.at * min(tokens << lg, kRows);
         job.n = 0;
       } else {
         while (index >= base + chunk && b0 + 32 < sequences) {
@@ -285,12 +288,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           const int start = __shfl_sync(0xffffffffu, first, at);
           const int local = index - base - __shfl_sync(0xffffffffu, sum, at) + jobs * p.Hkv;
           const int split = local / p.Hkv;
-          job.seq = job.q_tok = b0 + at;
+          job.ragged = nq > 1;
+          job.seq = b0 + at;
+          job.q_tok = job.seq * nq;
           job.g = local % p.Hkv;
           job.page0 = start + pages * split / jobs;
           job.end = min(__shfl_sync(0xffffffffu, L, at), (start + pages * (split + 1) / jobs) * P);
-          job.rows = 1 << lg;
-          job.share = table.parts + (((job.seq * p.Hkv + job.g) * pp.splits + split) << lg);
+          job.rows = nq << lg;
+          job.share = table.parts + ((job.seq * p.Hkv + job.g) * pp.splits + split) * job.rows;
           job.n = 0;
         }
       }
@@ -312,8 +317,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (job.n == 0) continue;
       if (loads > 0 && !wait(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
       if (elect_lane()) {
-        // of a tail only its own G rows: the others' scores may be anything
-        mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : (kHeadDim * 2) << lg);
+        // of a tail only its own rows: the others' scores may be anything
+        mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : kHeadDim * 2 * job.rows);
         for (int i = 0; i < 2; ++i)
           tma_3d(smem + Smem::q + i * kHalf, job.shared ? &map_q : &map_1, 64 * i, job.g << lg,
                  job.q_tok, &bars.q_full);
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // the first job's pages are looked up beside its lengths
     int early = 0;
     if ((int)blockIdx.x < table.ctas) {
-      const Cut x = cut_of<PPT>(table, lg, (int)blockIdx.x);
+      const Cut x = cut_of<PPT>(table, nq, lg, (int)blockIdx.x);
       early = p.block_table[(size_t)table.group[x.group].first * p.max_pages +
                             min(x.page0 + lane, table.group[x.group].pages - 1)];
     }
@@ -476,7 +481,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int pos0 = job.page0 * P;
       // the last position that the row sees; the least of the warp's rows, which go together
       int pr = job.end - 1;
-      if (job.shared && mine) pr = min(pr, length(job.q_tok + (row >> lg)) - 1);
+      if (job.ragged && mine) {
+        const int tok = job.q_tok + (row >> lg);
+        pr = min(pr, length(tok / nq) - nq + tok % nq);
+      }
       const int least = __reduce_min_sync(0xffffffffu, pr);
       float m = -CUDART_INF_F, l = 0.f;
       for (int i = 0; i < job.n; ++i, ++t) {
@@ -607,9 +615,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         todo &= todo - 1u;
         const float m_r = __shfl_sync(0xffffffffu, M, from);
         const int last = __shfl_sync(0xffffffffu, pr, from) + 1;
-        const int seq = job.q_tok + (r >> lg);
+        const int tok = job.q_tok + (r >> lg);
         const uint2 qw = *reinterpret_cast<const uint2*>(
-            p.q + ((size_t)seq * p.Hq + ((size_t)job.g << lg) + (r & (G - 1))) * kHeadDim + 4 * lane);
+            p.q + ((size_t)tok * p.Hq + ((size_t)job.g << lg) + (r & (G - 1))) * kHeadDim + 4 * lane);
         const float2 qa = h2f(qw.x), qb = h2f(qw.y);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -661,34 +669,36 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   if (warp == 10) tmem_free(tmem);
 }
 
-// The shares of a prefix and of a tail into out and lse: a warp a row (sequence, query head), lane l
+// The shares of a prefix and of a tail into out and lse: a warp a row (query token, query head), lane l
 // the dims 4 l .. 4 l + 3.  First come the prefix's splits
-// (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, G apart).
+// (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, a job's rows apart).
 constexpr int kPrefixJoinThreads = 128;
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
     const __grid_constant__ PrefixParams pp, const __grid_constant__ PrefixTable t) {
   const Params& p = pp.p;
   const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
   const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
-  const int h = at % p.Hq, b = min(at / p.Hq, p.B - 1), g = h / G;
+  const int h = at % p.Hq, tok = at / p.Hq, b = min(tok / pp.n, p.B - 1), g = h / G;
   const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
   const int shared = q.pages > 0 ? q.splits : 0;
   size_t slot0 = 0, step = 0;  // of the prefix's
   if (shared) {
-    const int rows = q.count * G, part_rows = min(rows, kPrefixRows);
+    const int rows = q.count * pp.n * G, part_rows = min(rows, kPrefixRows);
     const int blocks = (rows + kPrefixRows - 1) / kPrefixRows;
-    const int r = (b - q.first) * G + h % G;
+    const int r = (tok - q.first * pp.n) * G + h % G;
     slot0 = q.part0 + ((size_t)g * shared * blocks + r / kPrefixRows) * part_rows + r % kPrefixRows;
     step = (size_t)blocks * part_rows;
   }
-  const size_t tail0 = t.parts + ((size_t)b * p.Hkv + g) * pp.splits * G + h % G;
+  const int tail_rows = pp.n * G;
+  const size_t tail0 =
+      t.parts + ((size_t)b * p.Hkv + g) * pp.splits * tail_rows + tok % pp.n * G + h % G;
   auto slot = [&](int s) {
-    return s < shared ? slot0 + s * step : tail0 + (size_t)(s - shared) * G;
+    return s < shared ? slot0 + s * step : tail0 + (size_t)(s - shared) * tail_rows;
   };
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
-  if (at >= p.B * p.Hq) return;  // (the warp's)
+  if (tok >= p.B * pp.n) return;  // (the warp's)
   const int L = __ldcg(p.seq_lens + b);
   const bool known = L >= 0 && (long long)L <= (long long)p.max_pages * p.P;
   constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
@@ -754,19 +764,20 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
 
 }  // namespace
 
-cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, int piece_pages,
-                          cudaStream_t s) {
+cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int n_tokens, int splits,
+                          int piece_pages, cudaStream_t s) {
   PrefixParams pp{};
   pp.p = p;
   const int G = p.Hq / p.Hkv;
   pp.log_g = G == 8 ? 3 : G / 2;
+  pp.n = n_tokens;
   pp.splits = splits;
   pp.piece_pages = piece_pages;
   CUtensorMap mq, m1, mk, mv;
-  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B};
+  const cuuint64_t qd[3] = {kHeadDim, (cuuint64_t)p.Hq, (cuuint64_t)p.B * n_tokens};
   const cuuint64_t qs[2] = {kHeadDim * 2, (cuuint64_t)p.Hq * kHeadDim * 2};
   const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G)};
-  const cuuint32_t q1[3] = {64, (cuuint32_t)G, 1};
+  const cuuint32_t q1[3] = {64, (cuuint32_t)G, (cuuint32_t)n_tokens};
   cudaError_t e = make_map(&mq, p.q, 3, qd, qs, qb);
   if (e != cudaSuccess) return e;
   if ((e = make_map(&m1, p.q, 3, qd, qs, q1)) != cudaSuccess) return e;
@@ -784,7 +795,7 @@ cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int splits, int
   if (e != cudaSuccess) return e;
   void* join_args[] = {&pp, const_cast<PrefixTable*>(&t)};
   constexpr int per = kPrefixJoinThreads / 32;
-  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * p.Hq + per - 1) / per)),
+  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * n_tokens * p.Hq + per - 1) / per)),
                     dim3(kPrefixJoinThreads), 0, s, join_args);
 }
 

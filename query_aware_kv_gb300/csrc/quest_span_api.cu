@@ -162,6 +162,15 @@ int check_groups(const quest_cache_t& c, const quest_prefix_group_t* groups, int
   return total == c.batch ? QUEST_OK : bad("the groups' counts must sum to the batch");
 }
 
+// The query tokens of a sequence: a tail's rows are one work item's.
+int check_query_tokens(const quest_cache_t& c, int n) {
+  if (n < 1) return bad("n_tokens must be >= 1");
+  if ((long long)n * group_of(c) <= kPrefixRows) return QUEST_OK;
+  return set_last_error(QUEST_ERR_UNSUPPORTED,
+                        "n_tokens * (num_q_heads / num_kv_heads) exceeds 128 (quest_window_prefill "
+                        "takes any number of query tokens)");
+}
+
 // Whether sharing pays.  Two launches and a job's start and end cost some 8 us, and sequences that
 // read a short prefix each for itself find it in L2: 16 sequences of 32 / 8 heads behind 512 tokens
 // take 9.7 us each for itself and 11.0 shared, 32 behind 256 tokens 13.3 and 17.8, 4 of 32 MHA heads
@@ -177,10 +186,11 @@ constexpr int kPrefixStart = 3;  // what a job's start and end cost, in tiles
 // How the prefixes are cut.  A job takes `per` K / V tiles, so that the jobs fill the SMs once, or
 // twice, ..., whichever takes the fewest tiles one after another.
 PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* groups, int n,
-                       const quest_opts_t* o) {
+                       int n_tokens, const quest_opts_t* o) {
   PrefixTable t{};
   t.n = n;
-  const int G = group_of(c), user = user_split(o);
+  const int user = user_split(o);
+  const long long token_rows = (long long)n_tokens * group_of(c);
   int first = 0, longest = 0;
   for (int i = 0; i < n; ++i) {
     const int pages = groups[i].count > 1 ? groups[i].prefix_tokens / c.page_size : 0;
@@ -196,7 +206,7 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   for (int i = 0; i < n; ++i) {
     tiles[i] = (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
     items[i] = (int)(c.num_kv_heads *
-                     (((long long)t.group[i].count * G + kPrefixRows - 1) / kPrefixRows));
+                     ((t.group[i].count * token_rows + kPrefixRows - 1) / kPrefixRows));
     most = std::max(most, tiles[i]);
   }
   auto ctas = [&](int per) {
@@ -234,7 +244,7 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
     if (g.pages > 0) {
       const long long mine = (long long)items[i] * g.splits;
       jobs += mine;
-      parts += mine * std::min<long long>(kPrefixRows, (long long)g.count * G);
+      parts += mine * std::min<long long>(kPrefixRows, g.count * token_rows);
     }
     t.most_pages = std::max(t.most_pages, c.max_pages - g.pages);
   }
@@ -258,8 +268,9 @@ int tail_splits(const quest_cache_t& c, const PrefixTable& t, const quest_opts_t
 }
 
 // Places of all shares; the kernels count them in 32 bits.
-int prefix_parts(const quest_cache_t& c, const PrefixTable& t, int splits, size_t* parts) {
-  const long long tails = (long long)c.batch * c.num_q_heads * splits;
+int prefix_parts(const quest_cache_t& c, const PrefixTable& t, int n_tokens, int splits,
+                 size_t* parts) {
+  const long long tails = (long long)c.batch * n_tokens * c.num_q_heads * splits;
   if (t.parts + tails + t.ctas >= INT_MAX)
     return set_last_error(QUEST_ERR_UNSUPPORTED, "the batch has too many rows for its splits");
   *parts = (size_t)(t.parts + tails);
@@ -451,33 +462,34 @@ int quest_narrow_decode_step(const quest_narrow_cache_t* cache, const void* q, c
 }
 
 size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefix_group_t* groups,
-                                   int32_t n_groups, const quest_opts_t* opts) {
+                                   int32_t n_groups, int32_t n_tokens, const quest_opts_t* opts) {
   if (check_cache_desc(cache)) return 0;
   if (cache->batch == 0) return span_layout(*cache, 0, opts).total;
-  if (check_groups(*cache, groups, n_groups)) return 0;
-  const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
+  if (check_query_tokens(*cache, n_tokens) || check_groups(*cache, groups, n_groups)) return 0;
+  const PrefixTable t = prefix_cut(*cache, groups, n_groups, n_tokens, opts);
   size_t parts = 0;
-  if (prefix_parts(*cache, t, tail_splits(*cache, t, opts), &parts)) return 0;
+  if (prefix_parts(*cache, t, n_tokens, tail_splits(*cache, t, opts), &parts)) return 0;
   return span_layout(*cache, 0, opts, 1, parts).total;
 }
 
-int quest_prefix_decode(const quest_cache_t* cache, const void* q,
+int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tokens,
                         const quest_prefix_group_t* groups, int32_t n_groups, void* out, float* lse,
                         void* ws, size_t ws_bytes, const quest_opts_t* opts,
                         quest_stream_t stream) {
   int rc = check_cache_desc(cache);
   if (rc || cache->batch == 0) return rc;
+  if ((rc = check_query_tokens(*cache, n_tokens))) return rc;
   if ((rc = check_groups(*cache, groups, n_groups))) return rc;
   if ((rc = check_io(q, out, lse))) return rc;
-  const PrefixTable t = prefix_cut(*cache, groups, n_groups, opts);
+  const PrefixTable t = prefix_cut(*cache, groups, n_groups, n_tokens, opts);
   SpanParams sp{};
   const int splits = tail_splits(*cache, t, opts);
   size_t parts = 0;
-  if ((rc = prefix_parts(*cache, t, splits, &parts))) return rc;
+  if ((rc = prefix_parts(*cache, t, n_tokens, splits, &parts))) return rc;
   const SpanLayout L = span_layout(*cache, 0, opts, 1, parts);
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   sp.p = make_params(*cache, ws, L, opts);
-  if (t.ctas == 0) {  // nothing is shared: every sequence on its own
+  if (t.ctas == 0 && n_tokens == 1) {  // nothing is shared: every sequence on its own
     sp.mode = kSpanDense;
     return run_span(sp, false, cache->max_pages, opts, q, out, lse, stream, "quest_prefix_decode");
   }
@@ -486,7 +498,7 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q,
   sp.p.lse = lse;
   if (opts && opts->wait_limit_ns > 0) sp.p.wait_limit_ns = opts->wait_limit_ns;
   if (opts) sp.p.debug_flags = opts->debug_flags;
-  return launched(launch_prefix(sp.p, t, splits, tail_piece(*cache, opts),
+  return launched(launch_prefix(sp.p, t, n_tokens, splits, tail_piece(*cache, opts),
                                 static_cast<cudaStream_t>(stream)),
                   "quest_prefix_decode");
 }

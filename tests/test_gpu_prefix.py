@@ -130,6 +130,57 @@ def test_long_prefixes_and_pools_past_4_gib():
     right(far, qq, out, lse)
 
 
+@pytest.mark.parametrize("pps", [0, 1, 6])
+@pytest.mark.parametrize("geom,n", [((4, 4, 16), 2), ((4, 4, 16), 128), ((8, 1, 32), 16), ((8, 1, 32), 3),
+                                    ((8, 2, 16), 5), ((8, 2, 16), 1), ((6, 3, 32), 33)], ids=str)
+@pytest.mark.parametrize("batch", ["one", "few", "groups", "short", "empty", "blocks"])
+def test_the_last_tokens_of_every_sequence(batch, geom, n, pps):
+    """Drafted tokens: each sees what comes before it, in the prefix and in the tail; rows at negative
+    positions see nothing."""
+    if n * len(BATCHES[batch]) > 100 and batch == "blocks":
+        pytest.skip("the same rows as the other batches, many times")
+    cache, groups = make(BATCHES[batch], *geom, seed=n)
+    qq = torch.randn((cache.batch, n, geom[0], 128), device="cuda").half()
+    o = q.opts(pages_per_split=pps)
+    ws = q.prefix_workspace(cache, groups, o, n)
+    out, lse = q.prefix_decode(cache, qq, groups, ws, o)
+    ok(ws)
+    assert out.shape == qq.shape and lse.shape == qq.shape[:3]
+    check(cache, qq, out, lse, 0, BIG, True)
+    if n == 1:
+        one, one_lse = run(cache, groups, qq[:, 0].contiguous(), pps or 1000)
+        if pps:
+            assert torch.equal(one, out[:, 0]) and torch.equal(one_lse, lse[:, 0])
+
+
+def test_drafted_tokens_and_odd_values():
+    """An infinity at a drafted token reaches the tokens from it on, no other row."""
+    cache, groups = make([(200, [230, 215])], 8, 2, 16, seed=4)
+    n = 12
+    qq = torch.randn((2, n, 8, 128), device="cuda").half()
+    o = q.opts(pages_per_split=4)
+    ws = q.prefix_workspace(cache, groups, o, n)
+    want, want_lse = (t.clone() for t in q.prefix_decode(cache, qq, groups, ws, o))
+    at = 230 - 5
+    cache.v_pool[int(cache.block_table[0, at // 16]), :, at % 16, 9] = INF
+    out, lse = q.prefix_decode(cache, qq, groups, ws, o)
+    ok(ws)
+    assert torch.equal(lse, want_lse)
+    sees = torch.zeros((2, n), dtype=torch.bool, device="cuda")
+    sees[0, n - 5:] = True
+    assert bool((out[..., 9][sees] == INF).all())
+    out[..., 9][sees] = want[..., 9][sees]
+    for b in range(2):
+        L = int(cache.seq_lens[b])
+        allowed = R.window_mask(L, n, 0, BIG, "cuda")
+        for h in range(8):
+            k, v = logical(cache, b, h // 4, "k_pool"), logical(cache, b, h // 4, "v_pool")
+            v = torch.where(torch.isinf(v), 0.0, v)
+            ref = R.attend(qq[b, :, h], k, v, allowed)
+            ref[0][sees[b], 9] = want[b, sees[b], h, 9].double()
+            R.assert_close(out[b, :, h], lse[b, :, h], ref, True, f"{b} {h}")
+
+
 def test_without_lse_and_into_given_outputs():
     cache, groups = make(BATCHES["few"], 8, 2, 16)
     qq = queries(cache)
@@ -410,6 +461,15 @@ def test_refusals():
     for bad in (qq.float(), qq[:, :4], qq.cpu(), qq.transpose(0, 1)):
         with pytest.raises((ValueError, TypeError)):
             q.prefix_decode(cache, bad, groups, ws)
+    with pytest.raises(q.QuestError, match="128"):
+        q.prefix_workspace(cache, groups, None, 33)
+    with pytest.raises(q.QuestError):
+        q.prefix_decode(cache, queries(cache)[:, None][:, :0], groups, ws)
+    with pytest.raises(ValueError):
+        q.PrefixPlan(cache, groups, ws, n_tokens=-1)
+    o = q.opts(pages_per_split=1)
+    with pytest.raises(q.QuestError):  # a workspace for one token
+        q.prefix_decode(cache, qq[:, None].repeat(1, 32, 1, 1), groups, q.prefix_workspace(cache, groups, o), o)
     nar = q.NarrowCache.allocate(9, 2, 16, cache.block_table, cache.seq_lens, 8)
     with pytest.raises(TypeError):
         q.PrefixPlan(nar, groups, ws)

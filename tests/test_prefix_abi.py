@@ -29,27 +29,31 @@ def test_bad_groups_are_refused(lib):
     for rows in ([], [(3, 0)], [(5, 0)], [(4, -1)], [(4, 64 * 16 + 1)], [(0, 0), (4, 0)], [(-4, 0), (8, 0)],
                  [(2 ** 31 - 1, 0)] * 4, [(1, 0)] * 129):
         arr, n = groups(*rows)
-        assert lib.quest_prefix_workspace_size(d, arr, n, None) == 0
-        code = lib.quest_prefix_decode(d, 256, arr, n, 256, None, 256, BIG, None, None)
+        assert lib.quest_prefix_workspace_size(d, arr, n, 1, None) == 0
+        code = lib.quest_prefix_decode(d, 256, 1, arr, n, 256, None, 256, BIG, None, None)
         assert code == (q.QUEST_ERR_UNSUPPORTED if len(rows) > 128 else q.QUEST_ERR_INVALID_ARG)
-    assert lib.quest_prefix_workspace_size(d, None, 1, None) == 0
+    assert lib.quest_prefix_workspace_size(d, None, 1, 1, None) == 0
 
 
 def test_bad_arguments_are_refused(lib):
     c = desc(batch=4, num_q_heads=8, num_kv_heads=2, max_pages=64)
     d, (arr, n) = ctypes.byref(c), groups((4, 500))
-    need = lib.quest_prefix_workspace_size(d, arr, n, None)
+    need = lib.quest_prefix_workspace_size(d, arr, n, 1, None)
     assert need > 0
     for args in ((None, 256, None), (256, None, None), (264, 256, None), (256, 264, None), (256, 256, 258)):
-        assert lib.quest_prefix_decode(d, args[0], arr, n, args[1], args[2], 256, BIG, None,
+        assert lib.quest_prefix_decode(d, args[0], 1, arr, n, args[1], args[2], 256, BIG, None,
                                        None) == q.QUEST_ERR_INVALID_ARG
-    assert lib.quest_prefix_decode(d, 256, arr, n, 256, None, 256, need - 1, None, None) == q.QUEST_ERR_WORKSPACE
-    assert lib.quest_prefix_decode(d, 256, arr, n, 256, None, None, need, None, None) == q.QUEST_ERR_WORKSPACE
-    assert lib.quest_prefix_decode(None, 256, arr, n, 256, None, 256, BIG, None, None) == q.QUEST_ERR_INVALID_ARG
+    assert lib.quest_prefix_decode(d, 256, 1, arr, n, 256, None, 256, need - 1, None, None) == q.QUEST_ERR_WORKSPACE
+    assert lib.quest_prefix_decode(d, 256, 1, arr, n, 256, None, None, need, None, None) == q.QUEST_ERR_WORKSPACE
+    assert lib.quest_prefix_decode(None, 256, 1, arr, n, 256, None, 256, BIG, None, None) == q.QUEST_ERR_INVALID_ARG
     odd = ctypes.byref(desc(batch=4, num_q_heads=8, num_kv_heads=2, max_pages=64, head_dim=64))
-    assert lib.quest_prefix_decode(odd, 256, arr, n, 256, None, 256, BIG, None, None) == q.QUEST_ERR_UNSUPPORTED
+    assert lib.quest_prefix_decode(odd, 256, 1, arr, n, 256, None, 256, BIG, None, None) == q.QUEST_ERR_UNSUPPORTED
+    for tokens, code in ((0, q.QUEST_ERR_INVALID_ARG), (-1, q.QUEST_ERR_INVALID_ARG), (33, q.QUEST_ERR_UNSUPPORTED)):
+        assert lib.quest_prefix_workspace_size(d, arr, n, tokens, None) == 0
+        assert lib.quest_prefix_decode(d, 256, tokens, arr, n, 256, None, 256, BIG, None, None) == code
+    assert lib.quest_prefix_workspace_size(d, arr, n, 32, None) >= need
     none = ctypes.byref(desc(batch=0))
-    assert lib.quest_prefix_decode(none, None, None, 0, None, None, None, 0, None, None) == q.QUEST_OK
+    assert lib.quest_prefix_decode(none, None, 1, None, 0, None, None, None, 0, None, None) == q.QUEST_OK
 
 
 def test_workspaces_stay_in_proportion(lib):
@@ -64,7 +68,7 @@ def test_workspaces_stay_in_proportion(lib):
         arr, n = groups(*rows)
         for pps in (0, 1, 300):
             o = ctypes.byref(q.opts(pages_per_split=pps))
-            size = lib.quest_prefix_workspace_size(d, arr, n, o)
+            size = lib.quest_prefix_workspace_size(d, arr, n, 1, o)
             heads = batch * G * hkv
             assert size > heads * 520  # a share a row at least
             least = heads * 130 * 4 * (65 + 64 if pps else 2 + 64)
