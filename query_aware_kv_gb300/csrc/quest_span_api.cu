@@ -171,13 +171,17 @@ int check_query_tokens(const quest_cache_t& c, int n) {
                         "takes any number of query tokens)");
 }
 
-// Whether sharing pays.  Two launches and a job's start and end cost some 8 us, and sequences that
-// read a short prefix each for itself find it in L2: 16 sequences of 32 / 8 heads behind 512 tokens
-// take 9.7 us each for itself and 11.0 shared, 32 behind 256 tokens 13.3 and 17.8, 4 of 32 MHA heads
-// behind 1024 tokens 14.3 and 15.1, behind 2048 tokens 4 of 32 / 8 heads 16.8 and 11.3.  Few rows
-// gain sooner (4 sequences of 8 kv heads behind 512 tokens 11.4 and 9.3): their span decode splits
-// them and joins.
-constexpr int kShareTokens = 1024, kShareTokensFewRows = 512, kFewRows = 32;
+// Whether sharing pays: a long prefix, or many tokens that sequences would read again.  Two launches
+// and a job's start and end cost some 8 us, and a short prefix comes from L2: 16 sequences of 32 / 8
+// heads behind 512 tokens take 9.6 us each for itself and 11.0 shared, 32 behind 256 tokens 13.3 and
+// 17.8, 4 of 32 MHA heads behind 1024 tokens 14.3 and 16.4; 32 of 32 / 8 heads behind 512 tokens 15.8
+// and 13.4, 4 behind 2048 12.3 and 11.3, 2 behind 8192 17.4 and 14.4.
+constexpr int kShareTokens = 1536, kShareTokensInAll = 12288;
+// Each for itself, 16 to 32 rows are split so that 128 CTAs have a part of eight pages or more, joined
+// by the rows' last CTAs: the span decode's own choice, clusters on most of the GPU, takes longer (32
+// rows of 612 tokens 8.5 us in four parts, 11.3 in clusters of four; 16 of 2248 tokens 10.4 in eight
+// and 15.8), fewer rows find room for their clusters (4 of 2148 tokens: 9.3, and 11.3 in 32 parts).
+constexpr int kSomeRows = 16, kSomeRowsMost = 32, kSomeRowsCtas = 128;
 constexpr int kPrefixJobs = 96;  // of the prefixes, in one go: five eighths of the SMs, the others
                                  // begin with tails (152: 45.2 us for 40.0 at 32 tails of 512 tokens
                                  // behind 32K, 42.2 for 34.7 at tails of 16)
@@ -192,16 +196,16 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
   const int user = user_split(o);
   const long long token_rows = (long long)n_tokens * group_of(c);
   int first = 0, longest = 0;
+  long long again = 0;  // tokens that would be read again
   for (int i = 0; i < n; ++i) {
     const int pages = groups[i].count > 1 ? groups[i].prefix_tokens / c.page_size : 0;
     t.group[i] = PrefixTable::Group{first, groups[i].count, pages, 1, 0, 0};
     first += groups[i].count;
     longest = std::max(longest, pages * c.page_size);
+    again += (groups[i].count - 1LL) * pages * c.page_size;
   }
-  const bool few = (long long)c.batch * c.num_kv_heads <= kFewRows;
-  const bool pays = longest >= (few ? kShareTokensFewRows : kShareTokens);
   for (int i = 0; i < n && !user; ++i)  // (where some group shares, any that has a tile does)
-    if (!pays || t.group[i].pages * c.page_size < kPrefixTokens) t.group[i].pages = 0;
+    if ((longest < kShareTokens && again < kShareTokensInAll) || t.group[i].pages * c.page_size < kPrefixTokens) t.group[i].pages = 0;
   int tiles[QUEST_MAX_PREFIX_GROUPS], items[QUEST_MAX_PREFIX_GROUPS], most = 0;
   for (int i = 0; i < n; ++i) {
     tiles[i] = (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
@@ -490,6 +494,13 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tok
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   sp.p = make_params(*cache, ws, L, opts);
   if (t.ctas == 0 && n_tokens == 1) {  // nothing is shared: every sequence on its own
+    const int rows = cache->batch * cache->num_kv_heads;
+    quest_opts_t some{};
+    if (!user_split(opts) && rows >= kSomeRows && rows <= kSomeRowsMost) {
+      const int parts = std::max(1, std::min(kSomeRowsCtas / rows, cache->max_pages / 8));
+      some.pages_per_split = (cache->max_pages + parts - 1) / parts;
+      opts = &some;
+    }
     sp.mode = kSpanDense;
     return run_span(sp, false, cache->max_pages, opts, q, out, lse, stream, "quest_prefix_decode");
   }
