@@ -71,13 +71,13 @@ __device__ __forceinline__ void cos_sin(uint64_t turns, long long pos, float m, 
   const uint32_t quarter = at + 0x20000000u >> 30;
   const float rest = (float)(int)(at - (quarter << 30)) * 4.656612873077393e-10f;  // 2^-31
   // sin(pi r) / r and (cos(pi r) - 1) / r^2 as polynomials in r^2, interpolated at the Chebyshev
-  // nodes of [0, 1/16]: with fp32 sums within 9e-8 of the sine and 6e-8 of the cosine for |r| <= 1/4.
+  // nodes of [0, 1/16]: with fp32 sums within 5e-8 of the sine and 6e-8 of the cosine for |r| <= 1/4.
   // (sincospif, which reduces its argument once more, made a block's table its longest part.)
   const float u = rest * rest;
   float a = fmaf(0x1.4bc85cp-4f, u, -0x1.32ca9ep-1f);
   a = fmaf(a, u, 0x1.466bbap+1f);
   a = fmaf(a, u, -0x1.4abbcep+2f);
-  a = fmaf(a, u, 0x1.921fb6p+1f) * rest;
+  a = fmaf(rest, 0x1.921fb6p+1f, rest * fmaf(a, u, -0x1.777a5cp-24f));  // (pi in two parts)
   float b = fmaf(0x1.db6492p-3f, u, -0x1.55cb98p+0f);
   b = fmaf(b, u, 0x1.03c1eap+2f);
   b = fmaf(b, u, -0x1.3bd3ccp+2f);
