@@ -904,35 +904,47 @@ def _rotary_fn(cache):
     return lib.quest_narrow_prefill_rotary if isinstance(cache, NarrowCache) else lib.quest_prefill_rotary
 
 
+def _spaced(t, name: str, dtype: torch.dtype, shape):
+    """(data pointer, strides of sequences and tokens) of heads t [B][n][H][128]."""
+    if type(t) is not torch.Tensor or t.shape != shape or t.dtype is not dtype:
+        _heads(t, name, shape)
+        if t.dtype != dtype:
+            raise TypeError("q, k and v must be of one type")
+    s = t.stride()
+    if s[3] != 1 or (s[2] != HEAD_DIM and shape[2] > 1):
+        _heads(t, name, shape)
+    return t.data_ptr(), (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0)
+
+
 def _rotary_write(cache, rope, q, k, v, ws, q_out, offsets, stream):
     """k, v [B][n][Hkv][128], q [B][n][Hq][128] or None."""
-    B, n, Hq, Hkv = cache.batch, k.shape[1], cache.desc.num_q_heads, cache.num_kv_heads
-    if k.dtype not in (torch.float16, torch.bfloat16):
+    B, n, Hq, Hkv = cache.desc.batch, k.shape[1], cache.desc.num_q_heads, cache.desc.num_kv_heads
+    dtype = k.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise TypeError("q, k and v must be float16 or bfloat16")
-    io = QuestRotaryIo(dtype=_DTYPES[k.dtype], n_tokens=n)
-    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t is None and name == "q":
-            continue
-        _heads(t, name, (B, n, H, HEAD_DIM))
-        if t.dtype != k.dtype:
-            raise TypeError("q, k and v must be of one type")
-        setattr(io, name, t.data_ptr())
-        s = getattr(io, name + "_stride")
-        s[0], s[1] = t.stride(0) if B > 1 else 0, t.stride(1) if n > 1 else 0
+    k_at, k_stride = _spaced(k, "k", dtype, (B, n, Hkv, HEAD_DIM))
+    v_at, v_stride = _spaced(v, "v", dtype, (B, n, Hkv, HEAD_DIM))
+    q_at, q_stride, to = None, (0, 0), None
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
     else:
+        shape = (B, n, Hq, HEAD_DIM)
+        q_at, q_stride = _spaced(q, "q", dtype, shape)
         if q_out is None:
-            q_out = torch.empty((B, n, Hq, HEAD_DIM), dtype=torch.float16, device=q.device)
-        _need(q_out, "q_out", torch.float16, (B, n, Hq, HEAD_DIM))
-        io.q_out = q_out.data_ptr()
+            q_out = torch.empty(shape, dtype=torch.float16, device=q.device)
+        else:
+            _need(q_out, "q_out", torch.float16, shape)
+        to = q_out.data_ptr()
     if offsets is not None:
         _need(offsets, "offsets", torch.int32, (B,))
-        io.position_offsets = offsets.data_ptr()
     _here(cache, ws, q, k, v, q_out, offsets)
-    _check(_rotary_fn(cache)(ctypes.byref(cache.desc), rope.ref, ctypes.byref(io), ws.data_ptr(),
-                             ws.numel(), _stream(stream)))
+    io = QuestRotaryIo(q_at, k_at, v_at, q_stride, k_stride, v_stride, _DTYPES[dtype], n, to,
+                       _ptr(offsets))
+    rc = _rotary_fn(cache)(ctypes.byref(cache.desc), rope.ref, ctypes.byref(io), ws.data_ptr(),
+                           ws.numel(), _stream(stream))
+    if rc:
+        _check(rc)
     return q_out
 
 
