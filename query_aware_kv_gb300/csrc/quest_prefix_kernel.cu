@@ -1,16 +1,17 @@
 // quest_prefix_kernel.cu - attention of the last token or tokens of every sequence where groups of
-// sequences share a prefix, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM, operands by
-// TMA).
+// sequences share a prefix, on the fifth-generation tensor cores (tcgen05, accumulators in TMEM,
+// operands by TMA).
 //
 // The work is a queue of jobs, each a run of pages that up to 128 rows attend over, a row being
-// (query token, query head): first the cuts of the prefixes, whose rows are a group's query tokens with
-// the G heads of a kv head (so that a prefix is read once for all of them), then every sequence's own
-// tokens behind its prefix (G rows a query token).  A CTA an SM takes jobs in turn; the lengths are on the device
-// only, so nobody could deal them out evenly beforehand.  Per 128 tokens of a job:
+// (query token, query head): first the cuts of the prefixes, whose rows are a group's query tokens
+// with the G heads of a kv head (so that a prefix is read once for all of them), then every
+// sequence's own tokens behind its prefix (G rows a query token).  A CTA an SM takes jobs in turn;
+// the lengths are on the device only, so nobody could deal them out evenly beforehand.  Per 128
+// tokens of a job:
 //   S = Q K^T,   P = 2^(S c - m + 8),   O += P V
 // with a running maximum m and sum of weights per row, which sees the tokens up to its own position:
-// of a prefix all of them but where its sequence is shorter.  What a job
-// leaves is a share (m, sum, O) per row; prefix_join_kernel joins a row's shares.
+// of a prefix all of them but where its sequence is shorter.  What a job leaves is a share (m, sum,
+// O) per row; prefix_join_kernel joins a row's shares.
 //
 // Eight softmax warps share a tile: warps 0-3 its first 64 tokens, warps 4-7 the other 64, a thread
 // a row of 64 scores in registers.  Either half has a maximum, a sum and an O of its own (two O in
@@ -143,6 +144,28 @@ __device__ __forceinline__ Cut cut_of(const PrefixTable& t, int n, int lg, int c
   return x;
 }
 
+// A wait for the next job, or for what others do with this one, which may be a whole job long: its
+// limit is a second at least, however short the waits for copies and products may be (one of those
+// that runs out ends this one too).
+__device__ __forceinline__ bool idle_wait(const Params& p, uint64_t* bar, uint32_t parity,
+                                          volatile int* give_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  long long t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*give_up) return false;
+    const long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > max(p.wait_limit_ns, kDefaultWaitNs)) {
+      *give_up = 1;
+      record_at<kSitePrefix>(p, QUEST_ERR_TIMEOUT, -1, -1);
+      return false;
+    }
+  }
+}
+
 // What brings a half's part of a softmax to the maximum M of both (as part_factor of the span
 // decode: a part without a weight is 0, one of NaN scores goes on, an infinite O stays one).
 __device__ __forceinline__ float half_factor(float m, float l, float M) {
@@ -208,6 +231,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, bar, parity, give_up)) != 0;
   };
+  auto idle = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, idle_wait(p, bar, parity, give_up)) != 0;
+  };
   auto length = [&](int seq) {
     const int L = p.seq_lens[seq];
     if (L >= 0 && (long long)L <= (long long)p.max_pages * P) return L;
@@ -216,7 +242,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   };
   // The k-th job of the CTA, for every warp but the one that writes them; false: there is none.
   auto take = [&](int k, Job& job) {
-    if (!wait(&bars.job_full[k & 1], (uint32_t)(k >> 1) & 1)) return false;
+    if (!idle(&bars.job_full[k & 1], (uint32_t)(k >> 1) & 1)) return false;
     job = bars.job[k & 1];
     __syncwarp();
     return job.n >= 0;
@@ -241,7 +267,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (k > 0) {
         // not before this CTA's fetches are through with the job before: taken any earlier (all
         // CTAs took their first three at the start) the jobs were dealt out, not queued for
-        if (!wait(&bars.want, (uint32_t)(k - 1) & 1)) break;
+        if (!idle(&bars.want, (uint32_t)(k - 1) & 1)) break;
         if (lane == 0) index = (int)(gridDim.x + atomicAdd(p.exited, 1u));
         index = __shfl_sync(0xffffffffu, index, 0);
       }
@@ -300,7 +326,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
       }
       if (job.n == 0) job.n = max(0, job.end - job.page0 * P + kTokens - 1) / kTokens;
-      if (k >= 2 && !wait(&bars.job_free[k & 1], (uint32_t)((k >> 1) - 1) & 1)) break;
+      if (k >= 2 && !idle(&bars.job_free[k & 1], (uint32_t)((k >> 1) - 1) & 1)) break;
       if (lane == 0) {
         bars.job[k & 1] = job;
         mbar_arrive(&bars.job_full[k & 1]);
@@ -315,7 +341,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     for (int k = 0; take(k, job); ++k) {
       give_back(k);
       if (job.n == 0) continue;
-      if (loads > 0 && !wait(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
+      if (loads > 0 && !idle(&bars.q_free, (uint32_t)(loads - 1) & 1)) break;
       if (elect_lane()) {
         // of a tail only its own rows: the others' scores may be anything
         mbar_arrive_expect_tx(&bars.q_full, job.shared ? kTile : kHeadDim * 2 * job.rows);
@@ -669,9 +695,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   if (warp == 10) tmem_free(tmem);
 }
 
-// The shares of a prefix and of a tail into out and lse: a warp a row (query token, query head), lane l
-// the dims 4 l .. 4 l + 3.  First come the prefix's splits
-// (of the row's work item, part_rows rows apart), then the tail's (of the row's kv head, a job's rows apart).
+// The shares of a prefix and of a tail into out and lse: a warp a row (query token, query head), lane
+// l the dims 4 l .. 4 l + 3.  First come the prefix's splits (of the row's work item, part_rows rows
+// apart), then the tail's (of the row's kv head, a job's rows apart).
 constexpr int kPrefixJoinThreads = 128;
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
     const __grid_constant__ PrefixParams pp, const __grid_constant__ PrefixTable t) {
@@ -790,12 +816,14 @@ cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int n_tokens, i
   const void* fn = p.P == 16 ? (const void*)prefix_kernel<16> : (const void*)prefix_kernel<32>;
   if ((e = ensure_smem(fn, Smem::total)) != cudaSuccess) return e;
   void* args[] = {&pp, const_cast<PrefixTable*>(&t), &mq, &m1, &mk, &mv};
-  e = launch_pdl(fn, dim3((unsigned)std::min(t.ctas + (long long)p.B * p.Hkv * splits, (long long)kPrefixSms)), dim3(kPrefixThreads), Smem::total, s,
-                 args);
+  const long long jobs = t.ctas + (long long)p.B * p.Hkv * splits;  // at most
+  e = launch_pdl(fn, dim3((unsigned)std::min<long long>(jobs, kPrefixSms)), dim3(kPrefixThreads),
+                 Smem::total, s, args);
   if (e != cudaSuccess) return e;
   void* join_args[] = {&pp, const_cast<PrefixTable*>(&t)};
   constexpr int per = kPrefixJoinThreads / 32;
-  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((p.B * n_tokens * p.Hq + per - 1) / per)),
+  const long long rows = (long long)p.B * n_tokens * p.Hq;
+  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((rows + per - 1) / per)),
                     dim3(kPrefixJoinThreads), 0, s, join_args);
 }
 

@@ -395,6 +395,22 @@ def test_a_wait_that_runs_out_ends_the_call(batch, pps):
     right(cache, qq, out, lse)
 
 
+def test_a_short_limit_is_no_limit_on_work():
+    """A limit far below a job's own time (uncut prefixes and tails) changes nothing."""
+    cache, groups = make([(60000, [60100] * 40), (30000, [90000, 30001])], 8, 1, 32)
+    qq = queries(cache)
+    o = q.opts(pages_per_split=16384, wait_limit_ns=200_000)
+    ws = q.prefix_workspace(cache, groups, o)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    out, lse = q.prefix_decode(cache, qq, groups, ws, o)
+    start.record()
+    q.prefix_decode(cache, qq, groups, ws, o, out=out, lse=lse)
+    end.record()
+    ok(ws)
+    assert start.elapsed_time(end) > 0.3
+    right(cache, qq, out, lse)
+
+
 @pytest.mark.parametrize("hq,hkv,P,rope", [(8, 2, 16, dict()), (4, 4, 32, dict(rotary_dim=64, interleaved=True))])
 def test_a_serving_step_from_projections(hq, hkv, P, rope):
     """A shared prompt written once with turned keys, every sequence's own question behind it, then
