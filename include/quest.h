@@ -593,12 +593,13 @@ int quest_narrow_prefill_rotary(const quest_narrow_cache_t* cache, const quest_r
  * ---- Prefixes that sequences share ---------------------------------------------------
  *
  * Attention of the last token of every sequence (or its last few, drafted ones) over the tokens up
- * to it, where groups of sequences begin with the same tokens.  Group i is the next groups[i].count sequences of the
- * batch (the counts sum to `batch`), whose first prefix_tokens tokens are the same; of these
- * the whole pages, prefix_tokens / page_size of them, are read once for the group, through the
- * block-table row of the group's first sequence.  The block-table rows of all sequences of the
- * group hold the same entries for these pages, whatever the sequences' own lengths (which row is
- * read is the call's choice).  A sequence shorter than its prefix sees its own seq_len tokens.
+ * to it, where groups of sequences begin with the same tokens.  Group i is the next
+ * groups[i].count sequences of the batch (the counts sum to `batch`), whose first prefix_tokens
+ * tokens are the same; of these the whole pages, prefix_tokens / page_size of them, are read once
+ * for the group, through the block-table row of the group's first sequence.  The block-table rows
+ * of all sequences of the group hold the same entries for these pages, whatever the sequences' own
+ * lengths (which row is read is the call's choice).  A sequence shorter than its prefix sees its
+ * own seq_len tokens.
  * prefix_tokens = 0: nothing is shared.
  */
 typedef struct quest_prefix_group {
@@ -607,8 +608,8 @@ typedef struct quest_prefix_group {
 } quest_prefix_group_t;
 #define QUEST_MAX_PREFIX_GROUPS 128
 
-/* Bytes of workspace of quest_prefix_decode with these groups, n_tokens and opts; 0 if the arguments are
- * invalid.  One workspace serves calls with the same groups, and no calls but
+/* Bytes of workspace of quest_prefix_decode with these groups, n_tokens and opts; 0 if the
+ * arguments are invalid.  One workspace serves calls with the same ones, and no calls but
  * quest_prefix_decode. */
 size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefix_group_t* groups,
                                    int32_t n_groups, int32_t n_tokens, const quest_opts_t* opts);
@@ -617,11 +618,12 @@ size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefi
  * n_tokens + i (their keys and values are written before); out: fp16 of the same shape; lse: fp32
  * [batch][n_tokens][num_q_heads] or NULL.  n_tokens * (num_q_heads / num_kv_heads) is at most 128
  * (QUEST_ERR_UNSUPPORTED).  groups: HOST array, copied by the call.  A row that sees no token (an
- * empty sequence, a negative position) gives out = 0, lse = -inf; NaN and
- * infinities as in windowed attention.  Where sharing would not pay (prefixes of a few hundred
- * tokens) every sequence reads all of its tokens itself.  A call may be captured into a graph; the
- * sequences may grow between calls.
- * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns, debug_flags. */
+ * empty sequence, a negative position) gives out = 0, lse = -inf; NaN and infinities as in windowed
+ * attention.  Where sharing would not pay (prefixes of a few hundred tokens) every sequence reads
+ * all of its tokens itself.  A call may be captured into a graph; the sequences may grow between
+ * calls.
+ * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns (of the waits for
+ * copies and products; others wait a second at least), debug_flags. */
 int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tokens,
                         const quest_prefix_group_t* groups, int32_t n_groups, void* out,
                         float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,

@@ -1037,7 +1037,7 @@ class RotaryPlan:
         if self._many and _current_device() != self._dev:
             _not_current()
         w, dev, kv = self._words, self._dev, self._kvshape
-        dtype = q.dtype
+        dtype = getattr(q, "dtype", None)
         if not (type(q) is torch.Tensor and type(k_new) is torch.Tensor and
                 type(v_new) is torch.Tensor and k_new.dtype is dtype and v_new.dtype is dtype and
                 (dtype is torch.float16 or dtype is torch.bfloat16) and q.shape == self._qshape and

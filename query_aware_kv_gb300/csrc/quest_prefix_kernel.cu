@@ -144,9 +144,9 @@ __device__ __forceinline__ Cut cut_of(const PrefixTable& t, int n, int lg, int c
   return x;
 }
 
-// A wait for the next job, or for what others do with this one, which may be a whole job long: its
-// limit is a second at least, however short the waits for copies and products may be (one of those
-// that runs out ends this one too).
+// A wait for the next job, or for what other warps do with this one, which may be a whole job long
+// (or a row that is taken again): its limit is a second at least, however short the waits for copies
+// and products may be (one of those that runs out ends this one too).
 __device__ __forceinline__ bool idle_wait(const Params& p, uint64_t* bar, uint32_t parity,
                                           volatile int* give_up) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           now = checked(next, i * PPT + lane);
           next = entry(i * PPT + 32 + lane);
         }
-        if (total >= kSlots && !(ok = wait(&bars.free[slot][kv], ph))) break;
+        if (total >= kSlots && !(ok = idle(&bars.free[slot][kv], ph))) break;
         const bool leader = elect_lane();
         if (leader) mbar_arrive_expect_tx(&bars.full[slot][kv], kTile);
 #pragma unroll
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!(ok = wait(&bars.p_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
-        if (i == 0 && done > 0 && !(ok = wait(&bars.o_free, (uint32_t)(done - 1) & 1))) break;
+        if (!(ok = idle(&bars.p_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
+        if (i == 0 && done > 0 && !(ok = idle(&bars.o_free, (uint32_t)(done - 1) & 1))) break;
         fence_after();
         if (elect_lane()) {
 #pragma unroll
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int least = __reduce_min_sync(0xffffffffu, pr);
       float m = -CUDART_INF_F, l = 0.f;
       for (int i = 0; i < job.n; ++i, ++t) {
-        if (!(ok = wait(&bars.s_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
+        if (!(ok = idle(&bars.s_full[t & 1], (uint32_t)(t >> 1) & 1))) break;
         if (some) {  // (without a query in the warp's rows their weights may be anything)
           fence_after();
           const uint32_t s_now = s_col + (t & 1) * kTokens;
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int dim0 = 64 * half;
       float M = -CUDART_INF_F, Z = 0.f, f0 = 0.f, f1 = 0.f;
       if (job.n > 0) {
-        if (!(ok = wait(&bars.o_full, (uint32_t)done & 1))) break;
+        if (!(ok = idle(&bars.o_full, (uint32_t)done & 1))) break;
         ++done;
         fence_after();
         if (some) {
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           stash[half * kRows + row] = make_float2(m, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.pair[warp & 3]);
-          if (!(ok = wait(&bars.pair[warp & 3], pairs & 1))) break;
+          if (!(ok = idle(&bars.pair[warp & 3], pairs & 1))) break;
           ++pairs;
           const float2 other = stash[(half ^ 1) * kRows + row];
           M = fmaxf(m, other.x);

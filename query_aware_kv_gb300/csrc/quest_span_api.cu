@@ -205,7 +205,9 @@ PrefixTable prefix_cut(const quest_cache_t& c, const quest_prefix_group_t* group
     again += (groups[i].count - 1LL) * pages * c.page_size;
   }
   for (int i = 0; i < n && !user; ++i)  // (where some group shares, any that has a tile does)
-    if ((longest < kShareTokens && again < kShareTokensInAll) || t.group[i].pages * c.page_size < kPrefixTokens) t.group[i].pages = 0;
+    if ((longest < kShareTokens && again < kShareTokensInAll) ||
+        t.group[i].pages * c.page_size < kPrefixTokens)
+      t.group[i].pages = 0;
   int tiles[QUEST_MAX_PREFIX_GROUPS], items[QUEST_MAX_PREFIX_GROUPS], most = 0;
   for (int i = 0; i < n; ++i) {
     tiles[i] = (t.group[i].pages * c.page_size + kPrefixTokens - 1) / kPrefixTokens;
@@ -497,8 +499,8 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tok
     const int rows = cache->batch * cache->num_kv_heads;
     quest_opts_t some{};
     if (!user_split(opts) && rows >= kSomeRows && rows <= kSomeRowsMost) {
-      const int parts = std::max(1, std::min(kSomeRowsCtas / rows, cache->max_pages / 8));
-      some.pages_per_split = (cache->max_pages + parts - 1) / parts;
+      const int pieces = std::max(1, std::min(kSomeRowsCtas / rows, cache->max_pages / 8));
+      some.pages_per_split = (cache->max_pages + pieces - 1) / pieces;
       opts = &some;
     }
     sp.mode = kSpanDense;

@@ -411,6 +411,23 @@ def test_a_short_limit_is_no_limit_on_work():
     right(cache, qq, out, lse)
 
 
+def test_a_short_limit_is_no_limit_on_rows_taken_again():
+    """An infinite value makes every row of a job be taken again, a token at a time, while the CTA's
+    other warps are at its next job (the prefixes' jobs alone are more than there are CTAs)."""
+    cache, groups = make([(60000, [60030] * 4)] * 20, 64, 8, 32)
+    at = int(cache.block_table[0, 3])
+    cache.v_pool[at, :, 5, 9] = INF
+    qq = queries(cache)
+    o = q.opts(pages_per_split=16384, wait_limit_ns=300_000)
+    ws = q.prefix_workspace(cache, groups, o)
+    out, lse = q.prefix_decode(cache, qq, groups, ws, o)
+    ok(ws)
+    assert bool((out[:4, :, 9] == INF).all()) and bool(torch.isfinite(out[4:]).all())
+    cache.v_pool[at, :, 5, 9] = 0
+    out[..., 9] = run(cache, groups, qq, 16384)[0][..., 9]
+    right(cache, qq, out, lse)
+
+
 @pytest.mark.parametrize("hq,hkv,P,rope", [(8, 2, 16, dict()), (4, 4, 32, dict(rotary_dim=64, interleaved=True))])
 def test_a_serving_step_from_projections(hq, hkv, P, rope):
     """A shared prompt written once with turned keys, every sequence's own question behind it, then

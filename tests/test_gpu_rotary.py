@@ -309,6 +309,7 @@ def test_refusals():
                 lambda: q.append_rotary(c, rope, qq, k, v, ws),
                 lambda: q.RotaryPlan(c, rope, ws).append(qq[:, 0], k[:, 0], v[:, 0].bfloat16()),
                 lambda: q.RotaryPlan(c, rope, ws).append(qq[:, 0], k[:, 0, :1], v[:, 0]),
+                lambda: q.RotaryPlan(c, rope, ws).append(None, k[:, 0], v[:, 0]),
                 lambda: q.RotaryPlan(c, rope, ws).append(*(t[:, 0].float() for t in (qq, k, v)))):
         with pytest.raises((ValueError, TypeError, q.QuestError)):
             bad()
