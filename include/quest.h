@@ -534,8 +534,8 @@ int quest_window_prefill(const quest_cache_t* cache, const void* q, int32_t n_to
 typedef struct quest_rope {
     int32_t rotary_dim;  /* 8, 16, ..., 128 */
     int32_t interleaved; /* 0 or 1 */
-    float magnitude;     /* m */
-    int32_t reserved;
+    float magnitude;     /* m, */
+    float magnitude_low; /* and what it has beyond fp32 */
     uint64_t turns[64];  /* f_i / (2 pi) mod 1, in 2^-64ths */
 } quest_rope_t;
 

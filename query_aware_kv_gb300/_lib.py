@@ -87,7 +87,7 @@ class QuestPrefixGroup(ctypes.Structure):
 
 class QuestRope(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("magnitude_low", ctypes.c_float),
                 ("turns", ctypes.c_uint64 * 64)]
 
 

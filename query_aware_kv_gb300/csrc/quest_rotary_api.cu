@@ -24,7 +24,8 @@ bool rotary_dim_ok(int d) { return d >= 8 && d <= kHeadDim && d % 8 == 0; }
 
 int check_rope(const quest_rope_t* rope) {
   if (!rope) return bad("rope is NULL");
-  if (!rotary_dim_ok(rope->rotary_dim) || (rope->interleaved & ~1) || !std::isfinite(rope->magnitude))
+  if (!rotary_dim_ok(rope->rotary_dim) || (rope->interleaved & ~1) ||
+      !std::isfinite(rope->magnitude) || !std::isfinite(rope->magnitude_low))
     return bad("rope: not filled by quest_rope_init");
   return QUEST_OK;
 }
@@ -73,6 +74,7 @@ int quest_rope_init(quest_rope_t* rope, int32_t rotary_dim, int32_t interleaved,
   rope->rotary_dim = rotary_dim;
   rope->interleaved = interleaved;
   rope->magnitude = (float)magnitude;
+  rope->magnitude_low = (float)(magnitude - (double)rope->magnitude);
   // 1 / (2 pi) as the sum of two doubles; the product with f as hi + lo, its whole turns dropped
   const double r_hi = 0x1.45f306dc9c883p-3, r_lo = -0x1.6b01ec5417056p-57;
   for (int i = 0; i < rotary_dim / 2; ++i) {

@@ -9,7 +9,8 @@
 // Angles: f_i comes as a fraction of a turn in 2^-64 units, so t f_i mod 1 is one 64-bit integer
 // product whose overflow drops the whole turns exactly, at any 32-bit position.  Its upper 32
 // bits (an angle within 2^-32 of a turn, 1.5e-9) lose their quarter turns, the rest goes through
-// polynomials; the turn itself is in fp32, rounded once to the output's type.
+// polynomials whose sums have two parts; the turn itself is in fp32, rounded once to the output's
+// type.
 //
 // Bound by DRAM: a value costs its read and its write, and 3 flops.  Measured: 8192 tokens of 40
 // fp16 heads out of rows of 48 in 28 us (168 MB, 6.0 TB/s), 1999 tokens of 24 bf16 heads in 4.9 (25
@@ -63,28 +64,40 @@ template <> struct Four<float> {
 };
 
 // ---- the turn of a position
-__device__ __forceinline__ void cos_sin(uint64_t turns, long long pos, float m, float& c, float& s) {
+// m cos and m sin of the angle, the two at half a unit in the last place and little more: what is lost
+// beside the last rounding is kept as a second fp32 number up to it (a cosine that is off by twice as
+// much moves twice as many of the turned values to the neighbour of the right fp16 number).
+__device__ __forceinline__ void cos_sin(const quest_rope_t& rope, int i, long long pos, float& c,
+                                        float& s) {
   // (a product modulo 2^64 is the same for signed and unsigned factors)
-  const uint32_t at = (uint32_t)(turns * (uint64_t)pos >> 32);
-  // the nearest quarter turn and the rest, within an eighth of a turn, which keeps fp32's relative
-  // precision (of the whole angle as one fp32 number, 2^-25 of half a turn would be lost)
+  const uint32_t at = (uint32_t)(rope.turns[i] * (uint64_t)pos >> 32);
+  // the nearest quarter turn and the rest, within an eighth of a turn, as r + r_low half turns
   const uint32_t quarter = at + 0x20000000u >> 30;
-  const float rest = (float)(int)(at - (quarter << 30)) * 4.656612873077393e-10f;  // 2^-31
-  // sin(pi r) / r and (cos(pi r) - 1) / r^2 as polynomials in r^2, interpolated at the Chebyshev
-  // nodes of [0, 1/16]: with fp32 sums within 5e-8 of the sine and 6e-8 of the cosine for |r| <= 1/4.
-  // (sincospif, which reduces its argument once more, made a block's table its longest part.)
-  const float u = rest * rest;
-  float a = fmaf(0x1.4bc85cp-4f, u, -0x1.32ca9ep-1f);
-  a = fmaf(a, u, 0x1.466bbap+1f);
+  const int rest = (int)(at - (quarter << 30));
+  const float r = (float)rest * 0x1p-31f, r_low = (float)(rest - (int)(float)rest) * 0x1p-31f;
+  const float u = r * r, u_low = fmaf(2.f * r, r_low, fmaf(r, r, -u));
+  // sin(pi r) = r (pi + u A(u)) and cos(pi r) = 1 + u (B0 + u B(u)): A and B0 + u B interpolated at
+  // the Chebyshev nodes of [0, 1/16], within 1e-11 and 2e-10; pi and B0 in two parts.  (sincospif,
+  // which reduces its argument once more, made a block's table its longest part.)
+  constexpr float kPi = 0x1.921fb6p+1f, kPiLow = -0x1.777a5cp-24f;
+  constexpr float kB0 = -0x1.3bd3ccp+2f, kB0Low = -0x1.313d3p-23f;
+  float a = fmaf(0x1.4cb762p-4f, u, -0x1.32ce1ep-1f);
+  a = fmaf(a, u, 0x1.466bc2p+1f);
   a = fmaf(a, u, -0x1.4abbcep+2f);
-  a = fmaf(rest, 0x1.921fb6p+1f, rest * fmaf(a, u, -0x1.777a5cp-24f));  // (pi in two parts)
+  a = fmaf(a, u, kPiLow);
+  const float p = r * kPi;
+  const float p_low = fmaf(r, a, fmaf(r_low, kPi, fmaf(r, kPi, -p)));
   float b = fmaf(0x1.db6492p-3f, u, -0x1.55cb98p+0f);
   b = fmaf(b, u, 0x1.03c1eap+2f);
-  b = fmaf(b, u, -0x1.3bd3ccp+2f);
-  b = fmaf(b, u, 1.f);
-  const float x = quarter & 1u ? a : b, y = quarter & 1u ? b : a;
-  c = (quarter + 1u & 2u ? -x : x) * m;
-  s = (quarter & 2u ? -y : y) * m;
+  const float t = u * kB0, q = 1.f + t;
+  const float q_low =
+      fmaf(u, fmaf(b, u, kB0Low), fmaf(u_low, kB0, fmaf(u, kB0, -t))) + ((1.f - q) + t);
+  const float m = rope.magnitude, m_low = rope.magnitude_low;
+  const float sine = fmaf(p, m, fmaf(p, m_low, p_low * m));
+  const float cosine = fmaf(q, m, fmaf(q, m_low, q_low * m));
+  const float x = quarter & 1u ? sine : cosine, y = quarter & 1u ? cosine : sine;
+  c = quarter + 1u & 2u ? -x : x;
+  s = quarter & 2u ? -y : y;
 }
 
 // Lane c's two pieces (offsets in dims), and whether they are turned.
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     cs[i] = make_float2(1.f, 0.f);
-    if (at.turned) cos_sin(r.rope.turns[4 * c + i], pos, r.rope.magnitude, cs[i].x, cs[i].y);
+    if (at.turned) cos_sin(r.rope, 4 * c + i, pos, cs[i].x, cs[i].y);
     if (r.transposed) cs[i].y = -cs[i].y;
   }
 #pragma unroll 1
@@ -247,10 +260,9 @@ __device__ __forceinline__ void fill_table(const quest_rope_t& rope, long long p
                                            float2 (*table)[64]) {
   const int i = threadIdx.x & 63;
   if (i < rope.rotary_dim / 2) {
-    const uint64_t turns = rope.turns[i];
     for (int r = threadIdx.x >> 6; r < rows; r += NT / 64) {
       float c, s;
-      cos_sin(turns, pos + r, rope.magnitude, c, s);
+      cos_sin(rope, i, pos + r, c, s);
       table[r][i] = make_float2(c, s);
     }
   }
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(kAppendThreads) rotary_append_kernel(
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (at.turned)
-      cos_sin(w.rope.turns[4 * c + i], (long long)L + offset, w.rope.magnitude, cs[i].x, cs[i].y);
+      cos_sin(w.rope, 4 * c + i, (long long)L + offset, cs[i].x, cs[i].y);
 #pragma unroll 1
   for (; u < rows; u += kAppendThreads / 16) {
     const bool is_k = u < p.Hkv, is_v = !is_k && u < kv;

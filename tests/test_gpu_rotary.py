@@ -56,6 +56,24 @@ def test_rotate_is_exact_at_far_and_negative_positions():
     R.check(q.rotate(r, x, pos), *R.turned(r, x, pos))
 
 
+@pytest.mark.parametrize("name", ["plain", "yarn", "bands", "own"])
+def test_cosines_and_sines_lose_only_their_last_rounding(name):
+    """Of pairs (1, 0) the turn is m cos and m sin themselves.  Next to half a unit in the last place
+    (2^-24 of the value) there are the angle's cut (1.5e-9), and in the sine products of at most a
+    tenth that are rounded three times (1.8e-8): below 2e-8 together, and little in the mean."""
+    r, g = ROPES[name](), gen(5)
+    a, b = R.pairs(r)
+    pos = torch.randint(-2 ** 20, 2 ** 20, (2000,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.zeros((2000, 1, D), device="cuda")
+    x[..., a] = 1.0
+    y = q.rotate(r, x, pos)[:, 0].double().cpu()
+    t, m = R.angles(r, pos.cpu()), r.magnitude
+    for got, want in ((y[:, a], torch.cos(t) * m), (y[:, b], torch.sin(t) * m)):
+        far, nearest = (got - want).abs(), (want.float().double() - want).abs()
+        assert bool((far <= 2.0 ** -24 * want.abs() + 2e-8 * abs(m)).all())
+        assert float(far.square().mean().sqrt()) <= 1.1 * float(nearest.square().mean().sqrt()) + 1.5e-9
+
+
 def test_rotate_takes_strided_rows_and_writes_in_place():
     r, g = q.Rope(), gen(3)
     rows = normal(g, 2, 9, 12, D)

@@ -40,6 +40,14 @@ def test_turns_are_exact():
     assert r.rotary_dim == 128 and list(r.inv_freq) == f
 
 
+def test_a_magnitude_has_two_parts():
+    for m in (1.0, 0.75, 0.1 * math.log(8) + 1, -1 / 3, 1e-30):
+        d = q.Rope(magnitude=m).desc
+        assert d.magnitude == ctypes.c_float(m).value
+        assert abs(d.magnitude + d.magnitude_low - m) <= abs(m) * 2.0 ** -48 + 1e-45
+    assert q.Rope().desc.magnitude_low == 0.0
+
+
 def test_scalings():
     base, m = q.rope_frequencies(64, 10000.0)
     assert m == 1.0 and base[0] == 1.0 and base[16] == pytest.approx(0.01, rel=1e-14)
