@@ -27,8 +27,8 @@
 // 2.2 us with its last tile, of which 0.8 are the share on its way out, and its loads go on
 // meanwhile.  Measured: 16 sequences of 32 MHA heads with 2K tokens of their own behind 8K shared ones
 // 80 us (483 MB: 6.0 TB/s, 6.7 in the jobs' launch), 32 sequences of 32 / 8 heads with 512 behind
-// 32K 41 us (177 MB), of which 3 are the first lengths, pages and tiles, some 4 the last jobs, which
-// not every CTA has, and 6 the join with its launch.
+// 32K 40 us (177 MB), of which 3 are the first lengths, pages and tiles, some 4 the last jobs, which
+// not every CTA has, and 5 the join with its launch.
 //
 // (Two chains a CTA, which took whole tiles in turn with an issue warp each, faulted on long runs of
 // full row blocks for a reason that was not found, and are not here; tails on the span decode, in a
@@ -695,16 +695,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   if (warp == 10) tmem_free(tmem);
 }
 
-// The shares of a prefix and of a tail into out and lse: a warp a row (query token, query head), lane
-// l the dims 4 l .. 4 l + 3.  First come the prefix's splits (of the row's work item, part_rows rows
+// The shares of a prefix and of a tail into out and lse: a block of one warp a row (query token, query
+// head), lane l the dims 4 l .. 4 l + 3.  Such blocks wait beside the jobs' CTA, seven an SM: 0.9 us
+// less than blocks of four, of which one fits (40.4 and 41.4 us at 32 tails behind 32K).  First come the prefix's splits (of the row's work item, part_rows rows
 // apart), then the tail's (of the row's kv head, a job's rows apart).
-constexpr int kPrefixJoinThreads = 128;
-__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
+__global__ void __launch_bounds__(32) prefix_join_kernel(
     const __grid_constant__ PrefixParams pp, const __grid_constant__ PrefixTable t) {
   const Params& p = pp.p;
-  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
-  const int at = (int)blockIdx.x * (kPrefixJoinThreads / 32) + (int)(threadIdx.x >> 5);
-  const int h = at % p.Hq, tok = at / p.Hq, b = min(tok / pp.n, p.B - 1), g = h / G;
+  const int lane = threadIdx.x, G = p.Hq / p.Hkv, at = (int)blockIdx.x;
+  const int h = at % p.Hq, tok = at / p.Hq, b = tok / pp.n, g = h / G;
   const PrefixTable::Group& q = t.group[t.group_of_seq(b)];
   const int shared = q.pages > 0 ? q.splits : 0;
   size_t slot0 = 0, step = 0;  // of the prefix's
@@ -723,8 +722,7 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(
   };
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.exited = 0u;  // the queue, for the next call
-  if (tok >= p.B * pp.n) return;  // (the warp's)
+  if (at == 0 && lane == 0) *p.exited = 0u;  // the queue, for the next call
   const int L = __ldcg(p.seq_lens + b);
   const bool known = L >= 0 && (long long)L <= (long long)p.max_pages * p.P;
   constexpr int kOf = 2 * kPrefixSplits / 32;  // shares of a lane
@@ -821,10 +819,8 @@ cudaError_t launch_prefix(const Params& p, const PrefixTable& t, int n_tokens, i
                  Smem::total, s, args);
   if (e != cudaSuccess) return e;
   void* join_args[] = {&pp, const_cast<PrefixTable*>(&t)};
-  constexpr int per = kPrefixJoinThreads / 32;
   const long long rows = (long long)p.B * n_tokens * p.Hq;
-  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)((rows + per - 1) / per)),
-                    dim3(kPrefixJoinThreads), 0, s, join_args);
+  return launch_pdl((const void*)prefix_join_kernel, dim3((unsigned)rows), dim3(32), 0, s, join_args);
 }
 
 }  // namespace quest
