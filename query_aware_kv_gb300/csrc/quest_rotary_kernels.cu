@@ -362,6 +362,12 @@ __device__ __forceinline__ void turn_rows(const T* in, long long in_tok, __half*
     }
   }
 }
+// Rows of 128 16-bit values on their way to L2 (while the block makes its table).
+template <class T>
+__device__ __forceinline__ void prefetch_rows(const T* in, long long in_tok, int rows, int lane) {
+  for (int i = lane; i < 2 * rows; i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(in + (i >> 1) * in_tok + (i & 1) * 64));
+}
 template <class T>
 __device__ __forceinline__ void copy_rows(const T* in, long long in_tok, __half* out, int rows,
                                           int lane) {
@@ -387,7 +393,7 @@ __device__ __forceinline__ void copy_rows(const T* in, long long in_tok, __half*
 // position's 64 pairs are taken once for its four (eight) heads.  (Blocks of a head a
 // warp, or of eight warps, fill more tables and more waves: 519 tokens of four sequences into a
 // narrow cache took 18 and 19 us instead of 14.)
-// Measured: 32K tokens of 32 query and 32 kv heads 250 us (1.64 GB, 6.6 TB/s).
+// Measured: 32K tokens of 32 query and 32 kv heads 245 us (1.64 GB, 6.7 TB/s).
 template <class T, int P>
 __device__ __forceinline__ void queries(const WriteParams& w, int b, int h0, int t0, int t1, int L,
                                         const Pieces& at, const float2 (*table)[64], int lane) {
@@ -398,6 +404,25 @@ __device__ __forceinline__ void queries(const WriteParams& w, int b, int h0, int
                         w.q_tok, w.q_out + (((size_t)b * w.n + (t0 - L)) * p.Hq + h) * kHeadDim,
                         (size_t)p.Hq * kHeadDim, t1 - t0, at, w.rope.interleaved != 0, table, lane,
                         none);
+}
+
+// What a warp of a block reads of tokens [t0, t1): its kv head's keys and values, or its queries.
+// (Of pages of 16 tokens: 32K tokens of 32 heads 245 us for 250.  Twice as much a block is too much at
+// once: 271 for 253 at 32 tokens; and the narrow pages' kernel took 276 for 256 and 317 for 286.)
+template <class T>
+__device__ __forceinline__ void prefetch_tokens(const WriteParams& w, int b, int t0, int t1, int L,
+                                                int kv_blocks, int warp, int lane) {
+  if ((int)blockIdx.x >= kv_blocks) {
+    const int h0 = ((int)blockIdx.x - kv_blocks) * kQHeads + 2 * warp;
+    for (int h = h0; h < min(h0 + 2, w.p.Hq); ++h)
+      prefetch_rows(static_cast<const T*>(w.q) + b * w.q_seq + (t0 - L) * w.q_tok + h * kHeadDim,
+                    w.q_tok, t1 - t0, lane);
+  } else if (const int g = (int)blockIdx.x * kWriteWarps + warp; g < w.p.Hkv) {
+    prefetch_rows(static_cast<const T*>(w.k) + b * w.k_seq + (t0 - L) * w.k_tok + g * kHeadDim,
+                  w.k_tok, t1 - t0, lane);
+    prefetch_rows(static_cast<const T*>(w.v) + b * w.v_seq + (t0 - L) * w.v_tok + g * kHeadDim,
+                  w.v_tok, t1 - t0, lane);
+  }
 }
 
 template <class T, int P>
@@ -418,6 +443,7 @@ __global__ void __launch_bounds__(kWriteThreads) rotary_prefill_kernel(
   const int t0 = max(page * P, L), t1 = min(page * P + P, L + n);  // new tokens of this page
   if (t0 >= t1) return;  // (all of these are the block's)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hw = lane >> 4;
+  if constexpr (P == 16) prefetch_tokens<T>(w, b, t0, t1, L, kv_blocks, warp, lane);
   fill_table<kWriteThreads>(w.rope, (long long)t0 + (w.offsets ? w.offsets[b] : 0), t1 - t0, table);
   __syncthreads();
   const Pieces at = pieces(w.rope, lane & 15);
@@ -513,10 +539,11 @@ __device__ __forceinline__ void turn_page(const WriteParams& w, int b, int g, in
 // takes first.  A chunk that does not fit, or that meets an unmapped page, leaves the open page and
 // its box alone (the launch that advances the lengths finds the same).
 //
-// Registers are bounded for warps' sake: 32K tokens of 32 kv heads take 163 us so at page size 16
-// (169 at the compiler's 96 registers) and 176 at 32, whose warps hold 32 rows; blocks of eight
-// warps, four for the keys and four for the values, took 177 and 211.  (Without the turn 134 and 141:
-// the rest is its instructions, between the loads of a page and its stores.)
+// Registers are bounded for warps' sake: 32K tokens of 32 kv heads take 170 us so at page size 16 and
+// 182 at 32, whose warps hold 32 rows.  With cosines in one part these were 163 and 176, then 169 at the
+// compiler's 96 registers, and 177 and 211 in blocks of eight warps, four for the keys and four for the
+// values.  (Without the turn 134 and 141: the rest is its instructions, between the loads of a page and
+// its stores.)
 template <class T, int P>
 __global__ void __launch_bounds__(kWriteThreads, P == 16 ? 7 : 4) rotary_pages_kernel(
     const __grid_constant__ WriteParams w) {
