@@ -535,8 +535,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             for (int u = 0; u < 2; ++u) best[u] = max3(best[u], s[e + u], s[e + 2 + u]);
           const float top = fmaxf(best[0], best[1]) * p.qscale;
           // The reference moves only when a row exceeds it by 2^kLazy; the warp's rows move theirs
-          // together, l and O with them.
-          if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          // together, l and O with them.  Lanes without a query have no say: of a tail only its own
+          // rows were fetched, the others hold what the CTA's last job left there, which the order
+          // that the jobs were taken in decides.
+          if (__any_sync(0xffffffffu, mine && top > m + kLazy)) {
             const float mn = fmaxf(m, top);
             const float f = mn == -CUDART_INF_F ? 1.f : ex2(m - mn);
             m = mn;

@@ -1,0 +1,67 @@
+"""Shared-prefix attention: what a job of the queue may and may not depend on."""
+import pytest
+import torch
+
+import query_aware_kv_gb300 as q
+from test_gpu_prefix import make, queries
+from test_gpu_window import ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(0)
+
+
+def growing(cache, groups, by=4.0):
+    """Keys of a sequence's own tokens that grow with their position: the maxima move after a job's
+    first tile too."""
+    P, b = cache.page_size, 0
+    for count, prefix in groups:
+        for _ in range(count):
+            own = cache.block_table[b, prefix // P:].long()
+            up = 0.5 + by * torch.arange(len(own), device="cuda") / len(own)
+            cache.k_pool[own] = (cache.k_pool[own].float() * up[:, None, None, None]).half()
+            b += 1
+    return cache
+
+
+@pytest.mark.parametrize("geom,n", [((32, 8, 16), None), ((8, 8, 32), None), ((16, 8, 16), 3)], ids=str)
+def test_the_same_bits_every_time_with_default_splits(geom, n):
+    """Tails of several tiles behind several prefixes, more jobs than CTAs, which take them in any
+    order: no bit of a result depends on what a CTA did before."""
+    G = geom[0] // geom[1]
+    cache, groups = make([(2048, [2048 + 700 + 17 * i for i in range(128 // G)]),
+                          (1600, [1600 + 400 + 9 * i for i in range(20)])], *geom)
+    growing(cache, groups)
+    shape = (cache.batch, geom[0], 128) if n is None else (cache.batch, n, geom[0], 128)
+    # (the rows of either group move their maxima at other tiles)
+    qq = torch.randn(shape, device="cuda") * torch.linspace(0.2, 6, cache.batch, device="cuda").view(-1, *[1] * (len(shape) - 1))
+    qq = qq.half()
+    ws = q.prefix_workspace(cache, groups, None, n or 1)
+    plan = q.PrefixPlan(cache, groups, ws, n_tokens=n)
+    first = [t.clone() for t in plan.decode(qq)]
+    for _ in range(40):
+        out, lse = plan.decode(qq)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    ok(ws)
+
+
+@pytest.mark.parametrize("geom", [(32, 8, 16), (8, 8, 32)], ids=str)
+def test_a_sequence_does_not_depend_on_the_batch_beside_it(geom):
+    """Large queries of a prefix's rows stay in shared memory behind a tail's few rows: the tails of
+    the sequences beside that group are the same bits whatever they are."""
+    G = geom[0] // geom[1]
+    cache, groups = make([(2048, [2100] * (128 // G)), (0, [1100 + 50 * i for i in range(24)])], *geom)
+    growing(cache, groups, 2.0)
+    alone = slice(128 // G, None)
+    qq = queries(cache)
+    plan = q.PrefixPlan(cache, groups, q.prefix_workspace(cache, groups))
+    want = [t[alone].clone() for t in plan.decode(qq)]
+    for scale in (0.0, 8.0, 60.0):
+        other = qq.clone()
+        other[:128 // G] = torch.randn_like(other[:128 // G]) * scale
+        for _ in range(8):
+            out, lse = plan.decode(other)
+            assert torch.equal(out[alone], want[0]) and torch.equal(lse[alone], want[1]), scale
