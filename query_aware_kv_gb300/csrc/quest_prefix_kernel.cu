@@ -544,7 +544,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             m = mn;
             l *= f;
             if (i > 0) {
-              if (!(ok = wait(&bars.pv_done, (uint32_t)(t - 1) & 1))) break;
+              // (a product that the slowest warp's weights hold up: it may be taking rows again)
+              if (!(ok = idle(&bars.pv_done, (uint32_t)(t - 1) & 1))) break;
               fence_after();
 #pragma unroll 1
               for (int u = 0; u < 8; ++u) {

@@ -3,8 +3,9 @@ import pytest
 import torch
 
 import query_aware_kv_gb300 as q
-from test_gpu_prefix import make, queries
-from test_gpu_window import ok
+import span_reference as R
+from test_gpu_prefix import BIG, INF, make, queries
+from test_gpu_window import logical, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,43 @@ def test_a_sequence_does_not_depend_on_the_batch_beside_it(geom):
         for _ in range(8):
             out, lse = plan.decode(other)
             assert torch.equal(out[alone], want[0]) and torch.equal(lse[alone], want[1]), scale
+
+
+def close_to_64_bits(cache, qq, out, lse, rows, skip=()):
+    """The sequences `rows`; dims `skip` are not looked at."""
+    n, hq = qq.shape[1:3]
+    G = hq // cache.num_kv_heads
+    dims = [d for d in range(128) if d not in skip]
+    for b in rows:
+        L = int(cache.seq_lens[b])
+        allowed = R.window_mask(L, n, 0, BIG, "cuda")
+        for h in range(hq):
+            k, v = logical(cache, b, h // G, "k_pool"), logical(cache, b, h // G, "v_pool")
+            ref = R.attend(qq[b, :, h], k, torch.where(torch.isinf(v), 0.0, v), allowed)
+            ref = (ref[0][:, dims], ref[1], ref[2][:, dims], ref[3])
+            R.assert_close(out[b, :, h][:, dims], lse[b, :, h], ref, True, f"{b} {h}")
+
+
+def test_a_short_limit_is_no_limit_on_the_product_that_other_warps_hold_up():
+    """All rows of a job are taken again by the warps of one half, while the other half's are at the
+    next job, whose maxima move at its second tile: their wait for the product of its first tile is a
+    wait for the warps that are late.  (A sequence's 16 tokens of 8 heads are a job's 128 rows, and
+    there are two jobs a CTA.)"""
+    tokens, n = 8192, 16
+    cache, groups = make([(tokens, [tokens + 40] * 304)], 8, 1, 32)
+    for page in range(tokens // 32):  # (scores of the second tile: 14 in 2^x where the first had 1)
+        cache.k_pool[int(cache.block_table[0, page])] *= 0.25 if page < 4 else 4.0
+    at = int(cache.block_table[0, 3])
+    cache.v_pool[at, :, 5, 9] = INF
+    qq = torch.randn((304, n, 8, 128), device="cuda").half()
+    long = q.opts(pages_per_split=16384)
+    ws = q.prefix_workspace(cache, groups, long, n)
+    want, want_lse = q.prefix_decode(cache, qq, groups, ws, long)
+    ok(ws)
+    short = q.opts(pages_per_split=16384, wait_limit_ns=300_000)
+    for _ in range(3):
+        out, lse = q.prefix_decode(cache, qq, groups, ws, short)
+        ok(ws)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert bool((want[..., 9] == INF).all())
+    close_to_64_bits(cache, qq, want, want_lse, (0, 151, 303), skip=(9,))
