@@ -84,6 +84,7 @@ struct Bars {
   Job job[2];
   uint32_t tmem;
   int give_up;
+  unsigned moves;             // pages that warps have been through, taking rows again
   int fetched[2], q_fetched;  // K and V tiles, and queries, whose copies have been issued
 };
 
@@ -144,20 +145,26 @@ __device__ __forceinline__ Cut cut_of(const PrefixTable& t, int n, int lg, int c
   return x;
 }
 
-// A wait for the next job, or for what other warps do with this one, which may be a whole job long
-// (or a row that is taken again): its limit is a second at least, however short the waits for copies
-// and products may be (one of those that runs out ends this one too).
+// A wait for the next job, or for what other warps do with this one, which may be a whole job long:
+// its limit is a second at least, however short the waits for copies and products may be (one of
+// those that runs out ends this one too).  While a warp takes rows of a job again (32 rows of 512K
+// tokens take it 1.4 s) the limit starts anew with every page that it is through.
 __device__ __forceinline__ bool idle_wait(const Params& p, uint64_t* bar, uint32_t parity,
-                                          volatile int* give_up) {
+                                          volatile int* give_up, const volatile unsigned* moves) {
   if (mbar_try_wait(bar, parity)) return true;
   long long t0 = 0;
+  unsigned seen = 0;
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 1024; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*give_up) return false;
     const long long now = global_ns();
-    if (t0 == 0) t0 = now;
+    const unsigned at = *moves;
+    if (t0 == 0 || at != seen) {
+      t0 = now;
+      seen = at;
+    }
     if (now - t0 > max(p.wait_limit_ns, kDefaultWaitNs)) {
       *give_up = 1;
       record_at<kSitePrefix>(p, QUEST_ERR_TIMEOUT, -1, -1);
@@ -210,6 +217,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&bars.pair[i], 2);
     mbar_init(&bars.drain, 1);
     bars.give_up = bars.fetched[0] = bars.fetched[1] = bars.q_fetched = 0;
+    bars.moves = 0u;
     fence_mbar_init();
   }
   if (warp == 10) tmem_alloc(&bars.tmem);
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     return __all_sync(0xffffffffu, wait_at<kSitePrefix>(p, bar, parity, give_up)) != 0;
   };
   auto idle = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, idle_wait(p, bar, parity, give_up)) != 0;
+    return __all_sync(0xffffffffu, idle_wait(p, bar, parity, give_up, &bars.moves)) != 0;
   };
   auto length = [&](int seq) {
     const int L = p.seq_lens[seq];
@@ -651,6 +659,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int page = job.page0; page * P < last; ++page) {
+          if (lane == 0) atomicAdd(&bars.moves, 1u);
           const int phys = p.block_table[(size_t)job.seq * p.max_pages + page];
           if (phys < 0 || phys >= p.num_phys) continue;
           const size_t at = ((size_t)phys * p.Hkv + job.g) * P * kHeadDim + 4 * lane;

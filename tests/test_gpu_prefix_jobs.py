@@ -106,3 +106,30 @@ def test_a_short_limit_is_no_limit_on_the_product_that_other_warps_hold_up():
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert bool((want[..., 9] == INF).all())
     close_to_64_bits(cache, qq, want, want_lse, (0, 151, 303), skip=(9,))
+
+
+def test_the_longest_job_may_be_taken_again():
+    """Rows of 512K tokens in one job each, two jobs a CTA.  An infinite value of the first sequences
+    makes their 32 rows be taken again, a token at a time and for longer than a second: what waits for
+    them waits as long as they move on."""
+    B, n, P, pages = 304, 4, 32, 16384
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((pages + 4, 1, P, 128), generator=g, device="cuda", dtype=torch.float16) for _ in "kv")
+    bt = torch.arange(pages, device="cuda", dtype=torch.int32).repeat(B, 1)
+    for b in range(4):  # (a page of their own; the others hold the same ones without being a group)
+        bt[b, 7] = pages + b
+    lens = torch.full((B,), pages * P, dtype=torch.int32, device="cuda")
+    cache = q.PagedCache.allocate_meta(k, v, bt, lens, 8)
+    v[pages:, :, 5, 9] = INF
+    qq = torch.randn((B, n, 8, 128), device="cuda", generator=g, dtype=torch.float16)
+    groups = [(B, 0)]
+    o = q.opts(pages_per_split=pages)
+    ws = q.prefix_workspace(cache, groups, o, n)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    out, lse = q.prefix_decode(cache, qq, groups, ws, o)
+    end.record()
+    ok(ws)
+    assert start.elapsed_time(end) > 1000  # (or the test shows nothing)
+    assert bool((out[:4, ..., 9] == INF).all()) and bool(torch.isfinite(out[4:]).all())
+    close_to_64_bits(cache, qq, out, lse, (0, 4), skip=(9,))
