@@ -226,6 +226,14 @@ size_t span_max_parts(int batch, int hkv, bool user);
 // Whether the launch of a narrow chain step takes the selection itself (p.chain_select).
 bool span_selects(const SpanParams& sp, int pages);
 cudaError_t launch_span(const SpanParams& sp, bool narrow, int pages, cudaStream_t s);
+// How that launch would split its rows: CTAs a row, whether they are a cluster, and how many CTAs the
+// GPU holds at once.
+struct SpanChoice {
+  int splits;
+  bool cluster;
+  int slots;
+};
+SpanChoice span_choice(const SpanParams& sp, bool narrow, int pages);
 
 // ---- prefixes that sequences share
 constexpr int kPrefixRows = 128;    // query rows (sequence, head) of a work item of the prefixes

@@ -177,11 +177,25 @@ int check_query_tokens(const quest_cache_t& c, int n) {
 // 17.8, 4 of 32 MHA heads behind 1024 tokens 14.3 and 16.4; 32 of 32 / 8 heads behind 512 tokens 15.8
 // and 13.4, 4 behind 2048 12.3 and 11.3, 2 behind 8192 17.4 and 14.4.
 constexpr int kShareTokens = 1536, kShareTokensInAll = 12288;
-// Each for itself, 16 to 32 rows are split so that 128 CTAs have a part of eight pages or more, joined
-// by the rows' last CTAs: the span decode's own choice, clusters on most of the GPU, takes longer (32
-// rows of 612 tokens 8.5 us in four parts, 11.3 in clusters of four; 16 of 2248 tokens 10.4 in eight
-// and 15.8), fewer rows find room for their clusters (4 of 2148 tokens: 9.3, and 11.3 in 32 parts).
-constexpr int kSomeRows = 16, kSomeRowsMost = 32, kSomeRowsCtas = 128;
+// Each for itself, rows are split as the span decode splits them, but for two of its choices, which get
+// one wave of plain parts instead.  Clusters on more than 120 SMs (16 rows of eight): their last waits
+// for the first (16 rows of 612 tokens 11.7 us, 8.2 in nine parts; of 2248 16.6 and 10.9, of 8000 28.2
+// and 17.8).  And a second wave of CTAs, which it takes where the first leaves many SMs empty (22, 26,
+// 32, 33, 41 rows, ...), for parts of less than 64 blocks of 16 tokens.  In two waves and in one: 32
+// rows of 612 tokens 13.6 and 9.7 us, of up to 8000 26.0 and 25.5, of up to 16000 38.9 and 41.3, of up
+// to 64000 116 and 140 (lengths from a quarter of that on; all as long: 15.9 and 11.3 at 1200, 49.6 and
+// 45.3 at 16000); 60 rows of up to 2248 20.9 and 17.6, of 8000 36.1 and 38.7; 96 rows of up to 1200
+// 19.4 and 14.5, of 4000 31.2 and 34.8; 192 rows of up to 1200 24.1 and 22.0, of 2248 32.4 and 36.4 (all
+// as long: 44.5 and 41.0).
+constexpr int kClusterCtas = 120, kWaveBlocks = 64;
+int one_wave_split(const SpanParams& sp, int pages) {
+  const SpanChoice own = span_choice(sp, false, pages);
+  const long long rows = (long long)sp.p.B * sp.p.Hkv, ctas = rows * own.splits;
+  const bool late = ctas > own.slots && pages * (sp.p.P / 16) < kWaveBlocks * own.splits;
+  if (own.splits == 1 || !(late || (own.cluster && ctas > kClusterCtas))) return 0;
+  const int parts = (int)std::max(1LL, own.slots / rows);
+  return (pages + parts - 1) / parts;
+}
 constexpr int kPrefixJobs = 96;  // of the prefixes, in one go: five eighths of the SMs, the others
                                  // begin with tails (152: 45.2 us for 40.0 at 32 tails of 512 tokens
                                  // behind 32K, 42.2 for 34.7 at tails of 16)
@@ -496,14 +510,10 @@ int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tok
   if ((rc = check_workspace(ws, ws_bytes, L.total))) return rc;
   sp.p = make_params(*cache, ws, L, opts);
   if (t.ctas == 0 && n_tokens == 1) {  // nothing is shared: every sequence on its own
-    const int rows = cache->batch * cache->num_kv_heads;
-    quest_opts_t some{};
-    if (!user_split(opts) && rows >= kSomeRows && rows <= kSomeRowsMost) {
-      const int pieces = std::max(1, std::min(kSomeRowsCtas / rows, cache->max_pages / 8));
-      some.pages_per_split = (cache->max_pages + pieces - 1) / pieces;
-      opts = &some;
-    }
     sp.mode = kSpanDense;
+    quest_opts_t some{};
+    if (!user_split(opts) && (some.pages_per_split = one_wave_split(sp, cache->max_pages)) > 0)
+      opts = &some;
     return run_span(sp, false, cache->max_pages, opts, q, out, lse, stream, "quest_prefix_decode");
   }
   sp.p.q = static_cast<const __half*>(q);

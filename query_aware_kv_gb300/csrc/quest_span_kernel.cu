@@ -858,6 +858,12 @@ static SpanSplits span_splits(const SpanParams& sp, const SpanShape& shape, int 
   return {n, false};
 }
 
+SpanChoice span_choice(const SpanParams& sp, bool narrow, int pages) {
+  const SpanShape shape = span_shape(narrow, (long long)sp.p.B * sp.p.Hkv);
+  const SpanSplits splits = span_splits(sp, shape, pages);
+  return {splits.n, splits.cluster, kSms * shape.ctas};
+}
+
 size_t span_max_parts(int batch, int hkv, bool user) {
   const long long rows = (long long)batch * hkv;
   if (rows > kSplitRows) return 0;

@@ -133,3 +133,22 @@ def test_the_longest_job_may_be_taken_again():
     assert start.elapsed_time(end) > 1000  # (or the test shows nothing)
     assert bool((out[:4, ..., 9] == INF).all()) and bool(torch.isfinite(out[4:]).all())
     close_to_64_bits(cache, qq, out, lse, (0, 4), skip=(9,))
+
+
+@pytest.mark.parametrize("batch,hkv,tokens", [(4, 8, 20000), (24, 1, 700), (11, 2, 30000), (15, 4, 9000), (28, 1, 3000)])
+def test_unshared_rows_are_split_as_a_window_decodes_are(batch, hkv, tokens):
+    """Nothing shared: long rows, and any number of rows whose CTAs fit the GPU at once, take the split
+    that the span decode chooses for a window over everything, and so its bits."""
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    lens = [tokens - (3 * tokens * b) // (4 * batch) for b in range(batch)]
+    mp = -(-tokens // 16) + 1
+    k, v = (torch.randn((batch * mp, hkv, 16, 128), generator=g, device="cuda", dtype=torch.float16) for _ in "kv")
+    bt = torch.randperm(batch * mp, generator=g, device="cuda").view(batch, mp).int()
+    cache = q.PagedCache.allocate_meta(k, v, bt, torch.tensor(lens, dtype=torch.int32).cuda(), 4 * hkv)
+    qq = torch.randn((batch, 4 * hkv, 128), generator=g, device="cuda", dtype=torch.float16)
+    groups = [(batch, 0)]
+    ws, wws = q.prefix_workspace(cache, groups), q.window_workspace(cache)
+    out, lse = q.prefix_decode(cache, qq, groups, ws)
+    want, want_lse = q.window_decode(cache, qq, 0, BIG, wws)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    ok(ws), ok(wws)
