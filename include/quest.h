@@ -556,8 +556,8 @@ int quest_rotate(const quest_rope_t* rope, const void* x, int64_t x_stride,
 /* A chunk of n_tokens tokens per sequence on its way into a cache: q [batch][n_tokens]
  * [num_q_heads][128], k and v [batch][n_tokens][num_kv_heads][128], QUEST_FP16 or QUEST_BF16.
  * A token's heads are side by side; sequences and tokens are stride[0] and stride[1] elements
- * apart (multiples of 8; stride[0] is not used with one sequence, stride[1] not with one
- * token), so that q, k and v may be parts of one projection's rows. */
+ * apart, so that q, k and v may be parts of one projection's rows.  Strides are multiples of 8,
+ * also those that move nothing (stride[0] with one sequence, stride[1] with one token). */
 typedef struct quest_rotary_io {
     const void* q;       /* or NULL: no queries */
     const void* k;
@@ -577,8 +577,8 @@ typedef struct quest_rotary_io {
  * values and turned queries are rounded once to fp16 (of a bf16 number beyond fp16's range an
  * infinity is left); the boxes are those of the keys as stored.  Of fp16 inputs the same cache
  * and queries, bit for bit, as quest_rotate followed by quest_prefill.  A sequence with no room,
- * or with a touched page outside [0, num_phys), is reported and its length left unchanged.  One
- * launch with n_tokens = 1, otherwise two. */
+ * or with a touched page outside [0, num_phys), is reported and its length left unchanged; its
+ * q_out is not to be used.  One launch with n_tokens = 1, otherwise two. */
 int quest_prefill_rotary(const quest_cache_t* cache, const quest_rope_t* rope,
                          const quest_rotary_io_t* io, void* ws, size_t ws_bytes,
                          quest_stream_t stream);
@@ -620,10 +620,14 @@ size_t quest_prefix_workspace_size(const quest_cache_t* cache, const quest_prefi
  * (QUEST_ERR_UNSUPPORTED).  groups: HOST array, copied by the call.  A row that sees no token (an
  * empty sequence, a negative position) gives out = 0, lse = -inf; NaN and infinities as in windowed
  * attention.  Where sharing would not pay (prefixes of a few hundred tokens) every sequence reads
- * all of its tokens itself.  A call may be captured into a graph; the sequences may grow between
- * calls.
+ * all of its tokens itself.  Where a prefix is shared, or n_tokens > 1, every weight enters its
+ * product with the values as one fp16 number (off by 2^-11 of itself at most, as in
+ * quest_window_prefill); otherwise with 22 bits, as in quest_window_decode.  Sums are fp32, and a
+ * call gives the same bits every time.  A call may be captured into a graph; the sequences may grow
+ * between calls.
  * opts: pages_per_split (given, every group shares its prefix), wait_limit_ns (of the waits for
- * copies and products; others wait a second at least), debug_flags. */
+ * copies and products; waits for other warps' work are a second at least, from the last sign of
+ * that work on), debug_flags. */
 int quest_prefix_decode(const quest_cache_t* cache, const void* q, int32_t n_tokens,
                         const quest_prefix_group_t* groups, int32_t n_groups, void* out,
                         float* lse, void* ws, size_t ws_bytes, const quest_opts_t* opts,

@@ -860,7 +860,8 @@ def rotate(rope, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.T
            transposed: bool = False, stream=None) -> torch.Tensor:
     """Heads x [..., heads, 128] (fp16, bf16 or fp32) turned by their tokens' positions (int32, of
     x's leading dims).  ``transposed``: turned the other way, by the same magnitude: with a gradient
-    of the output as x, the gradient of the input.  ``out`` may be x."""
+    of the output as x, the gradient of the input (autograd records none of these calls).  ``out``
+    may be x."""
     shape = x.shape
     dtype = _DTYPES.get(x.dtype)
     if dtype is None:
@@ -954,7 +955,8 @@ def prefill_rotary(cache: PagedCache, rope, q: Optional[torch.Tensor], k: torch.
     """``prefill`` of a chunk as the projection leaves it: keys are turned by their positions
     (seq_lens[b] + i, plus offsets[b]) on the way into the pages, the turned queries are returned
     (fp16 [B][n][Hq][128]).  q [B][n][Hq][128] (or None), k, v [B][n][Hkv][128]: fp16 or bf16, their
-    tokens any multiple of 8 elements apart."""
+    tokens any multiple of 8 elements apart.  A ``NarrowCache`` is written as by
+    ``narrow_prefill_rotary``."""
     if k.dim() != 4:
         raise ValueError("k must be [batch][n_tokens][num_kv_heads][128]")
     return _rotary_write(cache, rope, q, k, v, ws, q_out, offsets, stream)
@@ -1135,7 +1137,8 @@ def prefix_decode(cache: PagedCache, q: torch.Tensor, groups: Sequence[Tuple[int
     sequences begin with the same tokens: ``groups`` holds (sequences, tokens of their common
     prefix) of the batch's sequences in order.  A prefix's whole pages are read once for its
     group.  q [B][Hq][128], or [B][n][Hq][128] for the last n tokens of every sequence (n Hq / Hkv
-    at most 128), which see what comes before them."""
+    at most 128), which see what comes before them.  Where something is shared, or n is above 1, weights
+    are fp16 numbers in their product with the values (2^-11), as in ``window_prefill``."""
     n = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else None
     return PrefixPlan(cache, groups, ws, o, out, lse, want_lse, stream, n).decode(q)
 

@@ -77,7 +77,8 @@ __device__ __forceinline__ void cos_sin(const quest_rope_t& rope, int i, long lo
   const float r = (float)rest * 0x1p-31f, r_low = (float)(rest - (int)(float)rest) * 0x1p-31f;
   const float u = r * r, u_low = fmaf(2.f * r, r_low, fmaf(r, r, -u));
   // sin(pi r) = r (pi + u A(u)) and cos(pi r) = 1 + u (B0 + u B(u)): A and B0 + u B interpolated at
-  // the Chebyshev nodes of [0, 1/16], within 1e-11 and 2e-10; pi and B0 in two parts.  (sincospif,
+  // the Chebyshev nodes of [0, 1/16]; pi and B0 in two parts, the other coefficients in fp32, with
+  // which the sine is within 1.4e-9 and the cosine within 2.2e-10.  (sincospif,
   // which reduces its argument once more, made a block's table its longest part.)
   constexpr float kPi = 0x1.921fb6p+1f, kPiLow = -0x1.777a5cp-24f;
   constexpr float kB0 = -0x1.3bd3ccp+2f, kB0Low = -0x1.313d3p-23f;
