@@ -153,7 +153,7 @@ __device__ __forceinline__ Cut cut_of(const PrefixTable& t, int n, int lg, int c
 // A wait for the next job, or for what other warps do with this one, which may be a whole job long:
 // its limit is a second at least, however short the waits for copies and products may be (one of
 // those that runs out ends this one too).  While a warp takes rows of a job again (32 rows of 512K
-// tokens take it 1.4 s) the limit starts anew with every page that it is through.
+// tokens take it 3 s) the limit starts anew with every page that it is through.
 __device__ __forceinline__ bool idle_wait(const Params& p, uint64_t* bar, uint32_t parity,
                                           volatile int* give_up, const volatile unsigned* moves) {
   if (mbar_try_wait(bar, parity)) return true;

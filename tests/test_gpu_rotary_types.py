@@ -116,3 +116,53 @@ def test_a_turn_that_leaves_fp16s_range():
         at = c.block_table[0, 0].long()
         assert float(got[0, 0, 0, 0]) == INF and float(c.k_pool[at, 0, 1, 0]) == INF
         assert float(c.v_pool[at, 0, 1, 0]) == float(h[0, 0, 0, 0].half())
+
+
+def test_strides_past_31_bits():
+    """Tokens and sequences 2.3 G elements apart."""
+    g, r, far = gen(5), q.Rope(), 2_300_000_000 // 8 * 8
+    base = torch.empty(far + 4096, dtype=torch.float16, device="cuda")
+    x = torch.as_strided(base, (2, 3, D), (far, D, 1))
+    x.copy_(normal(g, 2, 3, D))
+    pos = torch.tensor([5, 70000], dtype=torch.int32, device="cuda")
+    want = q.rotate(r, x.contiguous(), pos)
+    assert torch.equal(q.rotate(r, x, pos), want)
+    for narrow in (False, True):
+        for n in (1, 2):
+            shape, step = (2, n, 3, D), (far, 3 * D, D, 1)
+            k = torch.as_strided(base, shape, step)
+            k.copy_(normal(g, *shape))
+            c, ws = paged(g, 2, 3, 3, 16, [3, 15], 4, narrow)
+            a, b = copy_of(c), copy_of(c)
+            call = q.narrow_prefill_rotary if narrow else q.prefill_rotary
+            assert torch.equal(call(a, r, k, k, k, ws), call(b, r, *[k.contiguous()] * 3, ws))
+            same(a, b)
+    x.copy_(normal(g, 2, 3, D))
+    want = q.rotate(r, x.contiguous(), pos)
+    assert q.rotate(r, x, pos, out=x) is x and torch.equal(x, want)
+
+
+def test_writes_on_two_streams_at_once():
+    """Caches of their own, each written by its stream, beside turns on both."""
+    g, r = gen(6), q.Rope(96)
+    made = [paged(g, 3, 8, 2, 16, [0, 9, 30], 40, narrow) for narrow in (False, True)]
+    rows = [[normal(g, 3, n, 12, D) for n in (100, 1, 37, 1, 200)] for _ in made]
+    calls = q.prefill_rotary, q.narrow_prefill_rotary
+    want = []
+    for (c, ws), xs, call in zip(made, rows, calls):
+        a = copy_of(c)
+        want.append((a, [call(a, r, *parts(x, 8, 2), ws) for x in xs]))
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [(copy_of(c), []) for c, _ in made]
+        outs = [[torch.empty_like(t) for t in w[1]] for w in want]
+        torch.cuda.synchronize()
+        for i in range(5):
+            for (c, _), xs, call, s, o, (_, ws) in zip(got, rows, calls, streams, outs, made):
+                call(c, r, *parts(xs[i], 8, 2), ws, q_out=o[i], stream=s)
+        torch.cuda.synchronize()
+        for (a, t), (b, _), o in zip(want, got, outs):
+            same(a, b)
+            assert all(torch.equal(x, y) for x, y in zip(t, o))
+    assert all(q.read_status(ws)[0] == 0 for _, ws in made)
