@@ -13,8 +13,8 @@
 // type.
 //
 // Bound by DRAM: a value costs its read and its write, and 3 flops.  Measured: 8192 tokens of 40
-// fp16 heads out of rows of 48 in 28 us (168 MB, 6.0 TB/s), 1999 tokens of 24 bf16 heads in 4.9 (25
-// MB), 4 tokens in 2.9, which is the launch and two round trips.  A half-warp takes a row of
+// fp16 heads out of rows of 48 in 27 us (168 MB, 6.3 TB/s), 1999 tokens of 24 bf16 heads in 4.2 (25
+// MB), 4 tokens in 2.2, which is the launch and two round trips (calls of a graph, one after another).  A half-warp takes a row of
 // 128 dims, lane c two pieces of 4 dims whose four pairs are whole within the lane for either
 // layout (rotary_dim is a multiple of 8), so nothing is exchanged between lanes.
 #include <cuda_bf16.h>
